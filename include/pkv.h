@@ -347,6 +347,186 @@ PKV_API pkv_status pkv_attention_static_workspace(const pkv_tensor* q, const pkv
                                                   int32_t max_q_len, pkv_tensor* out, void* stream);
 
 /*
+ * A speculative decoding step.  The rows of a sequence in a step may be a
+ * tree of drafted tokens instead of a chain: node i of sequence s is packed
+ * row cu_seqlens_q[s] + i, its K/V row sits at cache position N_s - q_s + i
+ * like any new row, and it attends to the whole context (positions
+ * 0 .. N_s - q_s - 1) and to the drafted nodes its mask names.  One step is
+ *
+ *   pkv_tree_mask        parents -> mask and rotary positions
+ *   pkv_slot_mapping     cache slots of the nodes (as for a chain)
+ *   per layer:
+ *     pkv_rope_append    rotate q and k, write k and v into the cache
+ *     pkv_tree_attention the nodes' attention over the cache
+ *   pkv_tree_commit      per layer, once a path is accepted: its rows move
+ *                        to the front of the drafted rows
+ */
+
+/*
+ * pkv_rope_init -- the angles of a rotary position embedding, computed once
+ * on the host (no device access) and kept by the caller.
+ *
+ * Pair i of the first rot_dim elements of a head turns by
+ * position * f_i, f_i = base^(-2 i / rot_dim).  Elements past rot_dim pass
+ * through.  interleaved != 0: pair i is elements 2i, 2i + 1; else elements
+ * i, i + rot_dim / 2.  scaling stretches the angles for contexts longer than
+ * the trained original_max_position L by factor:
+ *   PKV_ROPE_PLAIN     f_i
+ *   PKV_ROPE_LINEAR    f_i / factor
+ *   PKV_ROPE_NTK       f_i of base * factor^(rot_dim / (rot_dim - 2))
+ *   PKV_ROPE_BY_PARTS  f_i (1 - r_i) + f_i / factor r_i, r_i rising from 0 to
+ *                      1 over the pair indices between those that make fast
+ *                      and slow turns (0: 32 and 1) over L positions, their
+ *                      bounds rounded outwards; cos and sin are multiplied by
+ *                      attention_factor (0: 0.1 ln(factor) + 1)
+ *   PKV_ROPE_SMOOTH    f_i w_i + f_i / factor (1 - w_i), w_i rising from 0 to
+ *                      1 as the turns L f_i / (2 pi) go from slow to fast
+ *                      (0: 1 and 4)
+ * attention_factor applies to every scaling (0: 1 except where noted).
+ * rot_dim: even, 2 .. 256; base > 1; factor > 0; L > 0 for the last two.
+ */
+typedef enum {
+  PKV_ROPE_PLAIN = 0,
+  PKV_ROPE_LINEAR = 1,
+  PKV_ROPE_NTK = 2,
+  PKV_ROPE_BY_PARTS = 3,
+  PKV_ROPE_SMOOTH = 4
+} pkv_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t scaling; /* pkv_rope_scaling */
+  int32_t reserved;
+  double base;
+  double factor;
+  double original_max_position;
+  double fast, slow;
+  double attention_factor;
+} pkv_rope_params;
+
+#define PKV_ROPE_MAX_PAIRS 128
+typedef struct {
+  uint64_t turns[PKV_ROPE_MAX_PAIRS]; /* f_i / (2 pi) mod 1, in units of 2^-64 turn */
+  float amplitude;                    /* factor on cos and sin */
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t ready; /* set by pkv_rope_init */
+} pkv_rope;
+
+PKV_API pkv_status pkv_rope_init(const pkv_rope_params* params, pkv_rope* rope);
+
+/*
+ * pkv_rope_append -- pkv_append with the rotary embedding of q and k in the
+ * same pass: reads q, k and v once, writes the rotated q and scatters the
+ * rotated k and v into their slots.
+ *
+ *   q, q_out      [T, Hq, D], same dtype; unit stride in D, 16-byte aligned
+ *                 rows; q_out may be q itself, but must not overlap it
+ *                 otherwise
+ *   k, v          [T, Hkv, D], q's dtype, as in pkv_append
+ *   positions     [T] int32 or int64 (device), any value
+ *   slot_mapping, k_cache, v_cache, k_scale, v_scale: as in pkv_append; a
+ *                 row with a negative slot is rotated into q_out and not
+ *                 written to the cache
+ *
+ * Angles are exact for every position: position * turns is taken modulo one
+ * turn in 64-bit integers.  The rotation is computed in fp32 and rounded
+ * once, to q's type and to the cache's type (an e4m3 code is that of
+ * (rotated k) * (1.0f / k_scale), not of a bf16 intermediate).
+ * Supported: pkv_append's dtypes; D a multiple of 8 up to 256, rot_dim <= D.
+ */
+PKV_API pkv_status pkv_rope_append(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* v,
+                                   const pkv_tensor* positions, const pkv_tensor* slot_mapping,
+                                   const pkv_rope* rope, pkv_tensor* q_out, pkv_tensor* k_cache,
+                                   pkv_tensor* v_cache, float k_scale, float v_scale, void* stream);
+
+/*
+ * pkv_tree_mask -- masks and positions of drafted trees from parent links.
+ *
+ *   parents       [T] int32: the parent of node i of its sequence, as a node
+ *                 index 0 .. i - 1, or -1 for a child of the last context token
+ *   cu_seqlens_q  [B+1] int32, seq_lens [B] int32 (N_s, drafted rows included)
+ *   tree_mask     [T, W] int32 (written), unit column stride: bit j % 32 of
+ *                 word j / 32 of row i is set when node i sees node j: itself
+ *                 and its ancestors
+ *   positions     [T] int32 (written): N_s - q_s + the node's depth (0 for a
+ *                 child of the context)
+ *
+ * A parent outside -1 .. i - 1 is recorded (bit 4) and taken as -1.  Rows of
+ * a sequence with inconsistent lengths or more than 32 W nodes are recorded
+ * (bit 4) and get an empty mask and position 0.  Rows at or beyond
+ * cu_seqlens_q[B] are left as they are.
+ */
+PKV_API pkv_status pkv_tree_mask(const pkv_tensor* parents, const pkv_tensor* cu_seqlens_q,
+                                 const pkv_tensor* seq_lens, pkv_tensor* tree_mask, pkv_tensor* positions,
+                                 void* stream);
+
+/*
+ * pkv_tree_attention -- attention of drafted trees over the paged cache.
+ *
+ * Node i of sequence s attends to keys 0 .. N_s - q_s - 1 and to key
+ * N_s - q_s + j for every bit j < q_s set in row cu_seqlens_q[s] + i of
+ * tree_mask (any mask: bits need not come from a tree, and a node sees itself
+ * only if its own bit is set).  A node that sees no key gets zeros.  Arguments
+ * as pkv_attention, and
+ *
+ *   tree_mask     [T, W] int32, unit column stride; W >= 1, and
+ *                 32 W >= max_q_len where that is given
+ *   max_q_len     a host-side upper bound on q_s (<= 0: unknown)
+ *   workspace     pkv_tree_attention_workspace_size() bytes, 256-byte aligned;
+ *                 scratch of one call: nothing in it is kept between calls
+ *
+ * A sequence with more than max_q_len (where given) or 32 W nodes, q_s < 0,
+ * q_s > N_s or N_s beyond its table is recorded (bit 4) and its rows are left
+ * as they are; so are rows at or beyond cu_seqlens_q[B].  A key whose block id
+ * is out of range is recorded (bit 2) and adds nothing.  Values of keys that a
+ * row does not see never reach it, infinities and NaN included.  Within a
+ * call a row's result depends on its own sequence only (lengths, pages'
+ * contents, queries, masks), not on block size, placement, max_q_len or the
+ * other sequences.
+ *
+ * Supported: bf16 q with bf16 or e4m3 caches at D = 64 and 128, f32 q with
+ * f32 caches at D a multiple of 32 up to 256; any block size, any Hq / Hkv,
+ * any q_s; num_blocks * block_size * Hkv within int32.
+ */
+PKV_API pkv_status pkv_tree_attention_workspace_size(const pkv_tensor* q, const pkv_tensor* block_tables,
+                                                     const pkv_tensor* k_cache, int32_t max_q_len, size_t* bytes);
+
+PKV_API pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_q,
+                                      const pkv_tensor* seq_lens, const pkv_tensor* block_tables,
+                                      const pkv_tensor* k_cache, const pkv_tensor* v_cache,
+                                      const pkv_tensor* tree_mask, float scale, float k_scale, float v_scale,
+                                      int32_t max_q_len, pkv_tensor* out, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * pkv_tree_commit -- keeps the accepted path of each drafted tree: the cache
+ * rows of its nodes move, in place, to the front of the drafted rows, and
+ * the sequence's length becomes context + path.
+ *
+ *   accepted       [B, A] int32, unit column stride: node indices of the
+ *                  path in ascending order; entries past the path are not read
+ *   accepted_lens  [B] int32: L_s, 0 .. min(A, q_s)
+ *   cu_seqlens_q, seq_lens, block_tables: those of the step
+ *   k_cache,
+ *   v_cache        any cache dtype (f32, bf16, e4m3); one layer
+ *   new_seq_lens   [B] int32 (written) or NULL: N_s - q_s + L_s; must not
+ *                  overlap seq_lens (every layer's call reads the step's)
+ *
+ * The row at position N_s - q_s + accepted[s][i] moves to N_s - q_s + i, bit
+ * for bit; other rows stay as they are.  A sequence whose lengths, path or
+ * block ids are inconsistent (a path that does not ascend or leaves
+ * 0 .. q_s - 1) is recorded (bit 4, block ids bit 2), keeps all its rows and
+ * gets new length N_s.  Sequences of one call must not share the blocks that
+ * hold their drafted rows.  Supported: D a multiple of 8.
+ */
+PKV_API pkv_status pkv_tree_commit(const pkv_tensor* accepted, const pkv_tensor* accepted_lens,
+                                   const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens,
+                                   const pkv_tensor* block_tables, pkv_tensor* k_cache, pkv_tensor* v_cache,
+                                   pkv_tensor* new_seq_lens, void* stream);
+
+/*
  * pkv_device_errors -- synchronise the stream, then return (in *flags) and
  * clear the record of out-of-range indices the kernels met on the current
  * device since the last call.  Bits: 1 = slot beyond the pool, 2 = block id

@@ -19,6 +19,16 @@ Functions (same names as the C ABI):
   pkv_attention_static_workspace(q, cu_seqlens_q, seq_lens, block_tables, k_cache,
                                  v_cache, scale, out, k_scale=1.0, v_scale=1.0, max_q_len=0)
   pkv_device_errors()
+and, from .speculative (a speculative decoding step):
+  pkv_rope_init(rot_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, ...)
+  pkv_rope_append(q, k, v, positions, slot_mapping, rope, k_cache, v_cache, q_out=None,
+                  k_scale=1.0, v_scale=1.0)
+  pkv_tree_mask(parents, cu_seqlens_q, seq_lens, max_q_len, tree_mask=None, positions=None)
+  pkv_tree_attention_workspace_size(q, block_tables, k_cache, max_q_len=0)
+  pkv_tree_attention(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, tree_mask,
+                     scale, out, k_scale=1.0, v_scale=1.0, max_q_len=0, workspace=None)
+  pkv_tree_commit(accepted, accepted_lens, cu_seqlens_q, seq_lens, block_tables,
+                  k_cache, v_cache, new_seq_lens=None)
 """
 import ctypes
 import os
@@ -26,7 +36,9 @@ import os
 import torch
 
 __all__ = ["PkvError", "pkv_slot_mapping", "pkv_csr_to_block_tables", "pkv_append", "pkv_attention", "pkv_attention_workspace_size",
-           "pkv_attention_plan", "pkv_attention_run", "pkv_attention_static_workspace", "pkv_device_errors", "pkv_version", "library_path", "load_library",
+           "pkv_attention_plan", "pkv_attention_run", "pkv_attention_static_workspace", "pkv_device_errors",
+           "pkv_rope_init", "pkv_rope_append", "pkv_tree_mask", "pkv_tree_attention_workspace_size", "pkv_tree_attention",
+           "pkv_tree_commit", "pkv_version", "library_path", "load_library",
            "EXPORTED", "STATIC_WORKSPACE_BYTES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,7 +47,9 @@ EXPORTED = ("pkv_slot_mapping", "pkv_append", "pkv_attention_workspace_size", "p
             "pkv_attention_plan", "pkv_attention_run",
             "pkv_attention_static_workspace", "pkv_device_errors", "pkv_status_string", "pkv_last_error",
             "pkv_version", "pkv_csr_to_block_tables", "pkv_bm_create", "pkv_bm_destroy", "pkv_bm_add_sequence", "pkv_bm_append",
-            "pkv_bm_free_sequence", "pkv_bm_block_table", "pkv_bm_build_step", "pkv_bm_stats")
+            "pkv_bm_free_sequence", "pkv_bm_block_table", "pkv_bm_build_step", "pkv_bm_stats",
+            "pkv_rope_init", "pkv_rope_append", "pkv_tree_mask", "pkv_tree_attention_workspace_size",
+            "pkv_tree_attention", "pkv_tree_commit")
 # PKV_STATIC_WORKSPACE_BYTES of include/pkv.h
 STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -271,3 +285,7 @@ def pkv_device_errors(device=None) -> int:
     flags = ctypes.c_uint32(0)
     _check(lib.pkv_device_errors(_stream(device), ctypes.byref(flags)))
     return int(flags.value)
+
+
+from .speculative import (Rope, pkv_rope_append, pkv_rope_init, pkv_tree_attention,  # noqa: E402,F401
+                          pkv_tree_attention_workspace_size, pkv_tree_commit, pkv_tree_mask)

@@ -41,6 +41,78 @@ cudaError_t launch_csr_tables(const int32_t* indptr, const int32_t* indices, int
 cudaError_t launch_append(const AppendParams& p, int src_kind, bool fp8, bool slots_i64,
                           cudaStream_t stream);
 
+// ---------------------------------------------------------------- rotary append
+struct RopeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;  // row strides (elements)
+  const void* positions;
+  const void* slots;
+  int32_t pos_i64, slots_i64;
+  void* k_cache;
+  void* v_cache;
+  int64_t T;
+  int32_t Hq, Hkv, D;
+  int64_t num_slots;
+  float k_inv_scale, v_inv_scale;
+  // units of work of a token, set by the launcher (see pkv_rope.cu)
+  int32_t rot_units, pass_units, v_units, units, units_per_part;
+  unsigned int* err;
+  pkv_rope rope;
+};
+// src_kind: 0 = f32 rows, 1 = bf16 rows.
+cudaError_t launch_rope_append(const RopeParams& p, int src_kind, bool fp8, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- drafted trees
+cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* cu_q, const int32_t* seq_lens, int32_t B, int64_t T,
+                             int32_t* mask, int64_t mask_stride, int32_t words, int32_t* positions, unsigned int* err,
+                             cudaStream_t st);
+
+struct CommitParams {
+  const int32_t* accepted;
+  int64_t accepted_stride;
+  int32_t A;
+  const int32_t* accepted_lens;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const int32_t* bt;
+  int64_t bt_stride;
+  int32_t max_blocks, B, bs;
+  int64_t num_blocks;
+  char* k_cache;
+  char* v_cache;
+  int64_t row_bytes;  // one token's row, all heads
+  int32_t* new_lens;  // may be NULL
+  unsigned int* err;
+};
+cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st);
+
+struct TreeParams {
+  const void* q;
+  int64_t q_st, q_sh;
+  void* out;
+  int64_t T, o_st, o_sh;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const int32_t* bt;
+  int64_t bt_stride;
+  int32_t max_blocks, B;
+  const int32_t* mask;
+  int64_t mask_stride;
+  int32_t max_nodes;  // sequences with more nodes are refused
+  const void* k_cache;
+  const void* v_cache;
+  int64_t num_blocks;
+  int32_t bs, bs_shift;
+  int32_t Hq, Hkv, G, D;
+  float qk_scale_log2, v_scale;
+  unsigned int* err;
+};
+// Plain kernel for f32 queries and caches.  out_kind: 0 = f32, 1 = bf16.
+cudaError_t launch_tree_f32(const TreeParams& p, int kv, int out_kind, cudaStream_t st);
+
 // ---------------------------------------------------------------- attention
 // Device workspace of one attention call (all offsets 256-byte aligned).
 // One decode unit: a logical chunk of one sequence (all KV heads share it).
@@ -224,5 +296,11 @@ cudaError_t launch_prefill_tc(const AttnParams& p, int out_kind, int64_t max_uni
 
 // Records msg as the calling thread's pkv_last_error() and returns st.
 pkv_status record_failure(pkv_status st, const std::string& msg);
+// Address of the device's error word and its SM count, with that device
+// current.
+pkv_status device_state(unsigned int** err, int* num_sms);
+// After the launches of a call: in check mode, wait for the stream and turn
+// a recorded device error into a status.
+pkv_status finish(cudaStream_t st, const char* what);
 
 }  // namespace pkv
