@@ -110,8 +110,15 @@ struct TreeParams {
   float qk_scale_log2, v_scale;
   unsigned int* err;
 };
-// Plain kernel for f32 queries and caches.  out_kind: 0 = f32, 1 = bf16.
-cudaError_t launch_tree_f32(const TreeParams& p, int kv, int out_kind, cudaStream_t st);
+// f32 queries and caches.  out_kind: 0 = f32, 1 = bf16.
+cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st);
+// bf16 queries, bf16 or e4m3 caches, D 64 or 128.  max_q: bound of a
+// sequence's nodes; max_ctx: tokens a block table can hold.  The workspace
+// holds tree_tc_rows_per_seq() partial rows (D + 1 floats per head) for each
+// sequence.
+int64_t tree_tc_rows_per_seq(int64_t max_q, int64_t max_ctx);
+cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t max_q, int64_t max_ctx, void* workspace,
+                           int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention
 // Device workspace of one attention call (all offsets 256-byte aligned).

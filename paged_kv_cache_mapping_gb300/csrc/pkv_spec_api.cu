@@ -13,6 +13,8 @@ using namespace pkv;
 
 namespace {
 
+constexpr int kTreeKeyTile = 128;  // chunk bounds are rounded up to key tiles in 32 bits
+
 pkv_status check_index_vector(const char* name, const pkv_tensor* t, int64_t len) {
   PKV_TRY(check_tensor(name, t, 1));
   PKV_NEED(t->dtype == PKV_I32 || t->dtype == PKV_I64, describe(name, t) + ": must be i32 or i64");
@@ -54,6 +56,11 @@ pkv_status check_mask(const char* name, const pkv_tensor* m, int64_t T) {
   PKV_NEED(m->shape[1] <= 1 || m->stride[1] == 1, std::string(name) + ": column stride must be 1");
   PKV_NEED(m->shape[0] <= 1 || m->stride[0] >= m->shape[1], std::string(name) + ": rows overlap");
   return PKV_OK;
+}
+
+// nodes a sequence may have: the caller's bound, else every row
+int64_t max_nodes_of(int32_t max_q_len, int64_t T) {
+  return max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T;
 }
 
 bool bytes_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -276,8 +283,11 @@ pkv_status pkv_tree_attention_workspace_size(const pkv_tensor* q, const pkv_tens
   PKV_TRY(check_tensor("block_tables", block_tables, 2));
   PKV_TRY(check_tensor("k_cache", k_cache, 4));
   PKV_NEED(bytes != nullptr, "bytes is NULL");
-  (void)max_q_len;
   *bytes = 0;
+  if (k_cache->dtype == PKV_F32) return PKV_OK;
+  const int64_t rows = block_tables->shape[0] *
+                       tree_tc_rows_per_seq(max_nodes_of(max_q_len, q->shape[0]), block_tables->shape[1] * k_cache->shape[1]);
+  *bytes = align_up(sizeof(float) * rows * q->shape[1] * (q->shape[2] + 1), 256);
   return PKV_OK;
 }
 
@@ -300,7 +310,9 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
   PKV_NEED(Hq <= (1 << 16), "Hq beyond 65536");
   PKV_NEED(out->shape[0] == T && out->shape[1] == Hq && out->shape[2] == D, describe("out", out) + " must have q's shape");
   PKV_NEED(out->dtype == PKV_F32 || out->dtype == PKV_BF16, "out must be f32 or bf16");
-  PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX, "max_blocks * block_size beyond int32");
+  PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX - kTreeKeyTile, "max_blocks * block_size beyond int32");
+  PKV_NEED(NB >= 1, "the cache has no blocks");
+  if (T * (Hq / Hkv) > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "T * Hq / Hkv beyond int32");
   if (NB * bs > INT32_MAX / Hkv)
     return fail(PKV_ERR_UNSUPPORTED, "num_blocks * block_size * Hkv beyond int32 (rows are numbered in 32 bits)");
   PKV_TRY(check_mask("tree_mask", tree_mask, T));
@@ -348,7 +360,8 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
   p.B = static_cast<int32_t>(B);
   p.mask = static_cast<const int32_t*>(tree_mask->data);
   p.mask_stride = tree_mask->stride[0];
-  p.max_nodes = static_cast<int32_t>(std::min<int64_t>(32 * tree_mask->shape[1], max_q_len > 0 ? max_q_len : INT32_MAX));
+  const int64_t max_q = max_nodes_of(max_q_len, T);
+  p.max_nodes = static_cast<int32_t>(std::min<int64_t>(32 * tree_mask->shape[1], max_q));
   p.k_cache = k_cache->data;
   p.v_cache = v_cache->data;
   p.num_blocks = NB;
@@ -365,7 +378,9 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
   PKV_TRY(device_state(&p.err, &sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0 || B == 0) return PKV_OK;
-  const cudaError_t e = launch_tree_f32(p, kv, out->dtype == PKV_BF16, st);
+  const int out_kind = out->dtype == PKV_BF16;
+  const cudaError_t e = kv == 0 ? launch_tree_f32(p, out_kind, st)
+                                : launch_tree_tc(p, kv == 2, out_kind, p.max_nodes, block_tables->shape[1] * bs, workspace, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return finish(st, "pkv_tree_attention");
 }

@@ -170,18 +170,12 @@ cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st) {
   return launch_ex(tree_commit_kernel<uint2>, grid, dim3(kCommitThreads), 0, st, true, p);
 }
 
-// ---------------------------------------------------------------- plain attention
-// One CTA per (row, KV head), a warp per query head of the group, lanes over
-// D: the simplest kernel that is right.
-__device__ __forceinline__ float elem(const float* p, int64_t i) { return __ldg(p + i); }
-__device__ __forceinline__ float elem(const __nv_bfloat16* p, int64_t i) { return static_cast<float>(p[i]); }
-__device__ __forceinline__ float elem(const uint8_t* p, int64_t i) {
-  const uint32_t h = e4m3x2_to_f16x2(p[i]);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffffu)));
-}
-
-template <typename QT, typename KT, typename OutT>
-__global__ void __launch_bounds__(128) tree_plain_kernel(TreeParams p) {
+// ---------------------------------------------------------------- fp32 attention
+// fp32 queries and caches, on the CUDA cores like pkv_attention's fp32 path:
+// one CTA per (row, KV head), a warp per query head of the group, lanes over
+// D, one key at a time.
+template <typename OutT>
+__global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
   launch_dependents();
   grid_dep_wait();
   const int64_t t = blockIdx.x;
@@ -192,23 +186,24 @@ __global__ void __launch_bounds__(128) tree_plain_kernel(TreeParams p) {
   const int c0 = __ldg(p.cu_q + s);
   const int q_s = __ldg(p.cu_q + s + 1) - c0;
   const int n = __ldg(p.seq_lens + s);
-  if (q_s < 0 || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs || t < c0 || t - c0 >= q_s || q_s > p.max_nodes) {
+  if (q_s < 0 || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs || t < c0 || t - c0 >= q_s || q_s > p.max_nodes ||
+      c0 < 0 || (int64_t)c0 + q_s > p.T) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrLengths);
     return;
   }
   const int ctx = n - q_s;
   const int per = p.D / 32;  // elements per lane, <= 8
-  const KT* kc = static_cast<const KT*>(p.k_cache);
-  const KT* vc = static_cast<const KT*>(p.v_cache);
+  const float* kc = static_cast<const float*>(p.k_cache);
+  const float* vc = static_cast<const float*>(p.v_cache);
   const int32_t* bt_row = p.bt + (int64_t)s * p.bt_stride;
   const int32_t* mask = p.mask + t * p.mask_stride;
   for (int hh = warp; hh < p.G; hh += blockDim.x >> 5) {
     const int h = g * p.G + hh;
-    const QT* qrow = static_cast<const QT*>(p.q) + t * p.q_st + (int64_t)h * p.q_sh;
+    const float* qrow = static_cast<const float*>(p.q) + t * p.q_st + (int64_t)h * p.q_sh;
     float qv[8], o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      qv[k] = k < per ? elem(qrow, lane + 32 * k) : 0.f;
+      qv[k] = k < per ? __ldg(qrow + lane + 32 * k) : 0.f;
       o[k] = 0.f;
     }
     float m = -INFINITY, l = 0.f;
@@ -224,7 +219,7 @@ __global__ void __launch_bounds__(128) tree_plain_kernel(TreeParams p) {
       float dot = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < per) dot = fmaf(qv[k], elem(kc, row + lane + 32 * k), dot);
+        if (k < per) dot = fmaf(qv[k], __ldg(kc + row + lane + 32 * k), dot);
 #pragma unroll
       for (int o2 = 16; o2 > 0; o2 >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o2);
       const float x = dot * p.qk_scale_log2;
@@ -234,27 +229,21 @@ __global__ void __launch_bounds__(128) tree_plain_kernel(TreeParams p) {
       l = l * alpha + w;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < per) o[k] = fmaf(w, elem(vc, row + lane + 32 * k), o[k] * alpha);
+        if (k < per) o[k] = fmaf(w, __ldg(vc + row + lane + 32 * k), o[k] * alpha);
       m = mn;
     }
     OutT* orow = static_cast<OutT*>(p.out) + t * p.o_st + (int64_t)h * p.o_sh;
-    const float inv = l == 0.f ? 0.f : p.v_scale / l;  // a row that sees nothing is zero
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zero
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < per) store1(orow + lane + 32 * k, l == 0.f ? 0.f : o[k] * inv);
   }
 }
 
-cudaError_t launch_tree_f32(const TreeParams& p, int kv, int out_kind, cudaStream_t st) {
+cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st) {
   const dim3 grid((unsigned)p.T, (unsigned)p.Hkv), block(128);
-  using B16 = __nv_bfloat16;
-#define PKV_TREE(Q, K) \
-  (out_kind ? launch_ex(tree_plain_kernel<Q, K, B16>, grid, block, 0, st, true, p) \
-            : launch_ex(tree_plain_kernel<Q, K, float>, grid, block, 0, st, true, p))
-  if (kv == 0) return PKV_TREE(float, float);
-  if (kv == 1) return PKV_TREE(B16, B16);
-  return PKV_TREE(B16, uint8_t);
-#undef PKV_TREE
+  return out_kind ? launch_ex(tree_f32_kernel<__nv_bfloat16>, grid, block, 0, st, true, p)
+                  : launch_ex(tree_f32_kernel<float>, grid, block, 0, st, true, p);
 }
 
 }  // namespace pkv
