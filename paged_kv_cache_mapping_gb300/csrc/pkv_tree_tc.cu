@@ -35,13 +35,18 @@
 // hi and lo, lo scaled by 16 with an accumulator of its own, so that the
 // smallest codes' step is 2^-17 of the row's reference.
 //
-// CTA: 12 warps.
-//   warp 0      items, and TMA copies of the K and V tiles of 128 keys: boxes
-//               of 16 or 8 slots that lie in one block, or, for other block
-//               sizes, four arbitrary rows at a time (tile::gather4).
-//   warp 1      issues the MMAs: S of tile g + 1, then P V of tile g.
-//   warps 2, 3  query rows: bf16 to the swizzled operand layout, or split to e4m3.
+// CTA: 16 warps.
+//   warp 0      finds the items and publishes each one ahead; copies K tiles
+//               of 128 keys by TMA: boxes of 16 or 8 slots that lie in one
+//               block, or, for other block sizes, four arbitrary rows at a time
+//               (tile::gather4).
+//   warp 1      issues the MMAs: S of tile g + 1, then P V of tile g.  The two
+//               parts of P are 2 N columns of one operand, so O holds their two
+//               products side by side and P V costs one pass of instructions.
+//   warp 2      query rows: bf16 to the swizzled operand layout, or split to e4m3.
+//   warp 3      copies V tiles.
 //   warps 4-11  softmax: lane quarter w % 4 = keys, half (w - 4) / 4 = rows.
+//   warps 12-15 write O / l of finished items while the next one runs.
 #include <cuda.h>
 
 #include <algorithm>
@@ -53,8 +58,8 @@ namespace pkv {
 namespace {
 
 constexpr int kKeys = 128;  // keys per tile (M of S^T, K of P V)
-constexpr int kThreads = 384;
-constexpr int kItemSlots = 4;
+constexpr int kThreads = 512;
+constexpr int kItemSlots = 6;
 constexpr int kInfoSlots = 8;
 
 // ---------------------------------------------------------------- chunking
@@ -84,20 +89,20 @@ struct Geo {
   static constexpr int kTileB = kKeys * kRowB;
   static constexpr int kParts = F8 ? 2 : 1;                   // parts of Q
   static constexpr int kQB = N * kRowB * kParts;
-  static constexpr int kPB = kKeys * 128;                     // one part of P: [128 keys][128 bytes]
+  static constexpr int kPRow = 2 * N * kEs;                   // both parts of P of one key
+  static constexpr int kPB = kKeys * (kPRow <= 128 ? 128 : 256);  // [1 or 2][128 keys][128 bytes]
   static constexpr int kNK = kTileB == 32768 ? 2 : kTileB == 16384 ? 4 : 6;
   static constexpr int kNV = kTileB == 32768 ? 3 : kTileB == 16384 ? 5 : 6;
   static constexpr int kNC = N / 2;                           // rows (columns of S^T) per softmax warp
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kNK * kTileB;
   static constexpr int kOffP = kOffV + kNV * kTileB;
-  static constexpr int kOffQ = kOffP + 2 * kPB;
+  static constexpr int kOffQ = kOffP + kPB;
   static constexpr int kOffMisc = kOffQ + 2 * kQB;
   static constexpr int kSmem = kOffMisc + (F8 ? 4096 : 3072);
-  // tensor memory: S 2 x N columns, then O: 2 x N (e4m3: hi and lo of each)
+  // tensor memory: S 2 x N columns, then O 2 x (hi N, lo N)
   static constexpr uint32_t kColO = 2 * N;
-  static constexpr uint32_t kOCols = F8 ? 2 * N : N;
-  static constexpr int kSteps = kRowB / 32;                   // MMA k steps of S^T (32 bytes each)
+  static constexpr uint32_t kOCols = 2 * N;
   static constexpr int kKeyStep = F8 ? 32 : 16;               // keys per MMA k step of P V
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kNK + 2 <= kInfoSlots, "tile info ring");
@@ -105,20 +110,20 @@ struct Geo {
 };
 
 struct Item {
-  int s, h, r0, rows;       // sequence, KV head, first row of the tile, rows of the sequence (q_s * G)
-  int t0, q_s, n, ctx;      // first packed row, nodes, keys, context keys
-  int k0, k1, c, nchunks;   // keys of the chunk, its index, chunks of the sequence
-  int live, pad0, pad1, pad2;
+  int s, h, r0;         // sequence (-1: no more items), KV head, first row of the tile
+  int t0, q_s, n;       // first packed row, nodes, keys
+  int k0, k1;           // keys of the chunk
+  int c, nchunks;       // its index, chunks of the sequence
 };
 
 // barrier area
 enum : int {
-  kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26, kBODone = 27, kBOFree = 28,
-  kBQFull = 30, kBQEmpty = 32, kBQsFull = 34, kBItemFull = 38, kBItemEmpty = 42, kBInfo = 46, kBGroup = 54,
-  kBAll = 56, kBDrain = 57, kSTmem = 58, kSAbort = 59, kSVote = 60 /* [2][2] ints: 60, 61 */, kSPoison = 62,
-  /* [3] ints: 62, 63 */
-  kOffItems = 512, kOffInfo = 768, kOffXch = 896, kOffLinv = 1920, kOffQs = 2688,
+  kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26, kBODone = 27, kBOFull = 28,
+  kBOFree = 30, kBQFull = 32, kBQEmpty = 34, kBQsFull = 36, kBLFull = 40, kBItemFull = 43, kBItemEmpty = 49,
+  kBInfo = 55, kBDrain = 63, kSTmem = 64, kSAbort = 65, kSPoison = 66 /* [3] ints: 66, 67 */,
+  kOffItems = 576, kOffInfo = 816, kOffXch = 944, kOffLinv = 1968, kOffRef = 2736, kOffQs = 2992,
 };
+static_assert(kOffItems + kItemSlots * (int)sizeof(Item) <= kOffInfo, "item ring");
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, int atom) {
@@ -132,29 +137,26 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool f8, bool a_mn, bool b_m
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// Issued from one lane of a converged warp (elect.sync), operands uniform.
-template <bool F8>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  if constexpr (F8) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc));
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc));
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+template <bool F8, int kSteps, int kA, int kB>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    if constexpr (F8) {
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a + k * kA), "l"(b + k * kB), "r"(id), "r"(k ? 1u : acc));
+    } else {
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a + k * kA), "l"(b + k * kB), "r"(id), "r"(k ? 1u : acc));
+    }
   }
 }
-
 __device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -208,10 +210,64 @@ __device__ __forceinline__ uint64_t l2_normal_policy() {
   return pol;
 }
 
+// Wait by a whole warp, at most 2^20 tries (tens of milliseconds and more; a
+// try suspends the warp for a while).  The code is kept short, here and below:
+// with the roles' code well past a hundred KB the instruction caches, not the
+// pipes, set the pace.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+      "W:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 1048576;\n\t@q bra W;\n"
+      "D:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// three-input max: exact, like two fmaxf
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// packed pairs of fp32: one instruction does two lanes' worth of work
+__device__ __forceinline__ unsigned long long pk2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void up2(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long sub2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ void st_s128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -221,16 +277,33 @@ __device__ __forceinline__ void st_s64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// largest of a warp's values, NaN passed over
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(__half2 h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
+  return r;
+}
+
 // 16-byte chunk c of row r in a swizzled [rows][atom bytes] tile
 template <int kAtomB>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   return kAtomB == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Reduces NC columns over the 32 lanes by halving: afterwards every lane
-// holds column lane / (32 / NC)'s result.
-template <int NC, typename Op>
-__device__ __forceinline__ float col_reduce(float (&v)[NC], int lane, Op op) {
+// Adds NC columns up over the 32 lanes by halving: afterwards every lane holds
+// column lane / (32 / NC)'s sum.
+template <int NC>
+__device__ __forceinline__ float col_sum(float (&v)[NC], int lane) {
   int w = NC;
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) {
@@ -241,24 +314,82 @@ __device__ __forceinline__ float col_reduce(float (&v)[NC], int lane, Op op) {
       for (int j = 0; j < NC / 2; ++j) {
         if (j < w) {
           const float send = up ? v[j] : v[j + w], keep = up ? v[j + w] : v[j];
-          v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
+          v[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
       }
     } else {
-      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], s));
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
     }
   }
   return v[0];
 }
 
+// Division of 0 <= x < 2^31 by a constant d >= 1 of the call: one multiply-high
+// and a shift.  M = floor(2^(32 + s) / d) + 1 with 2^s < d <= 2^(s + 1): M fits
+// 32 bits, x M / 2^(32 + s) passes x / d by at most x / 2^(32 + s) < 1 / d, so
+// the floor is exact.  d = 1 is x itself.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while (f.s < 31 && (2u << f.s) < d) ++f.s;
+  if (d > 1) f.m = static_cast<uint32_t>(((uint64_t)1 << (32 + f.s)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int quot(int x, const FastDiv& f) {
+  return f.d == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), f.m) >> f.s);
+}
+
 struct TcArgs {
   TreeParams p;
+  FastDiv by_g, by_bs;
   int32_t rows_per_seq;  // partial rows of a sequence
   int32_t box;           // slots per TMA box, 0: gather4
   int32_t out_bf16;
   float* part_o;         // [B * rows_per_seq, Hq, D] normalised chunk outputs
   float* part_lse;       // [B * rows_per_seq, Hq]
 };
+
+// A drafted value (element d of some V row) is not finite: the softmax warps
+// took it out of the product, and here it goes to the rows that see its key,
+// on top of what this thread has just stored.
+template <int D, bool F8>
+__device__ __noinline__ void add_poison(const TcArgs& a, const Item& it, int d, char* at, int64_t step, int64_t wrap,
+                                        bool wide, int count) {
+  const TreeParams& p = a.p;
+  const int i0 = it.r0 / p.G, g0 = it.r0 - i0 * p.G;
+  const int ctx = it.n - it.q_s;
+  for (int k = max(ctx, it.k0); k < it.k1; ++k) {
+    const int lb = k / p.bs, jj = k - ctx;
+    const int32_t blk = __ldg(p.bt + (int64_t)it.s * p.bt_stride + lb);
+    if ((uint32_t)blk >= (uint64_t)p.num_blocks) continue;
+    const int64_t va = (((int64_t)blk * p.bs + (k - lb * p.bs)) * p.Hkv + it.h) * D + d;
+    float x;
+    if constexpr (F8) {
+      const uint32_t hf = e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v_cache)[va]);
+      x = __half2float(__ushort_as_half(static_cast<unsigned short>(hf & 0xffffu)));
+    } else {
+      x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[va]);
+    }
+    if (fabsf(x) < INFINITY) continue;
+    char* y = at;
+    for (int c = 0, i = i0, g = g0; c < count; ++c) {
+      if ((static_cast<uint32_t>(__ldg(p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj >> 5))) >> (jj & 31)) & 1u) {
+        if (wide)
+          *reinterpret_cast<float*>(y) += x;
+        else
+          *reinterpret_cast<__nv_bfloat16*>(y) = __float2bfloat16_rn(__bfloat162float(*reinterpret_cast<__nv_bfloat16*>(y)) + x);
+      }
+      y += step;
+      if (++g == p.G) {
+        g = 0;
+        ++i;
+        y += wrap;
+      }
+    }
+  }
+}
 
 template <int D, int N, bool F8>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -273,11 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return b0 + 8 * i; };
   const uint32_t sK = s0 + G_::kOffK, sV = s0 + G_::kOffV, sP = s0 + G_::kOffP, sQ = s0 + G_::kOffQ;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 8 * kSAbort);
+  volatile int* poison = reinterpret_cast<volatile int*>(misc + 8 * kSPoison);  // [3]: item + 1
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 8 * kSTmem);
   Item* items = reinterpret_cast<Item*>(misc + kOffItems);
   uint32_t* info = reinterpret_cast<uint32_t*>(misc + kOffInfo);  // [kInfoSlots][4]: keys without a page
-  float* xch = reinterpret_cast<float*>(misc + kOffXch);          // [2][4][32]
+  float* xch = reinterpret_cast<float*>(misc + kOffXch);          // [2 halves][4 quarters][32]
   float* linv = reinterpret_cast<float*>(misc + kOffLinv);        // [3][64]
+  float* refs = reinterpret_cast<float*>(misc + kOffRef);         // [64]
   float* qscale = reinterpret_cast<float*>(misc + kOffQs);        // e4m3: [4][64]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0); };
@@ -298,24 +431,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBSFull + i), 1);
-      mbar_init(bar(kBOFree + i), 8);
-      mbar_init(bar(kBQFull + i), 2);
+      mbar_init(bar(kBOFull + i), 1);
+      mbar_init(bar(kBOFree + i), 4);
+      mbar_init(bar(kBQFull + i), 1);
       mbar_init(bar(kBQEmpty + i), 1);
-      mbar_init(bar(kBGroup + i), 4);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(bar(kBLFull + i), 8);
     mbar_init(bar(kBPFull), 8);
     mbar_init(bar(kBODone), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(kBQsFull + i), 1);
     for (int i = 0; i < kItemSlots; ++i) {
-      mbar_init(bar(kBQsFull + i), 2);
       mbar_init(bar(kBItemFull + i), 1);
-      mbar_init(bar(kBItemEmpty + i), 11);
+      mbar_init(bar(kBItemEmpty + i), 15);  // every warp but the first
     }
     for (int i = 0; i < kInfoSlots; ++i) mbar_init(bar(kBInfo + i), 1);
-    mbar_init(bar(kBAll), 8);
     mbar_init(bar(kBDrain), 1);
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) reinterpret_cast<volatile int*>(misc + 8 * kSVote)[i] = 0;
-    for (int i = 0; i < 4; ++i) reinterpret_cast<volatile int*>(misc + 8 * kSPoison)[i] = 0;
+    for (int i = 0; i < 3; ++i) poison[i] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane < 2)
@@ -333,21 +465,73 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // item j as the other warps take it
   auto take = [&](int j, Item& it) -> bool {
-    if (!mbar_wait_warp(bar(kBItemFull + j % kItemSlots), (j / kItemSlots) & 1, p.err)) return false;
+    if (!wait_bar(bar(kBItemFull + j % kItemSlots), (j / kItemSlots) & 1)) return false;
     it = items[j % kItemSlots];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBItemEmpty + j % kItemSlots));
-    return true;
+    return !aborted();
   };
   auto tiles_of = [](const Item& it) { return (it.k1 - it.k0 + kKeys - 1) / kKeys; };
 
+  // ---- copies of K or V tiles: pages, slots, TMA
+  const int bx = a.box;
+  const int n_box = bx ? kKeys / bx : 32;
+  const int key_of = bx ? (lane % n_box) * bx : lane * 4;  // first key of this lane's box (or four keys)
+  const int sub_of = bx ? lane / n_box : 0;                // its sub-tile
+  constexpr int32_t kPast = INT32_MIN;
+  // pages of this lane's keys in a tile
+  auto pages = [&](const Item& it, int t, int32_t (&blk)[4]) {
+    const int32_t* row = p.bt + (int64_t)it.s * p.bt_stride;
+    const int k = it.k0 + t * kKeys + key_of;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      blk[e] = kPast;
+      if ((e == 0 || !bx) && k + e < it.k1)
+        blk[e] = __ldg(row + quot(k + e, a.by_bs));
+    }
+  };
+  // copies the tile into dst; returns the lane's keys whose page is out of range
+  auto load_tile = [&](const Item& it, int t, const int32_t (&blk)[4], uint32_t dst, const CUtensorMap* map, uint32_t full,
+                       uint64_t pol) -> uint32_t {
+    const int k = it.k0 + t * kKeys + key_of;
+    uint32_t bad = 0;
+    int sl[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sl[e] = -1;
+      if (e > 0 && bx) continue;
+      if ((uint32_t)blk[e] < (uint64_t)p.num_blocks) {
+        sl[e] = (blk[e] - quot(k + e, a.by_bs)) * p.bs + k + e;
+      } else if (blk[e] != kPast) {
+        bad |= 1u << e;
+      }
+    }
+    if (lane == 0) mbar_arrive_expect_tx(full, G_::kTileB);
+    __syncwarp();
+    if (bx) {
+      // past the sequence, or a page out of range: out of bounds, which TMA fills with zeros
+      if (sub_of < G_::kSub)
+        tma_box(dst + sub_of * kKeys * AT + key_of * AT, map, sub_of * (AT / G_::kEs), it.h,
+                sl[0] >= 0 ? sl[0] : (int)(p.num_blocks * p.bs), full, pol);
+    } else {
+      int r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = sl[e] >= 0 ? sl[e] * Hkv + it.h : it.h;  // any row: the softmax drops it
+#pragma unroll
+      for (int u = 0; u < G_::kSub; ++u)
+        tma_gather4(dst + u * kKeys * AT + key_of * AT, map, u * (AT / G_::kEs), r, full, pol);
+    }
+    return bad;
+  };
+  // K and V are read once where one tile of rows holds them all
+  const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_normal_policy();
+  auto policy = [&](const Item& it) { return it.q_s * G <= N ? pol_once : pol_keep; };
+
   if (warp == 0) {
-    // ======================= items and copies =======================
-    const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_normal_policy();
-    const int64_t n_slots = p.num_blocks * p.bs;
+    // ======================= items, K tiles =======================
     int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
     int c0 = 0, q_s = 0, n = 0, chunk = 1, nchunks = 0, rts = 0;
-    long long cnt = 0, incl = 0, base = 0, total = 0;  // items: this sequence's, prefix in the group; before it; in it
+    int cnt = 0, incl = 0, base = 0, total = 0;  // items: this sequence's, prefix in the group; before it; in it
     auto load_group = [&]() {
       const int s = gb + lane;
       cnt = 0;
@@ -361,281 +545,252 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
         if (!bad && q_s > 0) {
           chunk = tree_chunk(n, q_s);
-          nchunks = static_cast<int>(((long long)n + chunk - 1) / chunk);
-          rts = static_cast<int>(((int64_t)q_s * G + N - 1) / N);
-          cnt = (long long)nchunks * Hkv * rts;
+          nchunks = (n - 1) / chunk + 1;
+          rts = (q_s * G - 1) / N + 1;
+          cnt = nchunks * Hkv * rts;
         }
       }
       incl = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       total = __shfl_sync(0xffffffffu, incl, 31);
     };
     load_group();
-    // item number x of the call, or live = 0 past the last
-    auto find = [&](long long x) -> Item {
+    // item number x of the call, or s = -1 past the last
+    auto find = [&](int x) -> Item {
       Item it{};
-      while (x >= base + total) {
+      it.s = -1;
+      while (x - base >= total) {
         base += total;
+        total = 0;
         gb += 32;
         if (gb >= p.B) return it;
         load_group();
       }
-      const int o = __ffs(__ballot_sync(0xffffffffu, base + incl > x)) - 1;
-      long long y = x - base - __shfl_sync(0xffffffffu, incl - cnt, o);
+      const int o = __ffs(__ballot_sync(0xffffffffu, incl > x - base)) - 1;
+      int y = x - base - __shfl_sync(0xffffffffu, incl - cnt, o);
       it.s = gb + o;
       it.t0 = __shfl_sync(0xffffffffu, c0, o);
       it.q_s = __shfl_sync(0xffffffffu, q_s, o);
       it.n = __shfl_sync(0xffffffffu, n, o);
       it.nchunks = __shfl_sync(0xffffffffu, nchunks, o);
       const int rt_n = __shfl_sync(0xffffffffu, rts, o), len = __shfl_sync(0xffffffffu, chunk, o);
-      it.r0 = static_cast<int>(y % rt_n) * N;
+      it.r0 = (y % rt_n) * N;
       y /= rt_n;
-      it.h = static_cast<int>(y % Hkv);
-      it.c = static_cast<int>(y / Hkv);
-      it.k0 = static_cast<int>((long long)it.c * len);
-      it.k1 = static_cast<int>(min((long long)it.n, (long long)it.k0 + len));
-      it.rows = it.q_s * G;
-      it.ctx = it.n - it.q_s;
-      it.live = 1;
+      it.h = y % Hkv;
+      it.c = y / Hkv;
+      it.k0 = it.c * len;
+      it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
       return it;
     };
-    const int bx = a.box;
-    const int n_box = bx ? kKeys / bx : 0;
-    const int key_of = bx ? (lane % n_box) * bx : lane * 4;  // first key of this lane's box (or four keys)
-    const int sub_of = bx ? lane / n_box : 0;                // its sub-tile
-    const bool issuer = bx ? sub_of < G_::kSub : true;
-    constexpr int32_t kPast = INT32_MIN;
-    // pages of this lane's keys in a tile
-    auto pages = [&](const Item& it, int t, int32_t (&blk)[4]) {
-      const int32_t* row = p.bt + (int64_t)it.s * p.bt_stride;
-      const int k = it.k0 + t * kKeys + key_of;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        blk[e] = kPast;
-        if ((e == 0 || !bx) && k + e < it.k1) blk[e] = __ldg(row + (p.bs_shift >= 0 ? (k + e) >> p.bs_shift : (k + e) / p.bs));
+    auto publish = [&](int j, const Item& it) -> bool {
+      if (!wait_bar(bar(kBItemEmpty + j % kItemSlots), ((j / kItemSlots) & 1) ^ 1)) return false;
+      if (lane == 0) {
+        items[j % kItemSlots] = it;
+        mbar_arrive(bar(kBItemFull + j % kItemSlots));
       }
+      __syncwarp();
+      return true;
     };
-    // slots of this lane's keys (-1: none), and the tile's keys whose page is
-    // out of range as bits in `info`
-    auto slots = [&](const Item& it, int t, const int32_t (&blk)[4], int (&sl)[4], int g) {
-      const int k = it.k0 + t * kKeys + key_of;
-      uint32_t bad = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sl[e] = -1;
-        if (e > 0 && bx) break;
-        if ((uint32_t)blk[e] < (uint64_t)p.num_blocks) {
-          const int lb = p.bs_shift >= 0 ? (k + e) >> p.bs_shift : (k + e) / p.bs;
-          sl[e] = blk[e] * p.bs + (k + e - lb * p.bs);
-        } else if (blk[e] != kPast) {
-          bad |= 1u << e;
+    // The walk: (it, t) is the tile to load, blk its pages.  Each step finds
+    // the tile after it and starts that one's page loads; at an item's first
+    // tile the item after it is found and published, so that its query rows
+    // load under this item.
+    int j = 0, g = 0, t = 0, nt = 0;
+    Item it{}, next{};
+    it.s = next.s = -1;
+    int32_t blk[4] = {kPast, kPast, kPast, kPast};
+    bool ok = true;
+    for (;;) {
+      if (t == nt) {  // the item is done (or none was begun): go to the next
+        it = next;
+        nt = tiles_of(it);
+        t = 0;
+        if (j > 0 && it.s < 0) break;
+        next = find(blockIdx.x + j * (int)gridDim.x);
+        ok = publish(j, next) && !aborted();
+        if (!ok) break;
+        ++j;
+        if (j == 1) {
+          nt = 0;
+          if (next.s >= 0) pages(next, 0, blk);
+          continue;
         }
       }
+      const bool last = t + 1 == nt;
+      int32_t nb[4] = {kPast, kPast, kPast, kPast};
+      if (!last || next.s >= 0) pages(last ? next : it, last ? 0 : t + 1, nb);
+      ok = wait_bar(bar(kBKEmpty + g % NK), ((g / NK) & 1) ^ 1);
+      if (!ok) break;
+      const uint32_t bad = load_tile(it, t, blk, sK + (g % NK) * G_::kTileB, &tm_k, bar(kBKFull + g % NK), policy(it));
+      // the tile's keys without a page, for the softmax
       uint32_t* w = info + (g % kInfoSlots) * 4;
       if (lane < 4) w[lane] = 0;
       __syncwarp();
       if (__any_sync(0xffffffffu, bad != 0)) {
         if (bad) {
           atomicOr(p.err, kErrBlockRange);
-          if (bx) {
-            if (sub_of == 0) atomicOr(w + key_of / 32, (bx == 16 ? 0xffffu : 0xffu) << (key_of & 31));
-          } else {
+          if (!bx) {
             atomicOr(w + key_of / 32, bad << (key_of & 31));
+          } else if (sub_of == 0) {
+            atomicOr(w + key_of / 32, (bx == 16 ? 0xffffu : 0xffu) << (key_of & 31));
           }
         }
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(bar(kBInfo + g % kInfoSlots));
-    };
-    auto load_tile = [&](const Item& it, const int (&sl)[4], uint32_t dst, const CUtensorMap* map, uint32_t full, uint64_t pol) {
-      if (lane == 0) mbar_arrive_expect_tx(full, G_::kTileB);
-      __syncwarp();
-      if (bx) {
-        // past the sequence, or a page out of range: out of bounds, which TMA fills with zeros
-        if (issuer)
-          tma_box(dst + sub_of * kKeys * AT + key_of * AT, map, sub_of * (AT / G_::kEs), it.h,
-                  sl[0] >= 0 ? sl[0] : (int)n_slots, full, pol);
-      } else {
-        int r[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = sl[e] >= 0 ? sl[e] * Hkv + it.h : it.h;  // any row: the softmax drops it
-#pragma unroll
-        for (int u = 0; u < G_::kSub; ++u)
-          tma_gather4(dst + u * kKeys * AT + key_of * AT, map, u * (AT / G_::kEs), r, full, pol);
-      }
-    };
-    int j = 0, g = 0;
-    bool ok = true;
-    Item it = find(blockIdx.x);
-    int vs[4] = {-1, -1, -1, -1};  // slots of tile g - 1, whose V follows K of tile g
-    int v_h = 0;
-    uint64_t v_pol = pol_once;
-    auto load_v = [&](int gv) -> bool {
-      if (!mbar_wait_warp(bar(kBVEmpty + gv % NV), ((gv / NV) & 1) ^ 1, p.err)) return false;
-      Item vi{};
-      vi.h = v_h;
-      load_tile(vi, vs, sV + (gv % NV) * G_::kTileB, &tm_v, bar(kBVFull + gv % NV), v_pol);
-      return true;
-    };
-    int32_t blk[4];
-    if (it.live) pages(it, 0, blk);
-    for (;; ++j) {
-      ok = ok && mbar_wait_warp(bar(kBItemEmpty + j % kItemSlots), ((j / kItemSlots) & 1) ^ 1, p.err) && !aborted();
-      if (!ok) break;
-      if (lane == 0) {
-        items[j % kItemSlots] = it;
-        mbar_arrive(bar(kBItemFull + j % kItemSlots));
-      }
-      __syncwarp();
-      if (!it.live) break;
-      const int nt = tiles_of(it);
-      const Item next = find(blockIdx.x + (long long)(j + 1) * gridDim.x);
-      // K and V are read once where one tile of rows holds them all
-      const uint64_t pol = it.rows <= N ? pol_once : pol_keep;
-      for (int t = 0; t < nt && ok; ++t, ++g) {
-        int32_t nb[4] = {kPast, kPast, kPast, kPast};
-        if (t + 1 < nt) {
-          pages(it, t + 1, nb);
-        } else if (next.live) {
-          pages(next, 0, nb);
-        }
-        ok = mbar_wait_warp(bar(kBKEmpty + g % NK), ((g / NK) & 1) ^ 1, p.err);
-        if (!ok) break;
-        int sl[4];
-        slots(it, t, blk, sl, g);
-        load_tile(it, sl, sK + (g % NK) * G_::kTileB, &tm_k, bar(kBKFull + g % NK), pol);
-        if (g > 0) ok = load_v(g - 1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          vs[e] = sl[e];
-          blk[e] = nb[e];
-        }
-        v_h = it.h;
-        v_pol = pol;
-      }
-      it = next;
+      for (int e = 0; e < 4; ++e) blk[e] = nb[e];
+      ++t;
+      ++g;
     }
-    if (ok && g > 0) ok = load_v(g - 1);
     if (!ok) *abort_flag = 1;
-    if (!ok || aborted()) {
-      // let the copies issued so far land before the CTA exits
-      for (int k = g - 1; k >= 0 && k >= g - NK; --k) mbar_wait_warp(bar(kBKFull + k % NK), (k / NK) & 1, p.err);
-      for (int k = g - 1; k >= 0 && k >= g - NV; --k) mbar_wait_warp(bar(kBVFull + k % NV), (k / NV) & 1, p.err);
+    if (aborted())  // let the copies issued so far land before the CTA exits
+      for (int k = g - 1; k >= 0 && k >= g - NK; --k) wait_bar(bar(kBKFull + k % NK), (k / NK) & 1);
+  } else if (warp == 3) {
+    // ======================= V tiles =======================
+    int j = 0, g = 0, t = 0, nt = 0;
+    Item it{}, next{};
+    it.s = next.s = -1;
+    int32_t blk[4] = {kPast, kPast, kPast, kPast};
+    bool ok = true;
+    for (;;) {  // as warp 0's walk
+      if (t == nt) {
+        it = next;
+        nt = tiles_of(it);
+        t = 0;
+        if (j > 0 && it.s < 0) break;
+        ok = take(j, next);
+        if (!ok) break;
+        ++j;
+        if (j == 1) {
+          nt = 0;
+          if (next.s >= 0) pages(next, 0, blk);
+          continue;
+        }
+      }
+      const bool last = t + 1 == nt;
+      int32_t nb[4] = {kPast, kPast, kPast, kPast};
+      if (!last || next.s >= 0) pages(last ? next : it, last ? 0 : t + 1, nb);
+      ok = wait_bar(bar(kBVEmpty + g % NV), ((g / NV) & 1) ^ 1);
+      if (!ok) break;
+      load_tile(it, t, blk, sV + (g % NV) * G_::kTileB, &tm_v, bar(kBVFull + g % NV), policy(it));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) blk[e] = nb[e];
+      ++t;
+      ++g;
     }
+    if (!ok) *abort_flag = 1;
+    if (aborted())
+      for (int k = g - 1; k >= 0 && k >= g - NV; --k) wait_bar(bar(kBVFull + k % NV), (k / NV) & 1);
   } else if (warp == 1) {
     // ======================= MMA =======================
-    constexpr uint32_t kIdS = idesc(N, F8, false, false), kIdO = idesc(N, F8, true, true);
-    Item it{};
+    constexpr uint32_t kIdS = idesc(N, F8, false, false), kIdO = idesc(2 * N, F8, true, true);
+    Item it;
     int j = 0, g = 0;
     auto issue_s = [&](int gg, int qb) -> bool {
-      if (!mbar_wait_warp(bar(kBKFull + gg % NK), (gg / NK) & 1, p.err)) return false;
+      if (!wait_bar(bar(kBKFull + gg % NK), (gg / NK) & 1)) return false;
       fence_after();
       const uint64_t dk = sdesc(sK + (gg % NK) * G_::kTileB, 16, 8 * AT, AT);
       const uint64_t dq = sdesc(sQ + qb * G_::kQB, 16, 8 * AT, AT);
       const uint32_t ts = tmem + (gg & 1) * N;
+      if (elect_one()) {
 #pragma unroll
       for (int part = 0; part < G_::kParts; ++part)
 #pragma unroll
-        for (int k = 0; k < G_::kSteps; ++k) {
-          constexpr int per = AT / 32;
-          const uint32_t ok_ = (uint32_t)((k / per) * kKeys * AT + (k % per) * 32) >> 4;
-          const uint32_t oq = (uint32_t)(part * N * G_::kRowB + (k / per) * N * AT + (k % per) * 32) >> 4;
-          mma<F8>(ts, dk + ok_, dq + oq, kIdS, (part | k) != 0);
-        }
+        for (int u = 0; u < G_::kSub; ++u)
+          mma_steps<F8, AT / 32, 2, 2>(ts, dk + (uint32_t)(u * kKeys * AT >> 4),
+                                       dq + (uint32_t)((part * N * G_::kRowB + u * N * AT) >> 4), kIdS, (part | u) != 0);
       commit(bar(kBSFull + (gg & 1)));
       commit(bar(kBKEmpty + gg % NK));
+      }
       __syncwarp();
       return true;
     };
     auto next_item = [&](int jj) -> bool {
       if (!take(jj, it)) return false;
-      return !it.live || mbar_wait_warp(bar(kBQFull + (jj & 1)), (jj >> 1) & 1, p.err);
+      return it.s < 0 || wait_bar(bar(kBQFull + (jj & 1)), (jj >> 1) & 1);
     };
     bool ok = next_item(0);
-    if (ok && it.live) ok = issue_s(0, 0);
-    while (ok && it.live && !aborted()) {
+    if (ok && it.s >= 0) ok = issue_s(0, 0);
+    while (ok && it.s >= 0) {
       const int nt = tiles_of(it), ob = j & 1;
       for (int t = 0; t < nt && ok; ++t, ++g) {
         if (t + 1 < nt) {
           ok = issue_s(g + 1, j & 1);
         } else {
-          commit(bar(kBQEmpty + (j & 1)));
+          if (elect_one()) commit(bar(kBQEmpty + (j & 1)));
           __syncwarp();
           ok = next_item(j + 1);
-          if (ok && it.live) ok = issue_s(g + 1, (j + 1) & 1);
+          if (ok && it.s >= 0) ok = issue_s(g + 1, (j + 1) & 1);
         }
-        ok = ok && mbar_wait_warp(bar(kBPFull), g & 1, p.err) &&
-             mbar_wait_warp(bar(kBVFull + g % NV), (g / NV) & 1, p.err) &&
-             (t > 0 || mbar_wait_warp(bar(kBOFree + ob), ((j >> 1) & 1) ^ 1, p.err));
+        ok = ok && wait_bar(bar(kBVFull + g % NV), (g / NV) & 1) &&
+             (t > 0 || wait_bar(bar(kBOFree + ob), ((j >> 1) & 1) ^ 1)) &&
+             wait_bar(bar(kBPFull), g & 1);
         if (!ok) break;
         fence_after();
-        const uint32_t to = tmem + G_::kColO + ob * G_::kOCols;
         // V^T: d contiguous, 8 keys = 8 AT bytes, sub-tiles kKeys AT apart.  With
         // D = 64 the M side's upper 64 rows repeat shifted keys; their lanes
         // are never read.
-        const uint64_t dv = sdesc(sV + (g % NV) * G_::kTileB, G_::kSub * AT / G_::kEs >= 128 && G_::kSub > 1 ? kKeys * AT : 8 * AT,
-                                  8 * AT, AT);
-        const uint64_t dp = sdesc(sP, G_::kPB, 1024, 128);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int k = 0; k < kKeys / G_::kKeyStep; ++k) {
-            const uint32_t ov = (uint32_t)(k * G_::kKeyStep * AT) >> 4;
-            const uint32_t op = (uint32_t)(part * G_::kPB + k * G_::kKeyStep * 128) >> 4;
-            const uint32_t acc = F8 ? (t > 0 || k > 0) : (t > 0 || k > 0 || part > 0);
-            mma<F8>(to + (F8 ? part * N : 0), dv + ov, dp + op, kIdO, acc);
-          }
-        commit(bar(kBVEmpty + g % NV));
+        constexpr int KS = G_::kKeyStep;
+        const uint64_t dv = sdesc(sV + (g % NV) * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
+        const uint64_t dp = sdesc(sP, kKeys * 128, 1024, 128);
+        const uint32_t to = tmem + G_::kColO + ob * G_::kOCols;
+        if (elect_one()) {
+        mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv, dp, kIdO, t > 0);
+        if constexpr (!F8) mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv + 4 * KS * AT / 16, dp + 4 * KS * 8, kIdO, 1);
         commit(bar(kBODone));
+        commit(bar(kBVEmpty + g % NV));
+        if (t + 1 == nt) commit(bar(kBOFull + ob));
+        }
         __syncwarp();
       }
       ++j;
     }
     if (!ok) *abort_flag = 1;
     // every MMA issued so far is finished before TMEM is freed
-    commit(bar(kBDrain));
+    if (elect_one()) commit(bar(kBDrain));
     __syncwarp();
-    mbar_wait_warp(bar(kBDrain), 0, p.err);
-  } else if (warp < 4) {
+    wait_bar(bar(kBDrain), 0);
+  } else if (warp == 2) {
     // ======================= query rows =======================
-    constexpr int kLanes = D / 8;            // lanes of a row (8 bf16 elements each)
-    constexpr int kPer = 32 / kLanes;        // rows per step of a warp
-    constexpr int kStepsQ = N / (2 * kPer);  // steps of a warp
-    constexpr int kBatch = kStepsQ < 8 ? kStepsQ : 8;
-    const int w = warp - 2, ch = lane % kLanes, rr = lane / kLanes;
+    constexpr int kLanes = D / 8;          // lanes of a row (8 bf16 elements each)
+    constexpr int kPer = 32 / kLanes;      // rows per step
+    constexpr int kStepsQ = N / kPer;
+    constexpr int kBatch = kStepsQ < (F8 ? 4 : 8) ? kStepsQ : (F8 ? 4 : 8);
+    const int ch = lane % kLanes, rr = lane / kLanes;
     bool ok = true;
     for (int j = 0;; ++j) {
       Item it;
-      ok = take(j, it) && !aborted();
-      if (!ok || !it.live) break;
-      const int qb = j & 1;
+      ok = take(j, it);
+      if (!ok || it.s < 0) break;
+      const int qb = j & 1, rows = it.q_s * G;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
       bool waited = false;
 #pragma unroll 1
-      for (int b = 0; b < kStepsQ && ok; b += kBatch) {
+      for (int b = 0; b < kStepsQ; b += kBatch) {
         uint4 x[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const int r = it.r0 + ((b + k) * 2 + w) * kPer + rr;
+          const int r = it.r0 + (b + k) * kPer + rr;
           x[k] = make_uint4(0, 0, 0, 0);
-          if (r < it.rows) {
-            const int i = r / G;
+          if (r < rows) {
+            const int i = quot(r, a.by_g);
             x[k] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(it.t0 + i) * p.q_st +
                                                         (int64_t)(it.h * G + r - i * G) * p.q_sh) + ch);
           }
         }
         if (!waited) {
-          ok = mbar_wait_warp(bar(kBQEmpty + qb), ((j >> 1) & 1) ^ 1, p.err);
+          ok = wait_bar(bar(kBQEmpty + qb), ((j >> 1) & 1) ^ 1);
           if (!ok) break;
           waited = true;
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const int r = ((b + k) * 2 + w) * kPer + rr;  // row of the tile
+          const int r = (b + k) * kPer + rr;  // row of the tile
           const uint32_t dst = sQ + qb * G_::kQB;
           if constexpr (!F8) {
             st_s128(dst + (ch * 16 / AT) * N * AT + swz<AT>(r, ch % (AT / 16)), x[k].x, x[k].y, x[k].z, x[k].w);
@@ -657,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               nan |= __shfl_xor_sync(0xffffffffu, nan, o);
             }
-            // 2^e <= largest < 2^(e + 1); e is kept where 2^(7 - e) is a normal number
+            // 2^e2 <= largest < 2^(e2 + 1); e2 stays where 2^(7 - e2) is a normal number
             int e2 = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
             e2 = e2 < -100 ? -100 : e2;
             const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
@@ -681,8 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t at = swz<AT>(r, ch >> 1) + (ch & 1) * 8;
             st_s64(dst + at, hi[0], hi[1]);
             st_s64(dst + N * G_::kRowB + at, lo[0], lo[1]);
-            if (ch == 0)
-              qscale[(j % 4) * 64 + r] = nan ? __uint_as_float(0x7fffffffu) : down * p.qk_scale_log2;
+            if (ch == 0) qscale[(j % 4) * 64 + r] = nan ? __uint_as_float(0x7fffffffu) : down * p.qk_scale_log2;
           }
         }
       }
@@ -695,383 +849,373 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok) *abort_flag = 1;
-  } else {
+  } else if (warp < 12) {
     // ======================= softmax =======================
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int w8 = warp - 4;
-    const int tg = quarter * 32 + lane;  // thread of the half's group; also this lane's key in a tile, and its d of O^T
+    const int tg = quarter * 32 + lane;  // thread of the half's group: this lane's key in a tile
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    constexpr float kTau = F8 ? 4.5f : 10.f;     // p may pass 2^0 by this much before the reference moves
-    constexpr float kUp = F8 ? 4.f : 0.f;        // e4m3: p is kept times 2^4
-    volatile int* vote = reinterpret_cast<volatile int*>(misc + 8 * kSVote) + 2 * half;
-    volatile int* poison = reinterpret_cast<volatile int*>(misc + 8 * kSPoison);  // [3]
+    // p may pass 2^0 (e4m3: 2^kUp, times which p is kept) by 2^kTau before a
+    // row's reference moves.  bf16 parts keep their precision over the whole
+    // exponent range, so the first reference is 0 unless the row's largest
+    // score lies beyond +-kTau; e4m3 parts want the largest p near 2^kUp.
+    constexpr float kTau = F8 ? 4.5f : 60.f;
+    constexpr float kUp = F8 ? 4.f : 0.f;
     float* xh = xch + half * 128;
-    int gs = 0, as = 0;  // group / whole synchronisations so far
-    auto group_sync = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBGroup + half));
-      const bool r = mbar_wait_warp(bar(kBGroup + half), gs & 1, p.err);
-      ++gs;
-      return r;
+    float* rh = refs + half * 32;
+    // A synchronisation of the half's four warps that also tells, to all of
+    // them alike, whether any wants the careful path (kCareful) or saw the
+    // abort flag (kLeave: all four leave after it).  The barrier counts
+    // threads: lane 0 of a warp stands for its wish, the others for the flag.
+    // A warp that gives up joins one more vote, and so does every warp at the
+    // end of the items: no warp is left waiting.
+    enum : int { kGo = 0, kCareful = 1, kLeave = 2 };
+    auto vote = [&](bool want, bool leave) -> int {
+      const bool stand = lane == 0 ? want : leave || *abort_flag != 0;
+      uint32_t n;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, %1, 128, p;\n\t}"
+          : "=r"(n)
+          : "r"(1 + half), "r"(stand ? 1 : 0)
+          : "memory");
+      return n > 4 ? kLeave : n > 0 ? kCareful : kGo;
     };
-    auto all_sync = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBAll));
-      const bool r = mbar_wait_warp(bar(kBAll), as & 1, p.err);
-      ++as;
-      return r;
-    };
-    auto fmax_op = [](float x, float y) { return fmaxf(x, y); };
-    auto add_op = [](float x, float y) { return x + y; };
+    if (tg < NC) rh[tg] = kUp;
     int g = 0;
-    bool ok = true;
-    float ref[NC], l[NC];
-    // the item whose O is still to be written
-    bool pend = false;
-    Item pi{};
-    int pj = 0;
-
-    // Writes O / l of item pj: lane = d, register = row.
-    auto epilogue = [&]() {
-      pend = false;
-      fence_after();
-      const uint32_t to = tmem + G_::kColO + (pj & 1) * G_::kOCols + lane_off + half * NC;
-      uint32_t o[NC];
-      tm_ld(to, o);
-      float v[NC];
-      if constexpr (F8) {
-        uint32_t o2[NC];
-        tm_ld(to + N, o2);
-        wait_ld();
-#pragma unroll
-        for (int c = 0; c < NC; ++c) v[c] = fmaf(__uint_as_float(o2[c]), 0.0625f, __uint_as_float(o[c]));
-      } else {
-        wait_ld();
-#pragma unroll
-        for (int c = 0; c < NC; ++c) v[c] = __uint_as_float(o[c]);
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBOFree + (pj & 1)));
-      if (tg >= D) return;
-      const float* li = linv + (pj % 3) * 64 + half * NC;
-      const int ra = pi.r0 + half * NC;  // first row of this half
-      if (poison[pj % 3] == pj + 1) {
-        // a drafted value is not finite: it was taken out of the product and
-        // goes to the rows that see its key
-        for (int k = max(pi.ctx, pi.k0); k < pi.k1; ++k) {
-          const int lb = k / p.bs;
-          const int32_t b = __ldg(p.bt + (int64_t)pi.s * p.bt_stride + lb);
-          if ((uint32_t)b >= (uint64_t)p.num_blocks) continue;
-          const int64_t at = (((int64_t)b * p.bs + (k - lb * p.bs)) * Hkv + pi.h) * D + tg;
-          float x;
-          if constexpr (F8) {
-            const uint32_t hf = e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v_cache)[at]);
-            x = __half2float(__ushort_as_half(static_cast<unsigned short>(hf & 0xffffu)));
-          } else {
-            x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
-          }
-          if (fabsf(x) < INFINITY) continue;
-          const int jj = k - pi.ctx;
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            const int r = ra + c;
-            if (r >= pi.rows) break;
-            if ((static_cast<uint32_t>(__ldg(p.mask + (int64_t)(pi.t0 + r / G) * p.mask_stride + (jj >> 5))) >> (jj & 31)) & 1u) {
-#pragma unroll
-              for (int e = 0; e < NC; ++e)
-                if (e == c) v[e] += x;
-            }
-          }
-        }
-      }
-      if (ra >= pi.rows) return;
-      int i = ra / G, gq = ra - i * G;
-      if (pi.nchunks == 1) {
-        int64_t at = (int64_t)(pi.t0 + i) * p.o_st + (int64_t)(pi.h * G + gq) * p.o_sh + tg;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          if (ra + c >= pi.rows) break;
-          const float s = li[c];
-          const float y = s == 0.f ? 0.f : v[c] * s;
-          if (a.out_bf16)
-            store1(static_cast<__nv_bfloat16*>(p.out) + at, y);
-          else
-            store1(static_cast<float*>(p.out) + at, y);
-          at += p.o_sh;
-          if (++gq == G) {
-            gq = 0;
-            at += p.o_st - (int64_t)G * p.o_sh;
-          }
-        }
-      } else {
-        int64_t at = (((int64_t)pi.s * a.rows_per_seq + (int64_t)i * pi.nchunks + pi.c) * p.Hq + pi.h * G + gq) * D + tg;
-        const int64_t wrap = ((int64_t)pi.nchunks * p.Hq - G) * D;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          if (ra + c >= pi.rows) break;
-          const float s = li[c];
-          a.part_o[at] = s == 0.f ? 0.f : v[c] * s;
-          at += D;
-          if (++gq == G) {
-            gq = 0;
-            at += wrap;
-          }
-        }
-      }
-    };
-
-    for (int j = 0;; ++j) {
+    bool ok = true, joined = vote(false, false) == kLeave;  // joined: left together with the group
+    for (int j = 0; !joined; ++j) {
       Item it;
-      ok = take(j, it) && !aborted();
-      if (!ok || !it.live) break;
-      const int nt = tiles_of(it);
+      if (!wait_bar(bar(kBItemFull + j % kItemSlots), (j / kItemSlots) & 1)) { ok = false; break; }
+      it = items[j % kItemSlots];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBItemEmpty + j % kItemSlots));
+      if (it.s < 0) break;
+      const int nt = tiles_of(it), rows = it.q_s * G, ctx = it.n - it.q_s;
+      const int ra = it.r0 + half * NC;  // first row of this half
       const float* qs = qscale + (j % 4) * 64 + half * NC;
       if (F8) {
-        ok = mbar_wait_warp(bar(kBQsFull + j % 4), (j >> 2) & 1, p.err);
+        ok = wait_bar(bar(kBQsFull + j % 4), (j >> 2) & 1);
         if (!ok) break;
       }
+      unsigned long long l2[NC / 2];  // the rows' sums over this lane's keys, in pairs
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        ref[c] = -INFINITY;
-        l[c] = 0.f;
-      }
-      const int ra = it.r0 + half * NC;
-      bool virgin = true;  // some row has not seen a key yet
+      for (int c = 0; c < NC / 2; ++c) l2[c] = 0ull;
+      uint32_t vmask = 0;  // rows of the half without a reference yet (stored as 0), after the first tile
       for (int t = 0; t < nt; ++t, ++g) {
-        ok = mbar_wait_warp(bar(kBSFull + (g & 1)), (g >> 1) & 1, p.err) &&
-             mbar_wait_warp(bar(kBInfo + g % kInfoSlots), (g / kInfoSlots) & 1, p.err);
+        ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1) &&
+             wait_bar(bar(kBInfo + g % kInfoSlots), (g / kInfoSlots) & 1);
         if (!ok) break;
         fence_after();
-        float x[NC];
-        {
-          uint32_t u[NC];
-          tm_ld(tmem + (g & 1) * N + half * NC + lane_off, u);
-          const uint32_t* bw = info + (g % kInfoSlots) * 4;
-          const uint32_t bad0 = bw[0], bad1 = bw[1], bad2 = bw[2], bad3 = bw[3];
-          wait_ld();
-#pragma unroll
-          for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(u[c]) * (F8 ? qs[c] : p.qk_scale_log2);
-          const int kt = it.k0 + t * kKeys;  // first key of the tile
-          const bool any_bad = (bad0 | bad1 | bad2 | bad3) != 0;
-          const bool masked = kt + kKeys > it.ctx || any_bad;
-          bool slow = t == 0 || masked || virgin;
-          if (masked) {
-            const int key = kt + tg, jj = key - it.ctx;
-            const uint32_t badw = quarter == 0 ? bad0 : quarter == 1 ? bad1 : quarter == 2 ? bad2 : bad3;
-            const bool in = key < it.k1 && !((badw >> lane) & 1u);
-            int i = ra / G, gq = ra - i * G;
-            const int32_t* mrow = p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj > 0 ? jj >> 5 : 0);
-#pragma unroll
+        uint32_t u[NC];  // q.k of the stored values
+        tm_ld(tmem + (g & 1) * N + half * NC + lane_off, u);
+        const uint4 bad = *reinterpret_cast<const uint4*>(info + (g % kInfoSlots) * 4);
+        wait_ld();
+        const int kt = it.k0 + t * kKeys;  // first key of the tile
+        const bool masked = kt + kKeys > ctx || (bad.x | bad.y | bad.z | bad.w) != 0;
+        uint32_t see = 0xffffffffu;  // rows that see this lane's key
+        if (masked) {
+          const int key = kt + tg, jj = key - ctx;
+          const uint32_t badw = quarter == 0 ? bad.x : quarter == 1 ? bad.y : quarter == 2 ? bad.z : bad.w;
+          if (key >= it.k1 || ((badw >> lane) & 1u)) {
+            see = 0;
+          } else if (jj >= 0) {
+            see = 0;
+            const int i = quot(ra, a.by_g);
+            int gq = ra - i * G;
+            const int32_t* m = p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj >> 5);
+#pragma unroll 4
             for (int c = 0; c < NC; ++c) {
-              bool see = in && ra + c < it.rows;
-              if (see && jj >= 0) see = (static_cast<uint32_t>(__ldg(mrow)) >> (jj & 31)) & 1u;
-              x[c] = see ? x[c] : -INFINITY;
+              if (ra + c < rows) see |= ((static_cast<uint32_t>(__ldg(m)) >> (jj & 31)) & 1u) << c;
               if (++gq == G) {
                 gq = 0;
-                mrow += p.mask_stride;
+                m += p.mask_stride;
               }
             }
-            // V rows that some row of the product must not see: zero what is
-            // past the sequence or has no page, and what is not finite among
-            // the drafted rows (the epilogue hands that on)
-            if (!mbar_wait_warp(bar(kBVFull + g % NV), (g / NV) & 1, p.err)) { ok = false; break; }
-            constexpr int kLn = G_::kRowB / 16, kRs = 32 / kLn;
-            const int ch = lane % kLn, rr = lane / kLn;
-            bool found = false;
-            for (int b = 0; b < 16; b += kRs) {
-              const int kk = w8 * 16 + b + rr;
-              const int ky = kt + kk;
-              const uint32_t bm = kk < 32 ? bad0 : kk < 64 ? bad1 : kk < 96 ? bad2 : bad3;
-              const bool gone = ky >= it.k1 || ((bm >> (kk & 31)) & 1u);
-              if (!gone && ky < it.ctx) continue;
-              const uint32_t at = sV + (g % NV) * G_::kTileB + (ch * 16 / AT) * kKeys * AT + swz<AT>(kk, ch % (AT / 16));
-              if (gone) {
-                st_s128(at, 0, 0, 0, 0);
-                continue;
-              }
-              uint32_t w[4];
+          }
+          // V rows that must not reach a row that does not see them: zero what
+          // is past the sequence or has no page, and what is not finite among
+          // the drafted rows (the rows that see those get it at the end)
+          if (!wait_bar(bar(kBVFull + g % NV), (g / NV) & 1)) { ok = false; break; }
+          constexpr int kLn = G_::kRowB / 16, kRs = 32 / kLn;
+          const int ch = lane % kLn, rr = lane / kLn;
+          bool found = false;
+#pragma unroll 1
+          for (int b = 0; b < 16; b += kRs) {
+            const int kk = (warp - 4) * 16 + b + rr, ky = kt + kk;
+            const uint32_t bm = kk < 32 ? bad.x : kk < 64 ? bad.y : kk < 96 ? bad.z : bad.w;
+            const bool gone = ky >= it.k1 || ((bm >> (kk & 31)) & 1u);
+            if (!gone && ky < ctx) continue;
+            const uint32_t at = sV + (g % NV) * G_::kTileB + (ch * 16 / AT) * kKeys * AT + swz<AT>(kk, ch % (AT / 16));
+            uint32_t w[4] = {0, 0, 0, 0};
+            bool hit = gone;
+            if (!gone) {
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-              bool hit = false;
+              constexpr uint32_t kExp = F8 ? 0x7fu : 0x7f80u, kAll = F8 ? 0xffu : 0xffffu;
+              constexpr int kBits = F8 ? 8 : 16;
+#pragma unroll 1
+              for (int f = 0; f < 32; f += kBits)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (F8) {
-#pragma unroll
-                  for (int f = 0; f < 4; ++f)
-                    if (((w[e] >> (8 * f)) & 0x7fu) == 0x7fu) {
-                      w[e] &= ~(0xffu << (8 * f));
-                      hit = true;
-                    }
-                } else {
-#pragma unroll
-                  for (int f = 0; f < 2; ++f)
-                    if (((w[e] >> (16 * f)) & 0x7f80u) == 0x7f80u) {
-                      w[e] &= ~(0xffffu << (16 * f));
-                      hit = true;
-                    }
-                }
-              }
-              if (hit) {
-                st_s128(at, w[0], w[1], w[2], w[3]);
-                found = true;
-              }
+                for (int e = 0; e < 4; ++e)
+                  if (((w[e] >> f) & kExp) == kExp) {
+                    w[e] &= ~(kAll << f);
+                    hit = true;
+                  }
+              found = found || hit;
             }
-            if (found) poison[j % 3] = j + 1;
-            fence_proxy_async_smem();
-            if (!all_sync()) { ok = false; break; }
+            if (hit) st_s128(at, w[0], w[1], w[2], w[3]);
           }
-          if (!slow) {
-            float top = -INFINITY;
+          if (found) poison[j % 3] = j + 1;
+        }
+        // y = score in base 2 less the row's reference, plus kUp
+        float y[NC];
+        for (bool again = false;; again = true) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) top = fmaxf(top, x[c] - ref[c]);
-            if (__any_sync(0xffffffffu, top > kTau)) vote[gs & 1] = gs + 1;
-            const int tag = gs + 1, vb = gs & 1;
-            if (!group_sync()) { ok = false; break; }
-            slow = vote[vb] == tag;
-          }
-          if (slow) {
-            float m[NC];
-#pragma unroll
-            for (int c = 0; c < NC; ++c) m[c] = x[c] == x[c] ? x[c] : -INFINITY;
-            const float mine = col_reduce<NC>(m, lane, fmax_op);
-            if (lane % (32 / NC) == 0) xh[quarter * 32 + lane / (32 / NC)] = mine;
-            if (!group_sync()) { ok = false; break; }
-            // move the references that were passed; O (every P V so far has
-            // run after this wait) and the sums follow, eight rows at a time
-            if (t > 0) {
-              if (!mbar_wait_warp(bar(kBODone), (g - 1) & 1, p.err)) { ok = false; break; }
-              fence_after();
+          for (int c = 0; c < NC; c += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(rh + c);
+            unsigned long long s01, s23;
+            if constexpr (F8) {
+              const float4 q = *reinterpret_cast<const float4*>(qs + c);
+              s01 = pk2(q.x, q.y);
+              s23 = pk2(q.z, q.w);
+            } else {
+              s01 = s23 = pk2(p.qk_scale_log2, p.qk_scale_log2);
             }
-            virgin = false;
+            up2(fma2(pk2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), s01, pk2(r.x, r.y)), y[c], y[c + 1]);
+            up2(fma2(pk2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])), s23, pk2(r.z, r.w)), y[c + 2], y[c + 3]);
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) y[c] = (see >> c) & 1u ? y[c] : -INFINITY;
+          }
+          if (again) break;
+          if (!masked && !(F8 && t == 0) && vmask == 0) {
+            float top = fmaxf(y[0], y[1]);
+#pragma unroll
+            for (int c = 2; c < NC; c += 2) top = fmax3(top, y[c], y[c + 1]);
+            bool want = top > kTau + kUp;
+            if (!F8 && t == 0) {
+              float low = fminf(y[0], y[1]);
+#pragma unroll
+              for (int c = 2; c < NC; c += 2) low = fmin3(low, y[c], y[c + 1]);
+              want = want || !(low >= -kTau);
+            }
+            const int v = vote(__any_sync(0xffffffffu, want), false);
+            if (v == kLeave) { ok = false; joined = true; break; }
+            if (v == kGo) break;
+          }
+          // ---- the careful path: the rows' largest y over the tile
+          float mine = 0.f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float m = redux_max(y[c]);  // NaN is passed over
+            mine = lane == c ? m : mine;
+          }
+          if (lane < NC) xh[quarter * 32 + lane] = mine;
+          if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+          // lane c: row c's new reference; the stored value is kUp - reference
+          float alpha = 1.f, nref = 0.f;
+          bool moved = false, none = false;
+          if (lane < NC) {
+            const float top = fmaxf(fmaxf(xh[lane], xh[32 + lane]), fmaxf(xh[64 + lane], xh[96 + lane]));
+            const float old = rh[lane];
+            nref = old;
+            if (t == 0 || ((vmask >> lane) & 1u)) {  // nothing summed so far, the reference is 0
+              none = top == -INFINITY;
+              if (!none && (F8 || fabsf(top) > kTau)) nref = old + kUp - top;
+            } else if (top > kTau + kUp) {
+              nref = old + kUp - top;
+              alpha = ex2(kUp - top);
+              moved = true;
+            }
+          }
+          vmask = __ballot_sync(0xffffffffu, none);
+          const bool any = __any_sync(0xffffffffu, moved);
+          // every warp has read the references
+          if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+          if (quarter == 0 && lane < NC) rh[lane] = nref;
+          if (any) {  // the same in the half's four warps
+#pragma unroll
+            for (int c = 0; c < NC; c += 2)
+              l2[c / 2] = mul2(l2[c / 2], pk2(__shfl_sync(0xffffffffu, alpha, c), __shfl_sync(0xffffffffu, alpha, c + 1)));
+            // t > 0: every P V so far has run after this wait
+            if (!wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
+            fence_after();
             const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + half * NC;
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < NC; b += 8) {
-              float al[8];
-              bool moved = false;  // the same in all warps of the half
+              uint32_t o[8], o2[8];
+              tm_ld(to + b, o);
+              tm_ld(to + N + b, o2);
+              wait_ld();
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                const float mx = fmaxf(fmaxf(xh[b + c], xh[32 + b + c]), fmaxf(xh[64 + b + c], xh[96 + b + c]));
-                float& rf = ref[b + c];
-                const bool need = mx > rf + kTau || (rf == -INFINITY && mx > -INFINITY);
-                const float nr = need ? mx : rf;
-                al[c] = need ? ex2(rf - nr) : 1.f;
-                moved = moved || need;
-                rf = nr;
-                virgin = virgin || nr == -INFINITY;
-                l[b + c] *= al[c];
+                const float f = __shfl_sync(0xffffffffu, alpha, b + c);
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                o2[c] = __float_as_uint(__uint_as_float(o2[c]) * f);
               }
-              if (t > 0 && moved) {
-#pragma unroll
-                for (int part = 0; part < (F8 ? 2 : 1); ++part) {
-                  uint32_t o[8];
-                  tm_ld(to + part * N + b, o);
-                  wait_ld();
-#pragma unroll
-                  for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
-                  tm_st(to + part * N + b, o);
-                }
-              }
+              tm_st(to + b, o);
+              tm_st(to + N + b, o2);
             }
             wait_st();
-            // xh is written again only after another synchronisation of the group
-            if (!group_sync()) { ok = false; break; }
           }
+          // the references are written
+          if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
         }
-        // P = 2^(s - ref), in two parts, to shared memory: row = key
+        if (!ok) break;
+        // P = 2^y in two parts, row = key, hi in columns 0 .. N - 1, lo in N .. 2 N - 1
         uint32_t hi[F8 ? NC / 4 : NC / 2], lo[F8 ? NC / 4 : NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float r0 = ref[c] == -INFINITY ? 0.f : ref[c], r1 = ref[c + 1] == -INFINITY ? 0.f : ref[c + 1];
-          const float p0 = ex2(x[c] - r0 + kUp), p1 = ex2(x[c + 1] - r1 + kUp);
-          l[c] += p0;
-          l[c + 1] += p1;
+          const float p0 = ex2(y[c]), p1 = ex2(y[c + 1]);
+          const unsigned long long pp = pk2(p0, p1);
+          l2[c / 2] = add2(l2[c / 2], pp);
           if constexpr (F8) {
-            const uint16_t h2 = f32x2_to_e4m3x2(p0, p1);
-            const uint32_t hf = e4m3x2_to_f16x2(h2);
-            const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-            const uint16_t l2 = f32x2_to_e4m3x2((p0 - hv.x) * 16.f, (p1 - hv.y) * 16.f);
+            // through f16 (11 bits, two values at a time): hi its e4m3 code, lo
+            // that of 16 times the exact remainder
+            const __half2 h = __floats2half2_rn(p0, p1);
+            const uint16_t h2 = f16x2_to_e4m3x2(h);
+            const uint32_t hb = e4m3x2_to_f16x2(h2);
+            const uint16_t l8 = f16x2_to_e4m3x2(__hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hb)), __float2half2_rn(16.f)));
             if (c & 2) {
               hi[c / 4] |= (uint32_t)h2 << 16;
-              lo[c / 4] |= (uint32_t)l2 << 16;
+              lo[c / 4] |= (uint32_t)l8 << 16;
             } else {
               hi[c / 4] = h2;
-              lo[c / 4] = l2;
+              lo[c / 4] = l8;
             }
           } else {
             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
             hi[c / 2] = __byte_perm(u0, u1, 0x7632);
-            lo[c / 2] = __byte_perm(__float_as_uint(p0 - __uint_as_float(u0 & 0xFFFF0000u)),
-                                    __float_as_uint(p1 - __uint_as_float(u1 & 0xFFFF0000u)), 0x7632);
+            float r0, r1;  // p - hi exactly: the truncated-away low bits
+            up2(sub2(pp, pk2(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))), r0, r1);
+            lo[c / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
           }
         }
         // the buffer is free once P V of the previous tile has run
-        if (g > 0 && !mbar_wait_warp(bar(kBODone), (g - 1) & 1, p.err)) { ok = false; break; }
-        if constexpr (F8) {
-          if constexpr (NC == 8) {
-            st_s64(sP + swz<128>(tg, 0) + half * 8, hi[0], hi[1]);
-            st_s64(sP + G_::kPB + swz<128>(tg, 0) + half * 8, lo[0], lo[1]);
+        if (g > 0 && !wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
+        auto put = [&](const uint32_t* x, int col) {  // NC columns of this key's row, from column col
+          const int at = col * G_::kEs;               // byte in the row
+          const uint32_t base = sP + (at >> 7) * (kKeys * 128) + 0u;
+          if constexpr (NC * G_::kEs == 8) {
+            st_s64(base + swz<128>(tg, (at & 127) >> 4) + (at & 8), x[0], x[1]);
           } else {
 #pragma unroll
-            for (int c = 0; c < NC / 16; ++c) {
-              const uint32_t at = sP + swz<128>(tg, half * (NC / 16) + c);
-              st_s128(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              st_s128(at + G_::kPB, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-            }
+            for (int q = 0; q < NC * G_::kEs / 16; ++q)
+              st_s128(base + swz<128>(tg, ((at & 127) >> 4) + q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < NC / 8; ++c) {
-            const uint32_t at = sP + swz<128>(tg, half * (NC / 8) + c);
-            st_s128(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-            st_s128(at + G_::kPB, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-          }
-        }
+        };
+        put(hi, half * NC);
+        put(lo, N + half * NC);
         fence_proxy_async_smem();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBPFull));
-        if (t == 0 && pend) epilogue();  // the previous item's last P V was waited for above
       }
       if (!ok) break;
       // the rows' sums over the lanes and the four warps of the half
       {
         float m[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) m[c] = l[c];
-        const float mine = col_reduce<NC>(m, lane, add_op);
+        for (int c = 0; c < NC; c += 2) up2(l2[c / 2], m[c], m[c + 1]);
+        const float mine = col_sum<NC>(m, lane);
         if (lane % (32 / NC) == 0) xh[quarter * 32 + lane / (32 / NC)] = mine;
-        if (!group_sync()) { ok = false; break; }
+        if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
         if (tg < NC) {
           const float s = (xh[tg] + xh[32 + tg]) + (xh[64 + tg] + xh[96 + tg]);
           linv[(j % 3) * 64 + half * NC + tg] = s == 0.f ? 0.f : p.v_scale / s;
-          float rf = 0.f;
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (c == tg) rf = ref[c];
           const int r = ra + tg;
-          if (it.nchunks > 1 && r < it.rows) {
-            const int i = r / G;
+          if (it.nchunks > 1 && r < rows) {
+            const int i = quot(r, a.by_g);
             a.part_lse[((int64_t)it.s * a.rows_per_seq + (int64_t)i * it.nchunks + it.c) * p.Hq + it.h * G + r - i * G] =
-                s == 0.f ? -INFINITY : rf + log2f(s) - kUp;
+                s == 0.f ? -INFINITY : __log2f(s) - rh[tg];  // reference + log2(sum) - kUp
+          }
+          rh[tg] = kUp;  // the next item's rows start at reference 0
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBLFull + j % 3));
+        // xh and the references have been read
+        if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (!joined) vote(false, !ok);
+  } else {
+    // ======================= O / l: lane = d, register = row =======================
+    const int d = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    constexpr float kLo = F8 ? 0.0625f : 1.f;  // the low part's weight
+    constexpr int kCols = N < 16 ? N : 16;     // rows at a time
+    bool ok = true;
+    for (int j = 0;; ++j) {
+      Item it;
+      ok = take(j, it);
+      if (!ok || it.s < 0) break;
+      ok = wait_bar(bar(kBLFull + j % 3), (j / 3) & 1) &&
+           wait_bar(bar(kBOFull + (j & 1)), (j >> 1) & 1);
+      if (!ok) break;
+      fence_after();
+      const int rows = it.q_s * G;
+      const float* li = linv + (j % 3) * 64;
+      const bool split = it.nchunks > 1, wide = split || !a.out_bf16;  // fp32 elements
+      const int i0 = quot(it.r0, a.by_g);
+      int gq = it.r0 - i0 * G;
+      // the first row's element d, the step to the group's next head, and from its last head to the next node
+      char* at;
+      int64_t step, wrap;
+      if (split) {
+        at = reinterpret_cast<char*>(a.part_o + (((int64_t)it.s * a.rows_per_seq + (int64_t)i0 * it.nchunks + it.c) * p.Hq +
+                                                 it.h * G + gq) * D + d);
+        step = D;
+        wrap = ((int64_t)it.nchunks * p.Hq - G) * D;
+      } else {
+        at = static_cast<char*>(p.out) +
+             ((int64_t)(it.t0 + i0) * p.o_st + (int64_t)(it.h * G + gq) * p.o_sh + d) * (wide ? 4 : 2);
+        step = p.o_sh;
+        wrap = p.o_st - (int64_t)G * p.o_sh;
+      }
+      step *= wide ? 4 : 2;
+      wrap *= wide ? 4 : 2;
+      char* const at0 = at;
+      const int count = min(N, rows - it.r0);
+#pragma unroll 1
+      for (int b = 0; b < N; b += kCols) {
+        const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + b;
+        uint32_t o[kCols], o2[kCols];
+        tm_ld(to, o);
+        tm_ld(to + N, o2);
+        wait_ld();
+        if (b + kCols == N) {  // the accumulator has been read
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBOFree + (j & 1)));
+        }
+        if (D == 128 || d < D) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            if (b + c < count) {
+              const float s = li[b + c];
+              const float v = fmaf(__uint_as_float(o2[c]), kLo, __uint_as_float(o[c])) * s;
+              const float y = s == 0.f ? 0.f : v;
+              if (wide)
+                *reinterpret_cast<float*>(at) = y;
+              else
+                *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
+              at += step;
+              if (++gq == G) {
+                gq = 0;
+                at += wrap;
+              }
+            }
           }
         }
-        if (!group_sync()) { ok = false; break; }
       }
-      pend = true;
-      pi = it;
-      pj = j;
-    }
-    if (ok && pend) {
-      if (mbar_wait_warp(bar(kBODone), (g - 1) & 1, p.err))
-        epilogue();
-      else
-        ok = false;
+      if (poison[j % 3] == j + 1 && (D == 128 || d < D)) add_poison<D, F8>(a, it, d, at0, step, wrap, wide, count);
     }
     if (!ok) *abort_flag = 1;
   }
   // ---- teardown
   fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrWaitTimeout);
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
@@ -1213,6 +1357,8 @@ cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t m
   TcArgs a{};
   a.p = p;
   a.out_bf16 = out_kind;
+  a.by_g = fast_div(static_cast<uint32_t>(p.G));
+  a.by_bs = fast_div(static_cast<uint32_t>(p.bs));
   const int64_t rps = tree_tc_rows_per_seq(max_q, max_ctx);
   a.rows_per_seq = static_cast<int32_t>(rps);
   a.part_o = static_cast<float*>(workspace);
