@@ -36,15 +36,14 @@
 // smallest codes' step is 2^-17 of the row's reference.
 //
 // CTA: 16 warps.
-//   warp 0      finds the items and publishes each one ahead; copies K tiles
-//               of 128 keys by TMA: boxes of 16 or 8 slots that lie in one
-//               block, or, for other block sizes, four arbitrary rows at a time
-//               (tile::gather4).
+//   warps 0, 3  copy the K and the V tiles of 128 keys by TMA: boxes of 16 or 8
+//               slots that lie in one block, or, for other block sizes, four
+//               arbitrary rows at a time (tile::gather4).
 //   warp 1      issues the MMAs: S of tile g + 1, then P V of tile g.  The two
 //               parts of P are 2 N columns of one operand, so O holds their two
 //               products side by side and P V costs one pass of instructions.
-//   warp 2      query rows: bf16 to the swizzled operand layout, or split to e4m3.
-//   warp 3      copies V tiles.
+//   warp 2      finds the items, publishes them and brings their query rows:
+//               bf16 to the swizzled operand layout, or split to e4m3.
 //   warps 4-11  softmax: lane quarter w % 4 = keys, half (w - 4) / 4 = rows.
 //   warps 12-15 write O / l of finished items while the next one runs.
 #include <cuda.h>
@@ -91,13 +90,16 @@ struct Geo {
   static constexpr int kQB = N * kRowB * kParts;
   static constexpr int kPRow = 2 * N * kEs;                   // both parts of P of one key
   static constexpr int kPB = kKeys * (kPRow <= 128 ? 128 : 256);  // [1 or 2][128 keys][128 bytes]
+  // two P buffers, so that no tile waits for the P V before it (an S commit
+  // covers the P V issued before that S); one where shared memory is short
+  static constexpr int kPBufs = kPRow == 256 && kTileB == 32768 ? 1 : 2;
   static constexpr int kNK = kTileB == 32768 ? 2 : kTileB == 16384 ? 4 : 6;
   static constexpr int kNV = kTileB == 32768 ? 3 : kTileB == 16384 ? 5 : 6;
   static constexpr int kNC = N / 2;                           // rows (columns of S^T) per softmax warp
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kNK * kTileB;
   static constexpr int kOffP = kOffV + kNV * kTileB;
-  static constexpr int kOffQ = kOffP + kPB;
+  static constexpr int kOffQ = kOffP + kPBufs * kPB;
   static constexpr int kOffMisc = kOffQ + 2 * kQB;
   static constexpr int kSmem = kOffMisc + (F8 ? 4096 : 3072);
   // tensor memory: S 2 x N columns, then O 2 x (hi N, lo N)
@@ -109,19 +111,20 @@ struct Geo {
   static_assert(kColO + 2 * kOCols <= 512, "tensor memory");
 };
 
-struct Item {
-  int s, h, r0;         // sequence (-1: no more items), KV head, first row of the tile
+struct alignas(16) Item {
+  int s, h, r0;         // sequence, KV head, first row of the tile
   int t0, q_s, n;       // first packed row, nodes, keys
   int k0, k1;           // keys of the chunk
   int c, nchunks;       // its index, chunks of the sequence
+  int nt, pad;          // key tiles (0: no more items)
 };
 
 // barrier area
 enum : int {
-  kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26, kBODone = 27, kBOFull = 28,
+  kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26 /* 2 */, kBOFull = 28,
   kBOFree = 30, kBQFull = 32, kBQEmpty = 34, kBQsFull = 36, kBLFull = 40, kBItemFull = 43, kBItemEmpty = 49,
-  kBInfo = 55, kBDrain = 63, kSTmem = 64, kSAbort = 65, kSPoison = 66 /* [3] ints: 66, 67 */,
-  kOffItems = 576, kOffInfo = 816, kOffXch = 944, kOffLinv = 1968, kOffRef = 2736, kOffQs = 2992,
+  kBODone = 55, kBDrain = 56, kSTmem = 57, kSAbort = 58, kSPoison = 59 /* [3] ints: 59, 60 */,
+  kOffItems = 496, kOffInfo = 784, kOffXch = 912, kOffLinv = 1936, kOffRef = 2704, kOffQs = 2960,
 };
 static_assert(kOffItems + kItemSlots * (int)sizeof(Item) <= kOffInfo, "item ring");
 
@@ -210,11 +213,12 @@ __device__ __forceinline__ uint64_t l2_normal_policy() {
   return pol;
 }
 
-// Wait by a whole warp, at most 2^20 tries (tens of milliseconds and more; a
-// try suspends the warp for a while).  The code is kept short, here and below:
-// with the roles' code well past a hundred KB the instruction caches, not the
-// pipes, set the pace.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+// A bounded wait, at most 2^20 tries (tens of milliseconds and more; a try
+// suspends the warp for a while), and the same by a whole warp.  The code is
+// kept short, here and below: sixteen warps in six roles share the SM's
+// instruction cache, and while the roles' code did not fit (105 to 166 KB in
+// all, 42 % of its requests missed) it set the pace, not the pipes.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
@@ -224,8 +228,22 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
-  return __all_sync(0xffffffffu, ok != 0);
+  return ok != 0;
 }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, poll(bar, parity));
+}
+// A place in a ring of n slots, and the parity of its pass.
+struct Ring {
+  int at = 0;
+  uint32_t pass = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      pass ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -354,12 +372,10 @@ struct TcArgs {
 // A drafted value (element d of some V row) is not finite: the softmax warps
 // took it out of the product, and here it goes to the rows that see its key,
 // on top of what this thread has just stored.
-template <int D, bool F8>
-__device__ __noinline__ void add_poison(const TcArgs& a, const Item& it, int d, char* at, int64_t step, int64_t wrap,
-                                        bool wide, int count) {
+template <int D, int N, bool F8>
+__device__ __noinline__ void add_poison(const TcArgs& a, const Item& it, int d) {
   const TreeParams& p = a.p;
-  const int i0 = it.r0 / p.G, g0 = it.r0 - i0 * p.G;
-  const int ctx = it.n - it.q_s;
+  const int ctx = it.n - it.q_s, rows = it.q_s * p.G;
   for (int k = max(ctx, it.k0); k < it.k1; ++k) {
     const int lb = k / p.bs, jj = k - ctx;
     const int32_t blk = __ldg(p.bt + (int64_t)it.s * p.bt_stride + lb);
@@ -373,19 +389,19 @@ __device__ __noinline__ void add_poison(const TcArgs& a, const Item& it, int d, 
       x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[va]);
     }
     if (fabsf(x) < INFINITY) continue;
-    char* y = at;
-    for (int c = 0, i = i0, g = g0; c < count; ++c) {
-      if ((static_cast<uint32_t>(__ldg(p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj >> 5))) >> (jj & 31)) & 1u) {
-        if (wide)
-          *reinterpret_cast<float*>(y) += x;
-        else
-          *reinterpret_cast<__nv_bfloat16*>(y) = __float2bfloat16_rn(__bfloat162float(*reinterpret_cast<__nv_bfloat16*>(y)) + x);
-      }
-      y += step;
-      if (++g == p.G) {
-        g = 0;
-        ++i;
-        y += wrap;
+    for (int r = it.r0; r < rows && r < it.r0 + N; ++r) {
+      const int i = r / p.G, hq = it.h * p.G + r - i * p.G;
+      if (!((static_cast<uint32_t>(__ldg(p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj >> 5))) >> (jj & 31)) & 1u)) continue;
+      if (it.nchunks > 1) {
+        a.part_o[(((int64_t)it.s * a.rows_per_seq + (int64_t)i * it.nchunks + it.c) * p.Hq + hq) * D + d] += x;
+      } else {
+        const int64_t at = (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh + d;
+        if (a.out_bf16) {
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + at;
+          *y = __float2bfloat16_rn(__bfloat162float(*y) + x);
+        } else {
+          static_cast<float*>(p.out)[at] += x;
+        }
       }
     }
   }
@@ -430,21 +446,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBSFull + i), 1);
+      mbar_init(bar(kBSFull + i), 2);
       mbar_init(bar(kBOFull + i), 1);
       mbar_init(bar(kBOFree + i), 4);
       mbar_init(bar(kBQFull + i), 1);
       mbar_init(bar(kBQEmpty + i), 1);
     }
     for (int i = 0; i < 3; ++i) mbar_init(bar(kBLFull + i), 8);
-    mbar_init(bar(kBPFull), 8);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kBPFull + i), 8);
     mbar_init(bar(kBODone), 1);
     for (int i = 0; i < 4; ++i) mbar_init(bar(kBQsFull + i), 1);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(bar(kBItemFull + i), 1);
       mbar_init(bar(kBItemEmpty + i), 15);  // every warp but the first
     }
-    for (int i = 0; i < kInfoSlots; ++i) mbar_init(bar(kBInfo + i), 1);
     mbar_init(bar(kBDrain), 1);
     *abort_flag = 0;
     for (int i = 0; i < 3; ++i) poison[i] = 0;
@@ -463,21 +478,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   launch_dependents();
 
-  // item j as the other warps take it
-  auto take = [&](int j, Item& it) -> bool {
-    if (!wait_bar(bar(kBItemFull + j % kItemSlots), (j / kItemSlots) & 1)) return false;
-    it = items[j % kItemSlots];
+  // the next item, as every warp but the finder takes it
+  auto take = [&](Ring& r, Item& it) -> bool {
+    if (!wait_bar(bar(kBItemFull) + 8 * r.at, r.pass)) return false;
+    const int4* q = reinterpret_cast<const int4*>(items + r.at);
+    *reinterpret_cast<int4*>(&it) = q[0];
+    *(reinterpret_cast<int4*>(&it) + 1) = q[1];
+    *(reinterpret_cast<int4*>(&it) + 2) = q[2];
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kBItemEmpty + j % kItemSlots));
+    if (lane == 0) mbar_arrive(bar(kBItemEmpty) + 8 * r.at);
+    r.next(kItemSlots);
     return !aborted();
   };
-  auto tiles_of = [](const Item& it) { return (it.k1 - it.k0 + kKeys - 1) / kKeys; };
 
   // ---- copies of K or V tiles: pages, slots, TMA
   const int bx = a.box;
   const int n_box = bx ? kKeys / bx : 32;
   const int key_of = bx ? (lane % n_box) * bx : lane * 4;  // first key of this lane's box (or four keys)
-  const int sub_of = bx ? lane / n_box : 0;                // its sub-tile
   constexpr int32_t kPast = INT32_MIN;
   // pages of this lane's keys in a tile
   auto pages = [&](const Item& it, int t, int32_t (&blk)[4]) {
@@ -490,12 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         blk[e] = __ldg(row + quot(k + e, a.by_bs));
     }
   };
-  // copies the tile into dst; returns the lane's keys whose page is out of range
-  auto load_tile = [&](const Item& it, int t, const int32_t (&blk)[4], uint32_t dst, const CUtensorMap* map, uint32_t full,
-                       uint64_t pol) -> uint32_t {
+  // slots of this lane's keys (-1: none); returns those whose page is out of range
+  auto slots = [&](const Item& it, int t, const int32_t (&blk)[4], int (&sl)[4]) -> uint32_t {
     const int k = it.k0 + t * kKeys + key_of;
     uint32_t bad = 0;
-    int sl[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       sl[e] = -1;
@@ -506,249 +521,182 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad |= 1u << e;
       }
     }
+    return bad;
+  };
+  // Copies a tile into dst.  The copies are issued by one elected lane, each
+  // box's slot handed over by a shuffle: the instruction takes its operands
+  // from uniform registers, and lanes that issue one copy each are served one
+  // after the other at about 150 clocks (2,450 for a bf16 tile's 16 boxes).
+  auto load_tile = [&](int h, const int (&sl)[4], uint32_t dst, const CUtensorMap* map, uint32_t full, uint64_t pol) {
     if (lane == 0) mbar_arrive_expect_tx(full, G_::kTileB);
     __syncwarp();
     if (bx) {
       // past the sequence, or a page out of range: out of bounds, which TMA fills with zeros
-      if (sub_of < G_::kSub)
-        tma_box(dst + sub_of * kKeys * AT + key_of * AT, map, sub_of * (AT / G_::kEs), it.h,
-                sl[0] >= 0 ? sl[0] : (int)(p.num_blocks * p.bs), full, pol);
-    } else {
-      int r[4];
+      const int mine = sl[0] >= 0 ? sl[0] : (int)(p.num_blocks * p.bs);
+#pragma unroll 1
+      for (int b = 0; b < n_box; b += 8) {
+        int s8[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = sl[e] >= 0 ? sl[e] * Hkv + it.h : it.h;  // any row: the softmax drops it
+        for (int k = 0; k < 8; ++k) s8[k] = __shfl_sync(0xffffffffu, mine, b + k);
+        if (elect_one()) {
 #pragma unroll
-      for (int u = 0; u < G_::kSub; ++u)
-        tma_gather4(dst + u * kKeys * AT + key_of * AT, map, u * (AT / G_::kEs), r, full, pol);
-    }
-    return bad;
-  };
-  // K and V are read once where one tile of rows holds them all
-  const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_normal_policy();
-  auto policy = [&](const Item& it) { return it.q_s * G <= N ? pol_once : pol_keep; };
-
-  if (warp == 0) {
-    // ======================= items, K tiles =======================
-    int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
-    int c0 = 0, q_s = 0, n = 0, chunk = 1, nchunks = 0, rts = 0;
-    int cnt = 0, incl = 0, base = 0, total = 0;  // items: this sequence's, prefix in the group; before it; in it
-    auto load_group = [&]() {
-      const int s = gb + lane;
-      cnt = 0;
-      if (s < p.B) {
-        c0 = __ldg(p.cu_q + s);
-        const int c1 = __ldg(p.cu_q + s + 1);
-        n = __ldg(p.seq_lens + s);
-        q_s = c1 - c0;
-        const bool bad = c0 < 0 || c1 < c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs ||
-                         q_s > p.max_nodes;
-        if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-        if (!bad && q_s > 0) {
-          chunk = tree_chunk(n, q_s);
-          nchunks = (n - 1) / chunk + 1;
-          rts = (q_s * G - 1) / N + 1;
-          cnt = nchunks * Hkv * rts;
-        }
-      }
-      incl = cnt;
+          for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      total = __shfl_sync(0xffffffffu, incl, 31);
-    };
-    load_group();
-    // item number x of the call, or s = -1 past the last
-    auto find = [&](int x) -> Item {
-      Item it{};
-      it.s = -1;
-      while (x - base >= total) {
-        base += total;
-        total = 0;
-        gb += 32;
-        if (gb >= p.B) return it;
-        load_group();
-      }
-      const int o = __ffs(__ballot_sync(0xffffffffu, incl > x - base)) - 1;
-      int y = x - base - __shfl_sync(0xffffffffu, incl - cnt, o);
-      it.s = gb + o;
-      it.t0 = __shfl_sync(0xffffffffu, c0, o);
-      it.q_s = __shfl_sync(0xffffffffu, q_s, o);
-      it.n = __shfl_sync(0xffffffffu, n, o);
-      it.nchunks = __shfl_sync(0xffffffffu, nchunks, o);
-      const int rt_n = __shfl_sync(0xffffffffu, rts, o), len = __shfl_sync(0xffffffffu, chunk, o);
-      it.r0 = (y % rt_n) * N;
-      y /= rt_n;
-      it.h = y % Hkv;
-      it.c = y / Hkv;
-      it.k0 = it.c * len;
-      it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
-      return it;
-    };
-    auto publish = [&](int j, const Item& it) -> bool {
-      if (!wait_bar(bar(kBItemEmpty + j % kItemSlots), ((j / kItemSlots) & 1) ^ 1)) return false;
-      if (lane == 0) {
-        items[j % kItemSlots] = it;
-        mbar_arrive(bar(kBItemFull + j % kItemSlots));
-      }
-      __syncwarp();
-      return true;
-    };
-    // The walk: (it, t) is the tile to load, blk its pages.  Each step finds
-    // the tile after it and starts that one's page loads; at an item's first
-    // tile the item after it is found and published, so that its query rows
-    // load under this item.
-    int j = 0, g = 0, t = 0, nt = 0;
-    Item it{}, next{};
-    it.s = next.s = -1;
-    int32_t blk[4] = {kPast, kPast, kPast, kPast};
-    bool ok = true;
-    for (;;) {
-      if (t == nt) {  // the item is done (or none was begun): go to the next
-        it = next;
-        nt = tiles_of(it);
-        t = 0;
-        if (j > 0 && it.s < 0) break;
-        next = find(blockIdx.x + j * (int)gridDim.x);
-        ok = publish(j, next) && !aborted();
-        if (!ok) break;
-        ++j;
-        if (j == 1) {
-          nt = 0;
-          if (next.s >= 0) pages(next, 0, blk);
-          continue;
-        }
-      }
-      const bool last = t + 1 == nt;
-      int32_t nb[4] = {kPast, kPast, kPast, kPast};
-      if (!last || next.s >= 0) pages(last ? next : it, last ? 0 : t + 1, nb);
-      ok = wait_bar(bar(kBKEmpty + g % NK), ((g / NK) & 1) ^ 1);
-      if (!ok) break;
-      const uint32_t bad = load_tile(it, t, blk, sK + (g % NK) * G_::kTileB, &tm_k, bar(kBKFull + g % NK), policy(it));
-      // the tile's keys without a page, for the softmax
-      uint32_t* w = info + (g % kInfoSlots) * 4;
-      if (lane < 4) w[lane] = 0;
-      __syncwarp();
-      if (__any_sync(0xffffffffu, bad != 0)) {
-        if (bad) {
-          atomicOr(p.err, kErrBlockRange);
-          if (!bx) {
-            atomicOr(w + key_of / 32, bad << (key_of & 31));
-          } else if (sub_of == 0) {
-            atomicOr(w + key_of / 32, (bx == 16 ? 0xffffu : 0xffu) << (key_of & 31));
-          }
+            for (int u = 0; u < G_::kSub; ++u)
+              tma_box(dst + u * kKeys * AT + (b + k) * bx * AT, map, u * (AT / G_::kEs), h, s8[k], full, pol);
         }
         __syncwarp();
       }
-      if (lane == 0) mbar_arrive(bar(kBInfo + g % kInfoSlots));
+    } else {
+      int r[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) blk[e] = nb[e];
-      ++t;
-      ++g;
+      for (int e = 0; e < 4; ++e) r[e] = sl[e] >= 0 ? sl[e] * Hkv + h : h;  // any row: the softmax drops it
+#pragma unroll 1
+      for (int b = 0; b < 32; ++b) {
+        int q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = __shfl_sync(0xffffffffu, r[e], b);
+        if (elect_one()) {
+#pragma unroll
+          for (int u = 0; u < G_::kSub; ++u)
+            tma_gather4(dst + u * kKeys * AT + b * 4 * AT, map, u * (AT / G_::kEs), q, full, pol);
+        }
+        __syncwarp();
+      }
+    }
+  };
+  // K and V are read once where one tile of rows holds them all
+  const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_normal_policy();
+
+  if (warp == 0 || warp == 3) {
+    // ======================= K tiles, V tiles =======================
+    const bool is_v = warp == 3;
+    const CUtensorMap* const map = is_v ? &tm_v : &tm_k;
+    const uint32_t tiles = is_v ? sV : sK, full = bar(is_v ? kBVFull : kBKFull), empty = bar(is_v ? kBVEmpty : kBKEmpty);
+    const int ns = is_v ? NV : NK;
+    Ring ir, r;
+    int g = 0;
+    bool ok = true;
+    for (;;) {
+      Item it;
+      ok = take(ir, it);
+      if (!ok || it.nt == 0) break;
+      const uint64_t pol = it.q_s * G <= N ? pol_once : pol_keep;
+      int32_t blk[4], nb[4];
+      pages(it, 0, blk);
+      for (int t = 0; t < it.nt; ++t, ++g) {
+        pages(it, t + 1, nb);  // past the chunk: none
+        ok = wait_bar(empty + 8 * r.at, r.pass ^ 1);
+        if (!ok) break;
+        int sl[4];
+        const uint32_t bad = slots(it, t, blk, sl);
+        if (!is_v) {
+          // the tile's keys without a page, for the softmax (before the arrival
+          // on the tile's barrier, which hands them on)
+          uint32_t* w = info + (g % kInfoSlots) * 4;
+          if (lane < 4) w[lane] = 0;
+          __syncwarp();
+          if (__any_sync(0xffffffffu, bad != 0)) {
+            if (bad) {
+              atomicOr(p.err, kErrBlockRange);
+              if (!bx) {
+                atomicOr(w + key_of / 32, bad << (key_of & 31));
+              } else if (lane < n_box) {
+                atomicOr(w + key_of / 32, (bx == 16 ? 0xffffu : 0xffu) << (key_of & 31));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        load_tile(it.h, sl, tiles + r.at * G_::kTileB, map, full + 8 * r.at, pol);
+        r.next(ns);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) blk[e] = nb[e];
+      }
+      if (!ok) break;
     }
     if (!ok) *abort_flag = 1;
     if (aborted())  // let the copies issued so far land before the CTA exits
-      for (int k = g - 1; k >= 0 && k >= g - NK; --k) wait_bar(bar(kBKFull + k % NK), (k / NK) & 1);
-  } else if (warp == 3) {
-    // ======================= V tiles =======================
-    int j = 0, g = 0, t = 0, nt = 0;
-    Item it{}, next{};
-    it.s = next.s = -1;
-    int32_t blk[4] = {kPast, kPast, kPast, kPast};
-    bool ok = true;
-    for (;;) {  // as warp 0's walk
-      if (t == nt) {
-        it = next;
-        nt = tiles_of(it);
-        t = 0;
-        if (j > 0 && it.s < 0) break;
-        ok = take(j, next);
-        if (!ok) break;
-        ++j;
-        if (j == 1) {
-          nt = 0;
-          if (next.s >= 0) pages(next, 0, blk);
-          continue;
+      for (int k = 0; k < ns && k < g; ++k) {
+        if (r.at-- == 0) {
+          r.at = ns - 1;
+          r.pass ^= 1;
         }
+        wait_bar(full + 8 * r.at, r.pass);
       }
-      const bool last = t + 1 == nt;
-      int32_t nb[4] = {kPast, kPast, kPast, kPast};
-      if (!last || next.s >= 0) pages(last ? next : it, last ? 0 : t + 1, nb);
-      ok = wait_bar(bar(kBVEmpty + g % NV), ((g / NV) & 1) ^ 1);
-      if (!ok) break;
-      load_tile(it, t, blk, sV + (g % NV) * G_::kTileB, &tm_v, bar(kBVFull + g % NV), policy(it));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) blk[e] = nb[e];
-      ++t;
-      ++g;
-    }
-    if (!ok) *abort_flag = 1;
-    if (aborted())
-      for (int k = g - 1; k >= 0 && k >= g - NV; --k) wait_bar(bar(kBVFull + k % NV), (k / NV) & 1);
   } else if (warp == 1) {
     // ======================= MMA =======================
     constexpr uint32_t kIdS = idesc(N, F8, false, false), kIdO = idesc(2 * N, F8, true, true);
-    Item it;
-    int j = 0, g = 0;
+    Ring ir, kr, vr;
+    int j = 0, g = 0, nt = 0;
+    // S of tile gg from the next K tile
     auto issue_s = [&](int gg, int qb) -> bool {
-      if (!wait_bar(bar(kBKFull + gg % NK), (gg / NK) & 1)) return false;
+      if (!wait_bar(bar(kBKFull) + 8 * kr.at, kr.pass)) return false;
       fence_after();
-      const uint64_t dk = sdesc(sK + (gg % NK) * G_::kTileB, 16, 8 * AT, AT);
+      const uint64_t dk = sdesc(sK + kr.at * G_::kTileB, 16, 8 * AT, AT);
       const uint64_t dq = sdesc(sQ + qb * G_::kQB, 16, 8 * AT, AT);
       const uint32_t ts = tmem + (gg & 1) * N;
       if (elect_one()) {
 #pragma unroll
-      for (int part = 0; part < G_::kParts; ++part)
+        for (int part = 0; part < G_::kParts; ++part)
 #pragma unroll
-        for (int u = 0; u < G_::kSub; ++u)
-          mma_steps<F8, AT / 32, 2, 2>(ts, dk + (uint32_t)(u * kKeys * AT >> 4),
-                                       dq + (uint32_t)((part * N * G_::kRowB + u * N * AT) >> 4), kIdS, (part | u) != 0);
-      commit(bar(kBSFull + (gg & 1)));
-      commit(bar(kBKEmpty + gg % NK));
+          for (int u = 0; u < G_::kSub; ++u)
+            mma_steps<F8, AT / 32, 2, 2>(ts, dk + (uint32_t)(u * kKeys * AT >> 4),
+                                         dq + (uint32_t)((part * N * G_::kRowB + u * N * AT) >> 4), kIdS, (part | u) != 0);
+        commit(bar(kBSFull + (gg & 1)));
+        commit(bar(kBKEmpty) + 8 * kr.at);
+        // the second arrival hands on what the tile's producer wrote (info)
+        mbar_arrive(bar(kBSFull + (gg & 1)));
       }
       __syncwarp();
+      kr.next(NK);
       return true;
     };
-    auto next_item = [&](int jj) -> bool {
-      if (!take(jj, it)) return false;
-      return it.s < 0 || wait_bar(bar(kBQFull + (jj & 1)), (jj >> 1) & 1);
-    };
-    bool ok = next_item(0);
-    if (ok && it.s >= 0) ok = issue_s(0, 0);
-    while (ok && it.s >= 0) {
-      const int nt = tiles_of(it), ob = j & 1;
-      for (int t = 0; t < nt && ok; ++t, ++g) {
-        if (t + 1 < nt) {
-          ok = issue_s(g + 1, j & 1);
-        } else {
-          if (elect_one()) commit(bar(kBQEmpty + (j & 1)));
-          __syncwarp();
-          ok = next_item(j + 1);
-          if (ok && it.s >= 0) ok = issue_s(g + 1, (j + 1) & 1);
-        }
-        ok = ok && wait_bar(bar(kBVFull + g % NV), (g / NV) & 1) &&
-             (t > 0 || wait_bar(bar(kBOFree + ob), ((j >> 1) & 1) ^ 1)) &&
-             wait_bar(bar(kBPFull), g & 1);
+    bool ok = true;
+    for (int t = 0;; ++t, ++g) {  // t: tile of item j - 1, whose S has been issued
+      if (t == nt - 1 && elect_one()) commit(bar(kBQEmpty + (~j & 1)));
+      int nt2 = nt;
+      if (t + 1 >= nt) {  // the tile whose S goes next is the next item's first
+        Item it;
+        ok = take(ir, it);
+        nt2 = it.nt;
+        if (!ok || (nt2 == 0 && nt == 0)) break;
+        ok = nt2 == 0 || wait_bar(bar(kBQFull + (j & 1)), (j >> 1) & 1);
+        if (!ok) break;
+      }
+      const int gs = nt == 0 ? g : g + 1, qb = t + 1 >= nt ? j & 1 : ~j & 1;
+      if (nt2 > 0 || t + 1 < nt) ok = issue_s(gs, qb);
+      if (nt > 0 && ok) {
+        const int ob = ~j & 1;
+        ok = wait_bar(bar(kBVFull) + 8 * vr.at, vr.pass) && (t > 0 || wait_bar(bar(kBOFree + ob), (((j - 1) >> 1) & 1) ^ 1)) &&
+             wait_bar(bar(kBPFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
         fence_after();
         // V^T: d contiguous, 8 keys = 8 AT bytes, sub-tiles kKeys AT apart.  With
         // D = 64 the M side's upper 64 rows repeat shifted keys; their lanes
         // are never read.
         constexpr int KS = G_::kKeyStep;
-        const uint64_t dv = sdesc(sV + (g % NV) * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
-        const uint64_t dp = sdesc(sP, kKeys * 128, 1024, 128);
+        const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
+        const uint64_t dp = sdesc(sP + (G_::kPBufs == 2 ? (g & 1) * G_::kPB : 0), kKeys * 128, 1024, 128);
         const uint32_t to = tmem + G_::kColO + ob * G_::kOCols;
         if (elect_one()) {
-        mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv, dp, kIdO, t > 0);
-        if constexpr (!F8) mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv + 4 * KS * AT / 16, dp + 4 * KS * 8, kIdO, 1);
-        commit(bar(kBODone));
-        commit(bar(kBVEmpty + g % NV));
-        if (t + 1 == nt) commit(bar(kBOFull + ob));
+          mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv, dp, kIdO, t > 0);
+          if constexpr (!F8) mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv + 4 * KS * AT / 16, dp + 4 * KS * 8, kIdO, 1);
+          commit(bar(kBODone));
+          commit(bar(kBVEmpty) + 8 * vr.at);
+          if (t + 1 == nt) commit(bar(kBOFull + ob));
         }
         __syncwarp();
+        vr.next(NV);
       }
-      ++j;
+      if (!ok) break;
+      if (t + 1 >= nt) {
+        if (nt == 0) --g;  // no tile was finished
+        if (nt2 == 0) break;
+        nt = nt2;
+        t = -1;
+        ++j;
+      }
     }
     if (!ok) *abort_flag = 1;
     // every MMA issued so far is finished before TMEM is freed
@@ -756,87 +704,127 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     wait_bar(bar(kBDrain), 0);
   } else if (warp == 2) {
-    // ======================= query rows =======================
+    // ======================= items, query rows =======================
+    int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
+    int c0 = 0, q_s = 0, n = 0, chunk = 1, nchunks = 0, rts = 0;
+    int cnt = 0, incl = 0, base = 0, total = 0;  // items: this sequence's, prefix in the group; before it; in it
     constexpr int kLanes = D / 8;          // lanes of a row (8 bf16 elements each)
     constexpr int kPer = 32 / kLanes;      // rows per step
     constexpr int kStepsQ = N / kPer;
-    constexpr int kBatch = kStepsQ < (F8 ? 4 : 8) ? kStepsQ : (F8 ? 4 : 8);
+    constexpr int kBatch = kStepsQ < 4 ? kStepsQ : 4;
     const int ch = lane % kLanes, rr = lane / kLanes;
+    Ring ir;
     bool ok = true;
-    for (int j = 0;; ++j) {
-      Item it;
-      ok = take(j, it);
-      if (!ok || it.s < 0) break;
+    gb = -32;
+    for (int j = 0, x = blockIdx.x;; ++j, x += gridDim.x) {
+      // item number x of the call
+      while (x - base >= total && gb < p.B) {
+        base += total;
+        gb += 32;
+        const int s = gb + lane;
+        cnt = 0;
+        if (s < p.B) {
+          c0 = __ldg(p.cu_q + s);
+          const int c1 = __ldg(p.cu_q + s + 1);
+          n = __ldg(p.seq_lens + s);
+          q_s = c1 - c0;
+          const bool bad = c0 < 0 || c1 < c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs ||
+                           q_s > p.max_nodes;
+          if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
+          if (!bad && q_s > 0) {
+            chunk = tree_chunk(n, q_s);
+            nchunks = (n - 1) / chunk + 1;
+            rts = (q_s * G - 1) / N + 1;
+            cnt = nchunks * Hkv * rts;
+          }
+        }
+        incl = cnt;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+      }
+      Item it{};
+      if (x - base < total) {
+        const int o = __ffs(__ballot_sync(0xffffffffu, incl > x - base)) - 1;
+        int y = x - base - __shfl_sync(0xffffffffu, incl - cnt, o);
+        it.s = gb + o;
+        it.t0 = __shfl_sync(0xffffffffu, c0, o);
+        it.q_s = __shfl_sync(0xffffffffu, q_s, o);
+        it.n = __shfl_sync(0xffffffffu, n, o);
+        it.nchunks = __shfl_sync(0xffffffffu, nchunks, o);
+        const int rt_n = __shfl_sync(0xffffffffu, rts, o), len = __shfl_sync(0xffffffffu, chunk, o);
+        const int z = y / rt_n;
+        it.r0 = (y - z * rt_n) * N;
+        it.c = z / Hkv;
+        it.h = z - it.c * Hkv;
+        it.k0 = it.c * len;
+        it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
+        it.nt = (it.k1 - it.k0 + kKeys - 1) / kKeys;
+      }
+      ok = wait_bar(bar(kBItemEmpty) + 8 * ir.at, ir.pass ^ 1) && !aborted();
+      if (!ok) break;
+      if (lane == 0) {
+        items[ir.at] = it;
+        mbar_arrive(bar(kBItemFull) + 8 * ir.at);
+      }
+      __syncwarp();
+      ir.next(kItemSlots);
+      if (it.nt == 0) break;
+      // its query rows; the buffer is free once the item two before has its scores
       const int qb = j & 1, rows = it.q_s * G;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-      bool waited = false;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ch * 8;
+      const uint32_t dst = sQ + qb * G_::kQB;
 #pragma unroll 1
       for (int b = 0; b < kStepsQ; b += kBatch) {
-        uint4 x[kBatch];
+        uint4 v[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int r = it.r0 + (b + k) * kPer + rr;
-          x[k] = make_uint4(0, 0, 0, 0);
+          v[k] = make_uint4(0, 0, 0, 0);
           if (r < rows) {
             const int i = quot(r, a.by_g);
-            x[k] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(it.t0 + i) * p.q_st +
-                                                        (int64_t)(it.h * G + r - i * G) * p.q_sh) + ch);
+            v[k] = __ldg(reinterpret_cast<const uint4*>(q + (it.t0 + i) * p.q_st + (it.h * G + r - i * G) * p.q_sh));
           }
         }
-        if (!waited) {
-          ok = wait_bar(bar(kBQEmpty + qb), ((j >> 1) & 1) ^ 1);
-          if (!ok) break;
-          waited = true;
-        }
+        if (b == 0) ok = wait_bar(bar(kBQEmpty + qb), ((j >> 1) & 1) ^ 1);
+        if (!ok) break;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int r = (b + k) * kPer + rr;  // row of the tile
-          const uint32_t dst = sQ + qb * G_::kQB;
           if constexpr (!F8) {
-            st_s128(dst + (ch * 16 / AT) * N * AT + swz<AT>(r, ch % (AT / 16)), x[k].x, x[k].y, x[k].z, x[k].w);
+            st_s128(dst + (ch * 16 / AT) * N * AT + swz<AT>(r, ch % (AT / 16)), v[k].x, v[k].y, v[k].z, v[k].w);
           } else {
-            float f[8];
-            const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            float mx = 0.f;
-            bool fine = true;
+            const uint32_t wd[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            // the row's largest element, as the bits of its absolute value (infinity and NaN on top)
+            uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[2 * e] = bf16_lo(wd[e]);
-              f[2 * e + 1] = bf16_hi(wd[e]);
-              mx = fmaxf(mx, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
-              fine = fine && fabsf(f[2 * e]) < INFINITY && fabsf(f[2 * e + 1]) < INFINITY;
-            }
-            int nan = !fine;
+            for (int e = 0; e < 4; ++e) top = max(top, max(wd[e] & 0x7fffu, (wd[e] >> 16) & 0x7fffu));
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) {
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              nan |= __shfl_xor_sync(0xffffffffu, nan, o);
-            }
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool nan = top >= 0x7f80u;
             // 2^e2 <= largest < 2^(e2 + 1); e2 stays where 2^(7 - e2) is a normal number
-            int e2 = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            e2 = e2 < -100 ? -100 : e2;
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+            const int e2 = max(static_cast<int>(top >> 7) - 127, -100);
+            const float up = nan ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float u0 = nan ? 0.f : f[2 * e] * up, u1 = nan ? 0.f : f[2 * e + 1] * up;
+              const float u0 = bf16_lo(wd[e]) * up, u1 = bf16_hi(wd[e]) * up;
               const uint16_t h2 = f32x2_to_e4m3x2(u0, u1);
               const uint32_t hf = e4m3x2_to_f16x2(h2);
               const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hf));
               const uint16_t l2 = f32x2_to_e4m3x2(u0 - hv.x, u1 - hv.y);
-              if (e & 1) {
-                hi[e >> 1] |= (uint32_t)h2 << 16;
-                lo[e >> 1] |= (uint32_t)l2 << 16;
-              } else {
-                hi[e >> 1] = h2;
-                lo[e >> 1] = l2;
-              }
+              hi[e >> 1] = e & 1 ? hi[e >> 1] | (uint32_t)h2 << 16 : h2;
+              lo[e >> 1] = e & 1 ? lo[e >> 1] | (uint32_t)l2 << 16 : l2;
             }
             const uint32_t at = swz<AT>(r, ch >> 1) + (ch & 1) * 8;
             st_s64(dst + at, hi[0], hi[1]);
             st_s64(dst + N * G_::kRowB + at, lo[0], lo[1]);
-            if (ch == 0) qscale[(j % 4) * 64 + r] = nan ? __uint_as_float(0x7fffffffu) : down * p.qk_scale_log2;
+            if (ch == 0)
+              qscale[(j % 4) * 64 + r] =
+                  nan ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23) * p.qk_scale_log2;
           }
         }
       }
@@ -880,16 +868,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       return n > 4 ? kLeave : n > 0 ? kCareful : kGo;
     };
     if (tg < NC) rh[tg] = kUp;
+    Ring ir;
     int g = 0;
     bool ok = true, joined = vote(false, false) == kLeave;  // joined: left together with the group
     for (int j = 0; !joined; ++j) {
       Item it;
-      if (!wait_bar(bar(kBItemFull + j % kItemSlots), (j / kItemSlots) & 1)) { ok = false; break; }
-      it = items[j % kItemSlots];
+      if (!wait_bar(bar(kBItemFull) + 8 * ir.at, ir.pass)) { ok = false; break; }
+      {
+        const int4* q = reinterpret_cast<const int4*>(items + ir.at);
+        *reinterpret_cast<int4*>(&it) = q[0];
+        *(reinterpret_cast<int4*>(&it) + 1) = q[1];
+        *(reinterpret_cast<int4*>(&it) + 2) = q[2];
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBItemEmpty + j % kItemSlots));
-      if (it.s < 0) break;
-      const int nt = tiles_of(it), rows = it.q_s * G, ctx = it.n - it.q_s;
+      if (lane == 0) mbar_arrive(bar(kBItemEmpty) + 8 * ir.at);
+      ir.next(kItemSlots);
+      if (it.nt == 0) break;
+      const int nt = it.nt, rows = it.q_s * G, ctx = it.n - it.q_s;
       const int ra = it.r0 + half * NC;  // first row of this half
       const float* qs = qscale + (j % 4) * 64 + half * NC;
       if (F8) {
@@ -901,8 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < NC / 2; ++c) l2[c] = 0ull;
       uint32_t vmask = 0;  // rows of the half without a reference yet (stored as 0), after the first tile
       for (int t = 0; t < nt; ++t, ++g) {
-        ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1) &&
-             wait_bar(bar(kBInfo + g % kInfoSlots), (g / kInfoSlots) & 1);
+        ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
         fence_after();
         uint32_t u[NC];  // q.k of the stored values
@@ -1090,11 +1084,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo[c / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
           }
         }
-        // the buffer is free once P V of the previous tile has run
-        if (g > 0 && !wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
+        // the buffer is free once P V of the tile that last used it has run: the
+        // previous one, or, with two buffers, the one before it, which this
+        // tile's S came after
+        if (G_::kPBufs == 1 && g > 0 && !wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
         auto put = [&](const uint32_t* x, int col) {  // NC columns of this key's row, from column col
           const int at = col * G_::kEs;               // byte in the row
-          const uint32_t base = sP + (at >> 7) * (kKeys * 128) + 0u;
+          const uint32_t base = sP + (G_::kPBufs == 2 ? (g & 1) * G_::kPB : 0) + (at >> 7) * (kKeys * 128);
           if constexpr (NC * G_::kEs == 8) {
             st_s64(base + swz<128>(tg, (at & 127) >> 4) + (at & 8), x[0], x[1]);
           } else {
@@ -1108,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBPFull));
+        if (lane == 0) mbar_arrive(bar(kBPFull + (g & 1)));
       }
       if (!ok) break;
       // the rows' sums over the lanes and the four warps of the half
@@ -1143,12 +1139,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int d = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     constexpr float kLo = F8 ? 0.0625f : 1.f;  // the low part's weight
-    constexpr int kCols = N < 16 ? N : 16;     // rows at a time
+    constexpr int kCols = 16;            // rows at a time
+    constexpr int kOff = (N + 31) / 32;  // row offsets held by a lane
+    Ring ir;
     bool ok = true;
     for (int j = 0;; ++j) {
       Item it;
-      ok = take(j, it);
-      if (!ok || it.s < 0) break;
+      ok = take(ir, it);
+      if (!ok || it.nt == 0) break;
       ok = wait_bar(bar(kBLFull + j % 3), (j / 3) & 1) &&
            wait_bar(bar(kBOFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
@@ -1156,59 +1154,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = it.q_s * G;
       const float* li = linv + (j % 3) * 64;
       const bool split = it.nchunks > 1, wide = split || !a.out_bf16;  // fp32 elements
-      const int i0 = quot(it.r0, a.by_g);
-      int gq = it.r0 - i0 * G;
-      // the first row's element d, the step to the group's next head, and from its last head to the next node
-      char* at;
-      int64_t step, wrap;
-      if (split) {
-        at = reinterpret_cast<char*>(a.part_o + (((int64_t)it.s * a.rows_per_seq + (int64_t)i0 * it.nchunks + it.c) * p.Hq +
-                                                 it.h * G + gq) * D + d);
-        step = D;
-        wrap = ((int64_t)it.nchunks * p.Hq - G) * D;
-      } else {
-        at = static_cast<char*>(p.out) +
-             ((int64_t)(it.t0 + i0) * p.o_st + (int64_t)(it.h * G + gq) * p.o_sh + d) * (wide ? 4 : 2);
-        step = p.o_sh;
-        wrap = p.o_st - (int64_t)G * p.o_sh;
+      // lane c (and c + 32): where row c's element 0 goes, in bytes from `to_base`; -1: no row
+      const int esz = wide ? 4 : 2;
+      const int64_t node = split ? (int64_t)it.nchunks * p.Hq * D : p.o_st, head = split ? D : p.o_sh;
+      char* const to_base = (split ? reinterpret_cast<char*>(a.part_o + ((int64_t)it.s * a.rows_per_seq + it.c) * p.Hq * D)
+                                   : static_cast<char*>(p.out) + it.t0 * p.o_st * esz) + it.h * G * head * esz;
+      long long off[kOff];
+#pragma unroll
+      for (int k = 0; k < kOff; ++k) {
+        const int r = it.r0 + lane + 32 * k, i = quot(r, a.by_g);
+        off[k] = lane + 32 * k < N && r < rows ? (i * node + (r - i * G) * head) * esz : -1;
       }
-      step *= wide ? 4 : 2;
-      wrap *= wide ? 4 : 2;
-      char* const at0 = at;
-      const int count = min(N, rows - it.r0);
+      char* const mine = to_base + d * esz;
 #pragma unroll 1
       for (int b = 0; b < N; b += kCols) {
         const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + b;
         uint32_t o[kCols], o2[kCols];
         tm_ld(to, o);
         tm_ld(to + N, o2);
+        float v[kCols];
         wait_ld();
         if (b + kCols == N) {  // the accumulator has been read
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBOFree + (j & 1)));
         }
-        if (D == 128 || d < D) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            if (b + c < count) {
-              const float s = li[b + c];
-              const float v = fmaf(__uint_as_float(o2[c]), kLo, __uint_as_float(o[c])) * s;
-              const float y = s == 0.f ? 0.f : v;
-              if (wide)
-                *reinterpret_cast<float*>(at) = y;
-              else
-                *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
-              at += step;
-              if (++gq == G) {
-                gq = 0;
-                at += wrap;
-              }
-            }
+        for (int c = 0; c < kCols; c += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(li + b + c);
+          const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = fmaf(__uint_as_float(o2[c + e]), kLo, __uint_as_float(o[c + e])) * sc[e];
+            v[c + e] = sc[e] == 0.f ? 0.f : x;
+          }
+        }
+        long long at[kCols];
+        const long long from = kOff > 1 && b >= 32 ? off[kOff - 1] : off[0];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) at[c] = __shfl_sync(0xffffffffu, from, (b & 31) + c);
+        if (D == 128 || d < D) {
+          if (wide) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+              if (at[c] >= 0) *reinterpret_cast<float*>(mine + at[c]) = v[c];
+          } else {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+              if (at[c] >= 0) *reinterpret_cast<__nv_bfloat16*>(mine + at[c]) = __float2bfloat16_rn(v[c]);
           }
         }
       }
-      if (poison[j % 3] == j + 1 && (D == 128 || d < D)) add_poison<D, F8>(a, it, d, at0, step, wrap, wide, count);
+      if (poison[j % 3] == j + 1 && (D == 128 || d < D)) add_poison<D, N, F8>(a, it, d);
     }
     if (!ok) *abort_flag = 1;
   }
