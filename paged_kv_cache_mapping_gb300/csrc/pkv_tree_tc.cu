@@ -79,6 +79,7 @@ __host__ __device__ inline int tree_chunk(int n, int q_s) {
 }
 
 // ---------------------------------------------------------------- geometry
+constexpr int kMiscBytes = 6656;
 template <int D, int N, bool F8>
 struct Geo {
   static constexpr int kEs = F8 ? 1 : 2;
@@ -94,14 +95,15 @@ struct Geo {
   // covers the P V issued before that S); one where shared memory is short
   static constexpr int kPBufs = kPRow == 256 && kTileB == 32768 ? 1 : 2;
   static constexpr int kNK = kTileB == 32768 ? 2 : kTileB == 16384 ? 4 : 6;
-  static constexpr int kNV = kTileB == 32768 ? 3 : kTileB == 16384 ? 5 : 6;
+  static constexpr int kNV = kTileB == 32768 ? 3 : kTileB == 16384 ? (kPRow == 256 ? 4 : 5) : 6;
   static constexpr int kNC = N / 2;                           // rows (columns of S^T) per softmax warp
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kNK * kTileB;
   static constexpr int kOffP = kOffV + kNV * kTileB;
   static constexpr int kOffQ = kOffP + kPBufs * kPB;
-  static constexpr int kOffMisc = kOffQ + 2 * kQB;
-  static constexpr int kSmem = kOffMisc + (F8 ? 4096 : 3072);
+  static constexpr int kQBufs = kPBufs;  // query tiles: the next item's arrives while this one runs
+  static constexpr int kOffMisc = kOffQ + kQBufs * kQB;
+  static constexpr int kSmem = kOffMisc + kMiscBytes;
   // tensor memory: S 2 x N columns, then O 2 x (hi N, lo N)
   static constexpr uint32_t kColO = 2 * N;
   static constexpr uint32_t kOCols = 2 * N;
@@ -122,10 +124,12 @@ struct alignas(16) Item {
 // barrier area
 enum : int {
   kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26 /* 2 */, kBOFull = 28,
-  kBOFree = 30, kBQFull = 32, kBQEmpty = 34, kBQsFull = 36, kBLFull = 40, kBItemFull = 43, kBItemEmpty = 49,
-  kBODone = 55, kBDrain = 56, kSTmem = 57, kSAbort = 58, kSPoison = 59 /* [3] ints: 59, 60 */,
-  kOffItems = 496, kOffInfo = 784, kOffXch = 912, kOffLinv = 1936, kOffRef = 2704, kOffQs = 2960,
+  kBOFree = 30, kBQFull = 32, kBQEmpty = 34, kBQsFull = 36, kBLFull = 40, kBLEmpty = 42, kBItemFull = 44,
+  kBItemEmpty = 50, kBODone = 56, kBDrain = 57, kSTmem = 58, kSAbort = 59, kSPoison = 60 /* [3] ints: 60, 61 */,
+  kOffItems = 496, kOffInfo = 784, kOffXch = 912 /* [2][4][32] */, kOffSum = 1936 /* [2][4][64] */,
+  kOffLref = 3984 /* [2][64] */, kOffRef = 4496 /* [3][64] */, kOffQs = 5264 /* e4m3: [4][64] */, kOffUnset = 6288,
 };
+static_assert(kOffUnset + 32 <= kMiscBytes, "shared memory");
 static_assert(kOffItems + kItemSlots * (int)sizeof(Item) <= kOffInfo, "item ring");
 
 // ---------------------------------------------------------------- PTX
@@ -425,10 +429,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item* items = reinterpret_cast<Item*>(misc + kOffItems);
   uint32_t* info = reinterpret_cast<uint32_t*>(misc + kOffInfo);  // [kInfoSlots][4]: keys without a page
   float* xch = reinterpret_cast<float*>(misc + kOffXch);          // [2 halves][4 quarters][32]
-  float* linv = reinterpret_cast<float*>(misc + kOffLinv);        // [3][64]
-  float* refs = reinterpret_cast<float*>(misc + kOffRef);         // [64]
+  float* sums = reinterpret_cast<float*>(misc + kOffSum);         // [2][4 quarters][64]: rows' sums of p
+  float* lref = reinterpret_cast<float*>(misc + kOffLref);        // [2][64]: their references, as kept
+  float* refs = reinterpret_cast<float*>(misc + kOffRef);         // [3][64]
+  volatile uint32_t* unset4 = reinterpret_cast<volatile uint32_t*>(misc + kOffUnset);  // [2 halves][4 quarters]
   float* qscale = reinterpret_cast<float*>(misc + kOffQs);        // e4m3: [4][64]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the shuffle tells the compiler that the warp index, and so the branch to a
+  // role, is the same for the whole warp: else every warp-wide instruction
+  // inside is compiled for a diverged warp
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0); };
   const int G = p.G, Hkv = p.Hkv;
 
@@ -452,7 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBQFull + i), 1);
       mbar_init(bar(kBQEmpty + i), 1);
     }
-    for (int i = 0; i < 3; ++i) mbar_init(bar(kBLFull + i), 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBLFull + i), 8);
+      mbar_init(bar(kBLEmpty + i), 4);
+    }
     for (int i = 0; i < 2; ++i) mbar_init(bar(kBPFull + i), 8);
     mbar_init(bar(kBODone), 1);
     for (int i = 0; i < 4; ++i) mbar_init(bar(kBQsFull + i), 1);
@@ -478,6 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   launch_dependents();
 
+  // item j's query buffer, and the parity of its pass
+  auto qbuf = [](int j) { return G_::kQBufs == 2 ? j & 1 : 0; };
+  auto qpass = [](int j) { return (uint32_t)(G_::kQBufs == 2 ? j >> 1 : j) & 1u; };
   // the next item, as every warp but the finder takes it
   auto take = [&](Ring& r, Item& it) -> bool {
     if (!wait_bar(bar(kBItemFull) + 8 * r.at, r.pass)) return false;
@@ -496,32 +511,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_box = bx ? kKeys / bx : 32;
   const int key_of = bx ? (lane % n_box) * bx : lane * 4;  // first key of this lane's box (or four keys)
   constexpr int32_t kPast = INT32_MIN;
-  // pages of this lane's keys in a tile
+  // pages of this lane's keys in a tile (one box's, or four keys')
   auto pages = [&](const Item& it, int t, int32_t (&blk)[4]) {
     const int32_t* row = p.bt + (int64_t)it.s * p.bt_stride;
     const int k = it.k0 + t * kKeys + key_of;
+    if (bx) {
+      blk[0] = k < it.k1 ? __ldg(row + quot(k, a.by_bs)) : kPast;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      blk[e] = kPast;
-      if ((e == 0 || !bx) && k + e < it.k1)
-        blk[e] = __ldg(row + quot(k + e, a.by_bs));
+      for (int e = 0; e < 4; ++e) blk[e] = k + e < it.k1 ? __ldg(row + quot(k + e, a.by_bs)) : kPast;
     }
   };
   // slots of this lane's keys (-1: none); returns those whose page is out of range
   auto slots = [&](const Item& it, int t, const int32_t (&blk)[4], int (&sl)[4]) -> uint32_t {
     const int k = it.k0 + t * kKeys + key_of;
-    uint32_t bad = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sl[e] = -1;
-      if (e > 0 && bx) continue;
-      if ((uint32_t)blk[e] < (uint64_t)p.num_blocks) {
-        sl[e] = (blk[e] - quot(k + e, a.by_bs)) * p.bs + k + e;
-      } else if (blk[e] != kPast) {
-        bad |= 1u << e;
-      }
-    }
-    return bad;
+    auto one = [&](int e) -> uint32_t {
+      const bool in = (uint32_t)blk[e] < (uint32_t)p.num_blocks;
+      sl[e] = in ? (blk[e] - quot(k + e, a.by_bs)) * p.bs + k + e : -1;
+      return !in && blk[e] != kPast ? 1u << e : 0u;
+    };
+    return bx ? one(0) : one(0) | one(1) | one(2) | one(3);
   };
   // Copies a tile into dst.  The copies are issued by one elected lane, each
   // box's slot handed over by a shuffle: the instruction takes its operands
@@ -654,17 +663,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     for (int t = 0;; ++t, ++g) {  // t: tile of item j - 1, whose S has been issued
-      if (t == nt - 1 && elect_one()) commit(bar(kBQEmpty + (~j & 1)));
+      if (t == nt - 1 && elect_one()) commit(bar(kBQEmpty + qbuf(j - 1)));
       int nt2 = nt;
       if (t + 1 >= nt) {  // the tile whose S goes next is the next item's first
         Item it;
         ok = take(ir, it);
         nt2 = it.nt;
         if (!ok || (nt2 == 0 && nt == 0)) break;
-        ok = nt2 == 0 || wait_bar(bar(kBQFull + (j & 1)), (j >> 1) & 1);
+        ok = nt2 == 0 || wait_bar(bar(kBQFull + qbuf(j)), qpass(j));
         if (!ok) break;
       }
-      const int gs = nt == 0 ? g : g + 1, qb = t + 1 >= nt ? j & 1 : ~j & 1;
+      const int gs = nt == 0 ? g : g + 1, qb = qbuf(t + 1 >= nt ? j : j - 1);
       if (nt2 > 0 || t + 1 < nt) ok = issue_s(gs, qb);
       if (nt > 0 && ok) {
         const int ob = ~j & 1;
@@ -711,7 +720,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kLanes = D / 8;          // lanes of a row (8 bf16 elements each)
     constexpr int kPer = 32 / kLanes;      // rows per step
     constexpr int kStepsQ = N / kPer;
-    constexpr int kBatch = kStepsQ < 4 ? kStepsQ : 4;
     const int ch = lane % kLanes, rr = lane / kLanes;
     Ring ir;
     bool ok = true;
@@ -773,62 +781,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ir.next(kItemSlots);
       if (it.nt == 0) break;
-      // its query rows; the buffer is free once the item two before has its scores
-      const int qb = j & 1, rows = it.q_s * G;
+      // its query rows; the buffer is free once the scores of the item that
+      // used it last are there
+      const int qb = qbuf(j), rows = it.q_s * G;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ch * 8;
       const uint32_t dst = sQ + qb * G_::kQB;
-#pragma unroll 1
-      for (int b = 0; b < kStepsQ; b += kBatch) {
-        uint4 v[kBatch];
+      ok = wait_bar(bar(kBQEmpty + qb), qpass(j) ^ 1);
+      if (!ok) break;
+#pragma unroll 4
+      for (int b = 0; b < kStepsQ; ++b) {
+        const int rt = b * kPer + rr, r = it.r0 + rt, i = quot(r, a.by_g);  // row of the tile, of the sequence; its node
+        const __nv_bfloat16* src = q + (it.t0 + i) * p.q_st + (it.h * G + r - i * G) * p.q_sh;
+        // straight to shared memory; a row past the last is zeros
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (ch * 16 / AT) * N * AT +
+                                                                            swz<AT>(rt, ch % (AT / 16))),
+                     "l"(r < rows ? src : q), "r"(r < rows ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      if constexpr (F8) {
+        // the bf16 row fills row rt of both parts' tiles; the lanes that hold it
+        // replace it by its two e4m3 parts
+#pragma unroll 2
+        for (int b = 0; b < kStepsQ; ++b) {
+          const int rt = b * kPer + rr;
+          uint32_t wd[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(wd[0]), "=r"(wd[1]), "=r"(wd[2]), "=r"(wd[3])
+                       : "r"(dst + (ch * 16 / AT) * N * AT + swz<AT>(rt, ch % (AT / 16))));
+          // the row's largest element, as the bits of its absolute value (infinity and NaN on top)
+          uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = it.r0 + (b + k) * kPer + rr;
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const int i = quot(r, a.by_g);
-            v[k] = __ldg(reinterpret_cast<const uint4*>(q + (it.t0 + i) * p.q_st + (it.h * G + r - i * G) * p.q_sh));
+          for (int e = 0; e < 4; ++e) top = max(top, max(wd[e] & 0x7fffu, (wd[e] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const bool nan = top >= 0x7f80u;
+          // 2^e2 <= largest < 2^(e2 + 1); e2 stays where 2^(7 - e2) is a normal number
+          const int e2 = max(static_cast<int>(top >> 7) - 127, -100);
+          const float up = nan ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float u0 = bf16_lo(wd[e]) * up, u1 = bf16_hi(wd[e]) * up;
+            const uint16_t h2 = f32x2_to_e4m3x2(u0, u1);
+            const uint32_t hf = e4m3x2_to_f16x2(h2);
+            const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+            const uint16_t l2 = f32x2_to_e4m3x2(u0 - hv.x, u1 - hv.y);
+            hi[e >> 1] = e & 1 ? hi[e >> 1] | (uint32_t)h2 << 16 : h2;
+            lo[e >> 1] = e & 1 ? lo[e >> 1] | (uint32_t)l2 << 16 : l2;
           }
-        }
-        if (b == 0) ok = wait_bar(bar(kBQEmpty + qb), ((j >> 1) & 1) ^ 1);
-        if (!ok) break;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = (b + k) * kPer + rr;  // row of the tile
-          if constexpr (!F8) {
-            st_s128(dst + (ch * 16 / AT) * N * AT + swz<AT>(r, ch % (AT / 16)), v[k].x, v[k].y, v[k].z, v[k].w);
-          } else {
-            const uint32_t wd[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            // the row's largest element, as the bits of its absolute value (infinity and NaN on top)
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(wd[e] & 0x7fffu, (wd[e] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const bool nan = top >= 0x7f80u;
-            // 2^e2 <= largest < 2^(e2 + 1); e2 stays where 2^(7 - e2) is a normal number
-            const int e2 = max(static_cast<int>(top >> 7) - 127, -100);
-            const float up = nan ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u0 = bf16_lo(wd[e]) * up, u1 = bf16_hi(wd[e]) * up;
-              const uint16_t h2 = f32x2_to_e4m3x2(u0, u1);
-              const uint32_t hf = e4m3x2_to_f16x2(h2);
-              const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-              const uint16_t l2 = f32x2_to_e4m3x2(u0 - hv.x, u1 - hv.y);
-              hi[e >> 1] = e & 1 ? hi[e >> 1] | (uint32_t)h2 << 16 : h2;
-              lo[e >> 1] = e & 1 ? lo[e >> 1] | (uint32_t)l2 << 16 : l2;
-            }
-            const uint32_t at = swz<AT>(r, ch >> 1) + (ch & 1) * 8;
-            st_s64(dst + at, hi[0], hi[1]);
-            st_s64(dst + N * G_::kRowB + at, lo[0], lo[1]);
-            if (ch == 0)
-              qscale[(j % 4) * 64 + r] =
-                  nan ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23) * p.qk_scale_log2;
-          }
+          const uint32_t at = swz<AT>(rt, ch >> 1) + (ch & 1) * 8;
+          __syncwarp();
+          st_s64(dst + at, hi[0], hi[1]);
+          st_s64(dst + N * G_::kRowB + at, lo[0], lo[1]);
+          if (ch == 0)
+            qscale[(j % 4) * 64 + rt] =
+                nan ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23) * p.qk_scale_log2;
         }
       }
-      if (!ok) break;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -849,7 +860,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kTau = F8 ? 4.5f : 60.f;
     constexpr float kUp = F8 ? 4.f : 0.f;
     float* xh = xch + half * 128;
-    float* rh = refs + half * 32;
     // A synchronisation of the half's four warps that also tells, to all of
     // them alike, whether any wants the careful path (kCareful) or saw the
     // abort flag (kLeave: all four leave after it).  The barrier counts
@@ -867,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           : "memory");
       return n > 4 ? kLeave : n > 0 ? kCareful : kGo;
     };
-    if (tg < NC) rh[tg] = kUp;
+    if (tg < NC) refs[half * 32 + tg] = kUp;  // item 0's
     Ring ir;
     int g = 0;
     bool ok = true, joined = vote(false, false) == kLeave;  // joined: left together with the group
@@ -887,6 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = it.nt, rows = it.q_s * G, ctx = it.n - it.q_s;
       const int ra = it.r0 + half * NC;  // first row of this half
       const float* qs = qscale + (j % 4) * 64 + half * NC;
+      // the rows' references, kept as kUp - reference; the next item's start at
+      // reference 0 (three sets: warps of the half may still read the last item's)
+      float* rh = refs + (j % 3) * 64 + half * 32;
+      if (tg < NC) refs[((j + 1) % 3) * 64 + half * 32 + tg] = kUp;
       if (F8) {
         ok = wait_bar(bar(kBQsFull + j % 4), (j >> 2) & 1);
         if (!ok) break;
@@ -894,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned long long l2[NC / 2];  // the rows' sums over this lane's keys, in pairs
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) l2[c] = 0ull;
-      uint32_t vmask = 0;  // rows of the half without a reference yet (stored as 0), after the first tile
+      uint32_t vmask = 0;  // rows of the half without a reference yet (stored as 0), once the first tile has set them
       for (int t = 0; t < nt; ++t, ++g) {
         ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
@@ -961,6 +975,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // y = score in base 2 less the row's reference, plus kUp
         float y[NC];
+        if (F8 && t == 0 && !masked) {
+          // the first reference: the row's largest score among 32 of the tile's
+          // keys (each warp takes a quarter of the rows over its own keys); the
+          // whole tile's is rarely 2^kTau above
+          float m = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q == quarter) {
+#pragma unroll
+              for (int c = 0; c < NC / 4; ++c) {
+                const int cc = q * (NC / 4) + c;
+                const float x = redux_max(__uint_as_float(u[cc]) * qs[cc]);
+                m = lane == c ? x : m;
+              }
+            }
+          const bool none = lane < NC / 4 && m == -INFINITY;
+          if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - m;
+          const uint32_t unset = __ballot_sync(0xffffffffu, none) << (quarter * (NC / 4));
+          if (lane == 0) unset4[half * 4 + quarter] = unset;
+          const int v = vote(unset != 0, false);
+          if (v == kLeave) { ok = false; joined = true; break; }
+          if (v == kCareful) vmask = unset4[half * 4] | unset4[half * 4 + 1] | unset4[half * 4 + 2] | unset4[half * 4 + 3];
+        }
         for (bool again = false;; again = true) {
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
@@ -981,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < NC; ++c) y[c] = (see >> c) & 1u ? y[c] : -INFINITY;
           }
           if (again) break;
-          if (!masked && !(F8 && t == 0) && vmask == 0) {
+          if (!masked && vmask == 0) {
             float top = fmaxf(y[0], y[1]);
 #pragma unroll
             for (int c = 2; c < NC; c += 2) top = fmax3(top, y[c], y[c + 1]);
@@ -1012,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float top = fmaxf(fmaxf(xh[lane], xh[32 + lane]), fmaxf(xh[64 + lane], xh[96 + lane]));
             const float old = rh[lane];
             nref = old;
-            if (t == 0 || ((vmask >> lane) & 1u)) {  // nothing summed so far, the reference is 0
+            if ((t == 0 && (!F8 || masked)) || ((vmask >> lane) & 1u)) {  // none yet, 0 stands in
               none = top == -INFINITY;
               if (!none && (F8 || fabsf(top) > kTau)) nref = old + kUp - top;
             } else if (top > kTau + kUp) {
@@ -1107,30 +1144,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kBPFull + (g & 1)));
       }
       if (!ok) break;
-      // the rows' sums over the lanes and the four warps of the half
+      // the rows' sums over this warp's keys go to the output warps
+      if (!wait_bar(bar(kBLEmpty + (j & 1)), ((j >> 1) & 1) ^ 1)) { ok = false; break; }
       {
         float m[NC];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) up2(l2[c / 2], m[c], m[c + 1]);
         const float mine = col_sum<NC>(m, lane);
-        if (lane % (32 / NC) == 0) xh[quarter * 32 + lane / (32 / NC)] = mine;
-        if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
-        if (tg < NC) {
-          const float s = (xh[tg] + xh[32 + tg]) + (xh[64 + tg] + xh[96 + tg]);
-          linv[(j % 3) * 64 + half * NC + tg] = s == 0.f ? 0.f : p.v_scale / s;
-          const int r = ra + tg;
-          if (it.nchunks > 1 && r < rows) {
-            const int i = quot(r, a.by_g);
-            a.part_lse[((int64_t)it.s * a.rows_per_seq + (int64_t)i * it.nchunks + it.c) * p.Hq + it.h * G + r - i * G] =
-                s == 0.f ? -INFINITY : __log2f(s) - rh[tg];  // reference + log2(sum) - kUp
-          }
-          rh[tg] = kUp;  // the next item's rows start at reference 0
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBLFull + j % 3));
-        // xh and the references have been read
-        if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+        const int at = (j & 1) * 64 + half * NC;
+        if (lane % (32 / NC) == 0) sums[(j & 1) * 256 + quarter * 64 + half * NC + lane / (32 / NC)] = mine;
+        if (tg < NC) lref[at + tg] = rh[tg];
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBLFull + (j & 1)));
     }
     if (!ok) *abort_flag = 1;
     if (!joined) vote(false, !ok);
@@ -1147,12 +1173,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it;
       ok = take(ir, it);
       if (!ok || it.nt == 0) break;
-      ok = wait_bar(bar(kBLFull + j % 3), (j / 3) & 1) &&
-           wait_bar(bar(kBOFull + (j & 1)), (j >> 1) & 1);
+      ok = wait_bar(bar(kBLFull + (j & 1)), (j >> 1) & 1);
+      if (!ok) break;
+      const int rows = it.q_s * G;
+      // lane c (and c + 32): 1 / (row c's sum), and its log2-sum-exp2 for the join
+      float inv[kOff];
+#pragma unroll
+      for (int k = 0; k < kOff; ++k) {
+        const int c = (lane + 32 * k) & (N - 1), r = it.r0 + c;
+        const float* q = sums + (j & 1) * 256 + c;
+        const float l = (q[0] + q[64]) + (q[128] + q[192]);
+        inv[k] = l == 0.f ? 0.f : p.v_scale / l;
+        if (warp == 12 && it.nchunks > 1 && r < rows && lane + 32 * k < N) {
+          const int i = quot(r, a.by_g);
+          a.part_lse[((int64_t)it.s * a.rows_per_seq + i * it.nchunks + it.c) * p.Hq + it.h * G + r - i * G] =
+              l == 0.f ? -INFINITY : __log2f(l) - lref[(j & 1) * 64 + (c / NC) * NC + c % NC];  // reference + log2(sum) - kUp
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBLEmpty + (j & 1)));
+      ok = wait_bar(bar(kBOFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
       fence_after();
-      const int rows = it.q_s * G;
-      const float* li = linv + (j % 3) * 64;
       const bool split = it.nchunks > 1, wide = split || !a.out_bf16;  // fp32 elements
       // lane c (and c + 32): where row c's element 0 goes, in bytes from `to_base`; -1: no row
       const int esz = wide ? 4 : 2;
@@ -1179,15 +1221,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBOFree + (j & 1)));
         }
+        const float si = kOff > 1 && b >= 32 ? inv[kOff - 1] : inv[0];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(li + b + c);
-          const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = fmaf(__uint_as_float(o2[c + e]), kLo, __uint_as_float(o[c + e])) * sc[e];
-            v[c + e] = sc[e] == 0.f ? 0.f : x;
-          }
+        for (int c = 0; c < kCols; ++c) {
+          const float sc = __shfl_sync(0xffffffffu, si, (b & 31) + c);
+          const float x = fmaf(__uint_as_float(o2[c]), kLo, __uint_as_float(o[c])) * sc;
+          v[c] = sc == 0.f ? 0.f : x;
         }
         long long at[kCols];
         const long long from = kOff > 1 && b >= 32 ? off[kOff - 1] : off[0];
