@@ -859,6 +859,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // score lies beyond +-kTau; e4m3 parts want the largest p near 2^kUp.
     constexpr float kTau = F8 ? 4.5f : 60.f;
     constexpr float kUp = F8 ? 4.f : 0.f;
+    // an e4m3 row's reference is set this far above the largest score seen, so
+    // that it rarely has to move again in a chunk
+    constexpr float kMargin = F8 ? 2.5f : 0.f;
     float* xh = xch + half * 128;
     // A synchronisation of the half's four warps that also tells, to all of
     // them alike, whether any wants the careful path (kCareful) or saw the
@@ -976,9 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // y = score in base 2 less the row's reference, plus kUp
         float y[NC];
         if (F8 && t == 0 && !masked) {
-          // the first reference: the row's largest score among 32 of the tile's
-          // keys (each warp takes a quarter of the rows over its own keys); the
-          // whole tile's is rarely 2^kTau above
+          // the first reference, from the row's largest score among 32 of the
+          // tile's keys (each warp takes a quarter of the rows over its own keys)
           float m = -INFINITY;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -991,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           const bool none = lane < NC / 4 && m == -INFINITY;
-          if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - m;
+          if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - kMargin - m;
           const uint32_t unset = __ballot_sync(0xffffffffu, none) << (quarter * (NC / 4));
           if (lane == 0) unset4[half * 4 + quarter] = unset;
           const int v = vote(unset != 0, false);
@@ -1051,10 +1053,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             nref = old;
             if ((t == 0 && (!F8 || masked)) || ((vmask >> lane) & 1u)) {  // none yet, 0 stands in
               none = top == -INFINITY;
-              if (!none && (F8 || fabsf(top) > kTau)) nref = old + kUp - top;
+              if (!none && (F8 || fabsf(top) > kTau)) nref = old + kUp - kMargin - top;
             } else if (top > kTau + kUp) {
-              nref = old + kUp - top;
-              alpha = ex2(kUp - top);
+              nref = old + kUp - kMargin - top;
+              alpha = ex2(kUp - kMargin - top);
               moved = true;
             }
           }
