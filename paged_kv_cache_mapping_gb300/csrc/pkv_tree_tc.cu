@@ -125,11 +125,12 @@ struct alignas(16) Item {
 enum : int {
   kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26 /* 2 */, kBOFull = 28,
   kBOFree = 30, kBQFull = 32, kBQEmpty = 34, kBQsFull = 36, kBLFull = 40, kBLEmpty = 42, kBItemFull = 44,
-  kBItemEmpty = 50, kBODone = 56, kBDrain = 57, kSTmem = 58, kSAbort = 59, kSPoison = 60 /* [3] ints: 60, 61 */,
-  kOffItems = 496, kOffInfo = 784, kOffXch = 912 /* [2][4][32] */, kOffSum = 1936 /* [2][4][64] */,
-  kOffLref = 3984 /* [2][64] */, kOffRef = 4496 /* [3][64] */, kOffQs = 5264 /* e4m3: [4][64] */, kOffUnset = 6288,
+  kBItemEmpty = 50, kBODone = 56, kBDrain = 57, kBGroup = 58, kSTmem = 60, kSAbort = 61, kSPoison = 62 /* [3] ints: 62, 63 */,
+  kOffItems = 512, kOffInfo = 800, kOffXch = 928 /* [2][4][32] */, kOffSum = 1952 /* [2][4][64] */,
+  kOffLref = 4000 /* [2][64] */, kOffRef = 4512 /* [3][64] */, kOffQs = 5280 /* e4m3: [4][64] */, kOffUnset = 6304 /* [2][4] */,
+  kOffFlag = 6336 /* [2][2] */,
 };
-static_assert(kOffUnset + 32 <= kMiscBytes, "shared memory");
+static_assert(kOffFlag + 16 <= kMiscBytes, "shared memory");
 static_assert(kOffItems + kItemSlots * (int)sizeof(Item) <= kOffInfo, "item ring");
 
 // ---------------------------------------------------------------- PTX
@@ -464,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBLFull + i), 8);
       mbar_init(bar(kBLEmpty + i), 4);
+      mbar_init(bar(kBGroup + i), 4);
     }
     for (int i = 0; i < 2; ++i) mbar_init(bar(kBPFull + i), 8);
     mbar_init(bar(kBODone), 1);
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBDrain), 1);
     *abort_flag = 0;
     for (int i = 0; i < 3; ++i) poison[i] = 0;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<volatile int*>(misc + kOffFlag)[i] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane < 2)
@@ -863,40 +866,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     // that it rarely has to move again in a chunk
     constexpr float kMargin = F8 ? 2.5f : 0.f;
     float* xh = xch + half * 128;
-    // A synchronisation of the half's four warps that also tells, to all of
-    // them alike, whether any wants the careful path (kCareful) or saw the
-    // abort flag (kLeave: all four leave after it).  The barrier counts
-    // threads: lane 0 of a warp stands for its wish, the others for the flag.
-    // A warp that gives up joins one more vote, and so does every warp at the
-    // end of the items: no warp is left waiting.
-    enum : int { kGo = 0, kCareful = 1, kLeave = 2 };
-    auto vote = [&](bool want, bool leave) -> int {
-      const bool stand = lane == 0 ? want : leave || *abort_flag != 0;
-      uint32_t n;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, %1, 128, p;\n\t}"
-          : "=r"(n)
-          : "r"(1 + half), "r"(stand ? 1 : 0)
-          : "memory");
-      return n > 4 ? kLeave : n > 0 ? kCareful : kGo;
+    // A vote of the half's four warps, cast and counted apart so that work can
+    // go between: count() tells all four alike whether any of them wanted.
+    volatile int* flag = reinterpret_cast<volatile int*>(misc + kOffFlag) + 2 * half;  // [2]: number of the vote that wants
+    int votes = 0;
+    auto cast = [&](bool want) {
+      if (lane == 0) {
+        if (want) flag[votes & 1] = votes + 1;
+        mbar_arrive(bar(kBGroup + half));
+      }
+    };
+    auto count = [&](bool& wanted) -> bool {
+      const bool r = wait_bar(bar(kBGroup + half), votes & 1);
+      wanted = flag[votes & 1] == votes + 1;
+      ++votes;
+      return r;
+    };
+    auto sync = [&]() -> bool {  // also orders the four warps' shared memory
+      bool w;
+      __syncwarp();
+      cast(false);
+      return count(w);
     };
     if (tg < NC) refs[half * 32 + tg] = kUp;  // item 0's
     Ring ir;
     int g = 0;
-    bool ok = true, joined = vote(false, false) == kLeave;  // joined: left together with the group
-    for (int j = 0; !joined; ++j) {
+    bool ok = sync();
+    for (int j = 0; ok; ++j) {
       Item it;
-      if (!wait_bar(bar(kBItemFull) + 8 * ir.at, ir.pass)) { ok = false; break; }
-      {
-        const int4* q = reinterpret_cast<const int4*>(items + ir.at);
-        *reinterpret_cast<int4*>(&it) = q[0];
-        *(reinterpret_cast<int4*>(&it) + 1) = q[1];
-        *(reinterpret_cast<int4*>(&it) + 2) = q[2];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBItemEmpty) + 8 * ir.at);
-      ir.next(kItemSlots);
-      if (it.nt == 0) break;
+      ok = take(ir, it);
+      if (!ok || it.nt == 0) break;
       const int nt = it.nt, rows = it.q_s * G, ctx = it.n - it.q_s;
       const int ra = it.r0 + half * NC;  // first row of this half
       const float* qs = qscale + (j % 4) * 64 + half * NC;
@@ -916,10 +915,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
         fence_after();
-        uint32_t u[NC];  // q.k of the stored values
-        tm_ld(tmem + (g & 1) * N + half * NC + lane_off, u);
+        const uint32_t ts = tmem + (g & 1) * N + half * NC + lane_off;  // this tile's q.k of the stored values
         const uint4 bad = *reinterpret_cast<const uint4*>(info + (g % kInfoSlots) * 4);
-        wait_ld();
         const int kt = it.k0 + t * kKeys;  // first key of the tile
         const bool masked = kt + kKeys > ctx || (bad.x | bad.y | bad.z | bad.w) != 0;
         uint32_t see = 0xffffffffu;  // rows that see this lane's key
@@ -978,29 +975,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // y = score in base 2 less the row's reference, plus kUp
         float y[NC];
+        uint32_t hi[F8 ? NC / 4 : NC / 2], lo[F8 ? NC / 4 : NC / 2];
         if (F8 && t == 0 && !masked) {
           // the first reference, from the row's largest score among 32 of the
           // tile's keys (each warp takes a quarter of the rows over its own keys)
+          uint32_t u[8];
           float m = -INFINITY;
+          constexpr int kSample = NC / 4 < 8 ? NC / 4 : 8;
+          tm_ld(tmem + (g & 1) * N + lane_off + (half * NC + quarter * (NC / 4)) / 8 * 8, u);
+          wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q == quarter) {
-#pragma unroll
-              for (int c = 0; c < NC / 4; ++c) {
-                const int cc = q * (NC / 4) + c;
-                const float x = redux_max(__uint_as_float(u[cc]) * qs[cc]);
-                m = lane == c ? x : m;
-              }
-            }
+          for (int c = 0; c < 8; ++c) {
+            const int cc = c - (half * NC + quarter * (NC / 4)) % 8;  // row of the quarter
+            const float x = redux_max(__uint_as_float(u[c]) * qs[(quarter * (NC / 4)) / 8 * 8 + c]);
+            m = lane == cc && cc < kSample ? x : m;
+          }
           const bool none = lane < NC / 4 && m == -INFINITY;
           if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - kMargin - m;
           const uint32_t unset = __ballot_sync(0xffffffffu, none) << (quarter * (NC / 4));
           if (lane == 0) unset4[half * 4 + quarter] = unset;
-          const int v = vote(unset != 0, false);
-          if (v == kLeave) { ok = false; joined = true; break; }
-          if (v == kCareful) vmask = unset4[half * 4] | unset4[half * 4 + 1] | unset4[half * 4 + 2] | unset4[half * 4 + 3];
+          __syncwarp();
+          cast(unset != 0);
+          bool some;
+          if (!count(some)) { ok = false; break; }
+          if (some) vmask = unset4[half * 4] | unset4[half * 4 + 1] | unset4[half * 4 + 2] | unset4[half * 4 + 3];
         }
-        for (bool again = false;; again = true) {
+        // first try: all of the tile's work against the references there are;
+        // careful: new references; last: the work against those
+        enum : int { kTry, kCareful, kLast };
+        for (int mode = masked || vmask ? kCareful : kTry;;) {
+          uint32_t u[NC];
+          tm_ld(ts, u);
+          wait_ld();
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
             const float4 r = *reinterpret_cast<const float4*>(rh + c);
@@ -1019,8 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < NC; ++c) y[c] = (see >> c) & 1u ? y[c] : -INFINITY;
           }
-          if (again) break;
-          if (!masked && vmask == 0) {
+          if (mode == kTry) {
             float top = fmaxf(y[0], y[1]);
 #pragma unroll
             for (int c = 2; c < NC; c += 2) top = fmax3(top, y[c], y[c + 1]);
@@ -1031,9 +1036,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 2; c < NC; c += 2) low = fmin3(low, y[c], y[c + 1]);
               want = want || !(low >= -kTau);
             }
-            const int v = vote(__any_sync(0xffffffffu, want), false);
-            if (v == kLeave) { ok = false; joined = true; break; }
-            if (v == kGo) break;
+            cast(__any_sync(0xffffffffu, want));
+          }
+          if (mode != kCareful) {
+            // P = 2^y in two parts, row = key, hi in columns 0 .. N - 1, lo in N .. 2 N - 1
+            // (while the vote is out: if it asks for care, all of this is done again)
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+              const float p0 = ex2(y[c]), p1 = ex2(y[c + 1]);
+              const unsigned long long pp = pk2(p0, p1);
+              y[c] = p0;
+              y[c + 1] = p1;
+              if constexpr (F8) {
+                // through f16 (11 bits, two values at a time): hi its e4m3 code, lo
+                // that of 16 times the exact remainder
+                const __half2 h = __floats2half2_rn(p0, p1);
+                const uint16_t h2 = f16x2_to_e4m3x2(h);
+                const uint32_t hb = e4m3x2_to_f16x2(h2);
+                const uint16_t l8 = f16x2_to_e4m3x2(__hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hb)), __float2half2_rn(16.f)));
+                if (c & 2) {
+                  hi[c / 4] |= (uint32_t)h2 << 16;
+                  lo[c / 4] |= (uint32_t)l8 << 16;
+                } else {
+                  hi[c / 4] = h2;
+                  lo[c / 4] = l8;
+                }
+              } else {
+                const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                hi[c / 2] = __byte_perm(u0, u1, 0x7632);
+                float r0, r1;  // p - hi exactly: the truncated-away low bits
+                up2(sub2(pp, pk2(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))), r0, r1);
+                lo[c / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+              }
+            }
+            if (mode == kLast) break;
+            bool wanted;
+            ok = count(wanted);
+            if (!ok || !wanted) break;
+            mode = kCareful;
+            continue;
           }
           // ---- the careful path: the rows' largest y over the tile
           float mine = 0.f;
@@ -1043,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mine = lane == c ? m : mine;
           }
           if (lane < NC) xh[quarter * 32 + lane] = mine;
-          if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+          if (!sync()) { ok = false; break; }
           // lane c: row c's new reference; the stored value is kUp - reference
           float alpha = 1.f, nref = 0.f;
           bool moved = false, none = false;
@@ -1063,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           vmask = __ballot_sync(0xffffffffu, none);
           const bool any = __any_sync(0xffffffffu, moved);
           // every warp has read the references
-          if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+          if (!sync()) { ok = false; break; }
           if (quarter == 0 && lane < NC) rh[lane] = nref;
           if (any) {  // the same in the half's four warps
 #pragma unroll
@@ -1091,38 +1132,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_st();
           }
           // the references are written
-          if (vote(false, false) == kLeave) { ok = false; joined = true; break; }
+          if (!sync()) { ok = false; break; }
+          mode = kLast;
         }
         if (!ok) break;
-        // P = 2^y in two parts, row = key, hi in columns 0 .. N - 1, lo in N .. 2 N - 1
-        uint32_t hi[F8 ? NC / 4 : NC / 2], lo[F8 ? NC / 4 : NC / 2];
 #pragma unroll
-        for (int c = 0; c < NC; c += 2) {
-          const float p0 = ex2(y[c]), p1 = ex2(y[c + 1]);
-          const unsigned long long pp = pk2(p0, p1);
-          l2[c / 2] = add2(l2[c / 2], pp);
-          if constexpr (F8) {
-            // through f16 (11 bits, two values at a time): hi its e4m3 code, lo
-            // that of 16 times the exact remainder
-            const __half2 h = __floats2half2_rn(p0, p1);
-            const uint16_t h2 = f16x2_to_e4m3x2(h);
-            const uint32_t hb = e4m3x2_to_f16x2(h2);
-            const uint16_t l8 = f16x2_to_e4m3x2(__hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hb)), __float2half2_rn(16.f)));
-            if (c & 2) {
-              hi[c / 4] |= (uint32_t)h2 << 16;
-              lo[c / 4] |= (uint32_t)l8 << 16;
-            } else {
-              hi[c / 4] = h2;
-              lo[c / 4] = l8;
-            }
-          } else {
-            const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-            hi[c / 2] = __byte_perm(u0, u1, 0x7632);
-            float r0, r1;  // p - hi exactly: the truncated-away low bits
-            up2(sub2(pp, pk2(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))), r0, r1);
-            lo[c / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-          }
-        }
+        for (int c = 0; c < NC; c += 2) l2[c / 2] = add2(l2[c / 2], pk2(y[c], y[c + 1]));
         // the buffer is free once P V of the tile that last used it has run: the
         // previous one, or, with two buffers, the one before it, which this
         // tile's S came after
@@ -1161,7 +1176,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBLFull + (j & 1)));
     }
     if (!ok) *abort_flag = 1;
-    if (!joined) vote(false, !ok);
   } else {
     // ======================= O / l: lane = d, register = row =======================
     const int d = (warp & 3) * 32 + lane;
