@@ -285,8 +285,9 @@ pkv_status pkv_tree_attention_workspace_size(const pkv_tensor* q, const pkv_tens
   PKV_NEED(bytes != nullptr, "bytes is NULL");
   *bytes = 0;
   if (k_cache->dtype == PKV_F32) return PKV_OK;
-  const int64_t rows = block_tables->shape[0] *
-                       tree_tc_rows_per_seq(max_nodes_of(max_q_len, q->shape[0]), block_tables->shape[1] * k_cache->shape[1]);
+  const int64_t B = block_tables->shape[0], Hkv = k_cache->shape[2], G = Hkv > 0 ? q->shape[1] / Hkv : 1;
+  const int64_t rows = B * tree_tc_rows_per_seq(B, Hkv, G, max_nodes_of(max_q_len, q->shape[0]),
+                                                block_tables->shape[1] * k_cache->shape[1]);
   *bytes = align_up(sizeof(float) * rows * q->shape[1] * (q->shape[2] + 1), 256);
   return PKV_OK;
 }
@@ -381,7 +382,7 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
   if (T == 0 || B == 0) return PKV_OK;
   const int out_kind = out->dtype == PKV_BF16;
   const cudaError_t e = kv == 0 ? launch_tree_f32(p, out_kind, st)
-                                : launch_tree_tc(p, kv == 2, out_kind, p.max_nodes, block_tables->shape[1] * bs, workspace, sms, st);
+                                : launch_tree_tc(p, kv == 2, out_kind, max_q, block_tables->shape[1] * bs, workspace, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return finish(st, "pkv_tree_attention");
 }

@@ -20,8 +20,8 @@
 // so its result does not depend on the rows beside it.
 //
 // Work: an item is (sequence, chunk of keys, KV head, tile of N rows).  The
-// chunk length follows from the sequence's own length and node count, chunks
-// write normalised partials and log2-sum-exp2, and a second small kernel joins
+// chunk length follows from the sequence's own length and node count and the
+// call's shapes, not from the other sequences (tree_chunk).  Chunks write normalised partials and log2-sum-exp2, and a second small kernel joins
 // them in order.  Items are dealt to the persistent CTAs (one per SM) in
 // strides; every CTA finds its items by scanning the lengths, 32 sequences per
 // step, so a call needs no plan, keeps nothing between calls, and its
@@ -62,20 +62,31 @@ constexpr int kItemSlots = 6;
 constexpr int kInfoSlots = 8;
 
 // ---------------------------------------------------------------- chunking
-// Keys per chunk: at most 64 chunks, at most 1024 / q_s (so that a sequence
-// has at most 1024 partial rows per head), at least 256 keys, whole tiles.  A
-// function of the sequence alone.
+// Keys per chunk, from the sequence's own length and node count and from how
+// many (sequence, KV head, row tile) units the call has: few units are cut
+// finely so that every SM has work, many are cut coarsely, since each chunk
+// costs its rows' partials (512 bytes per row and head, written and read) and
+// an item's start and end.  At least `least` keys, at most `most` chunks, and
+// at most kTreePartRows / q_s of them, so that a sequence has at most that many
+// partial rows per head.
 constexpr int kTreeMaxChunks = 64;
 constexpr int kTreePartRows = 1024;
-constexpr int kTreeMinChunk = 256;
+struct Chunking {
+  int32_t least, most;
+};
+inline Chunking tree_chunking(int64_t units) {
+  Chunking c;
+  c.least = units >= 512 ? 1024 : units >= 128 ? 512 : 256;
+  const int64_t m = 2432 / (units < 1 ? 1 : units);  // 16 items per SM
+  c.most = static_cast<int32_t>(m < 8 ? 8 : m > kTreeMaxChunks ? kTreeMaxChunks : m);
+  return c;
+}
 
-__host__ __device__ inline int tree_chunk(int n, int q_s) {
-  int most = kTreePartRows / q_s;
-  most = most < 1 ? 1 : most > kTreeMaxChunks ? kTreeMaxChunks : most;
-  long long c = ((long long)n + most - 1) / most;
-  c = (c + kKeys - 1) / kKeys * kKeys;
-  if (most == 1) return static_cast<int>(c < 0x7fffff80ll ? c : 0x7fffff80ll);
-  return static_cast<int>(c < kTreeMinChunk ? kTreeMinChunk : c);
+__host__ __device__ inline int tree_chunk(int n, int q_s, Chunking k) {
+  const int rows = kTreePartRows / q_s;
+  const int most = rows < 1 ? 1 : rows < k.most ? rows : k.most;
+  const int c = ((n - 1) / most / kKeys + 1) * kKeys;  // ceil(n / most) in whole tiles; n < 2^31 - 128
+  return most > 1 && c < k.least ? k.least : c;
 }
 
 // ---------------------------------------------------------------- geometry
@@ -368,6 +379,7 @@ struct TcArgs {
   TreeParams p;
   FastDiv by_g, by_bs;
   int32_t rows_per_seq;  // partial rows of a sequence
+  Chunking chunking;
   int32_t box;           // slots per TMA box, 0: gather4
   int32_t out_bf16;
   float* part_o;         // [B * rows_per_seq, Hq, D] normalised chunk outputs
@@ -743,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            q_s > p.max_nodes;
           if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
           if (!bad && q_s > 0) {
-            chunk = tree_chunk(n, q_s);
+            chunk = tree_chunk(n, q_s, a.chunking);
             nchunks = (n - 1) / chunk + 1;
             rts = (q_s * G - 1) / N + 1;
             cnt = nchunks * Hkv * rts;
@@ -1280,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // eight chunks' loads in flight.  grid: (sequences, parts of a sequence's rows).
 template <int D, typename OutT>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, const float* part_o, const float* part_lse,
-                                                        int rows_per_seq) {
+                                                        int rows_per_seq, Chunking chunking) {
   grid_dep_wait();
   launch_dependents();
   constexpr int E = D / 32;
@@ -1289,8 +1301,8 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, cons
   const int q_s = c1 - c0;
   if (c0 < 0 || c1 <= c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs || q_s > p.max_nodes)
     return;
-  const int chunk = tree_chunk(n, q_s);
-  const int nc = static_cast<int>(((long long)n + chunk - 1) / chunk);
+  const int chunk = tree_chunk(n, q_s, chunking);
+  const int nc = (n - 1) / chunk + 1;
   if (nc == 1) return;
   const int64_t rows = (int64_t)q_s * p.Hq;
   for (int64_t r = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.y * 8) {
@@ -1398,8 +1410,16 @@ cudaError_t launch_t(TcArgs a, int64_t max_items, int num_sms, cudaStream_t st) 
 
 }  // namespace
 
-int64_t tree_tc_rows_per_seq(int64_t max_q, int64_t max_ctx) {
-  const int64_t chunks = std::min<int64_t>(kTreeMaxChunks, (max_ctx + kTreeMinChunk - 1) / kTreeMinChunk);
+// Rows per MMA tile: the narrowest that holds the largest tree.
+static int tree_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+static Chunking call_chunking(int64_t B, int64_t Hkv, int64_t rows) {
+  const int64_t N = tree_tile_rows(rows);
+  return tree_chunking(B * Hkv * ((rows + N - 1) / N));
+}
+
+int64_t tree_tc_rows_per_seq(int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_ctx) {
+  const Chunking c = call_chunking(B, Hkv, max_q * G);
+  const int64_t chunks = std::min<int64_t>(c.most, (max_ctx + c.least - 1) / c.least);
   if (chunks <= 1) return 0;
   return std::min<int64_t>(max_q * chunks, kTreePartRows);
 }
@@ -1411,13 +1431,13 @@ cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t m
   a.out_bf16 = out_kind;
   a.by_g = fast_div(static_cast<uint32_t>(p.G));
   a.by_bs = fast_div(static_cast<uint32_t>(p.bs));
-  const int64_t rps = tree_tc_rows_per_seq(max_q, max_ctx);
+  const int64_t rps = tree_tc_rows_per_seq(p.B, p.Hkv, p.G, max_q, max_ctx);
   a.rows_per_seq = static_cast<int32_t>(rps);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (int64_t)p.B * rps * p.Hq * p.D;
-  // rows per MMA tile: the narrowest that holds the largest tree
   const int64_t rows = max_q * p.G;
-  const int N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int N = tree_tile_rows(rows);
+  a.chunking = call_chunking(p.B, p.Hkv, rows);
   const int64_t most = (int64_t)p.B * kTreeMaxChunks * p.Hkv * ((rows + N - 1) / N);
   cudaError_t e;
 #define PKV_TC1(D, F8)                                      \
@@ -1433,7 +1453,7 @@ cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t m
   const int64_t want = (max_q * p.Hq + 7) / 8;
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(want, (8 * num_sms + p.B - 1) / p.B));
   const dim3 grid((unsigned)p.B, (unsigned)y);
-#define PKV_JOIN(D, O) launch_ex(tree_join_kernel<D, O>, grid, dim3(256), 0, st, true, p, (const float*)a.part_o, (const float*)a.part_lse, a.rows_per_seq)
+#define PKV_JOIN(D, O) launch_ex(tree_join_kernel<D, O>, grid, dim3(256), 0, st, true, p, (const float*)a.part_o, (const float*)a.part_lse, a.rows_per_seq, a.chunking)
   if (p.D == 128) return out_kind ? PKV_JOIN(128, __nv_bfloat16) : PKV_JOIN(128, float);
   return out_kind ? PKV_JOIN(64, __nv_bfloat16) : PKV_JOIN(64, float);
 #undef PKV_JOIN

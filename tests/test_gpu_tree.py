@@ -189,14 +189,20 @@ def test_one_dominant_key_and_many_small_ones():
     compare(b)
 
 
-def test_unknown_max_q_len_and_wide_masks_change_nothing():
-    b = Batch([300, 20, 5], [8, 1, 40], 8, 2, 128, 16, "bf16", seed=17, mask_words=5)
+def test_wide_masks_and_the_other_sequences_change_nothing():
+    b = Batch([3000, 20, 500], [8, 1, 40], 8, 2, 128, 16, "bf16", seed=17, mask_words=5)
     a = Dev(b).run().clone()
-    assert torch.equal(a, Dev(b).run(max_q=0))
-    assert torch.equal(a, Dev(b).run(max_q=160))
-    one = Batch([300], [8], 8, 2, 128, 16, "bf16", seed=17)
-    one.q, one.kc, one.vc, one.tables, one.mask, one.nb = b.q[:8], b.kc, b.vc, b.tables[:1], b.mask[:8], b.nb
-    assert torch.equal(a[:8], Dev(one).run())  # alone as in the batch
+    assert torch.equal(a, Dev(b).run(max_q=40))
+    compare(b, out=Dev(b).run(max_q=0))  # unknown: every row could be one tree's
+    compare(b, out=Dev(b).run(max_q=160))
+    # the other sequences get other lengths, queries and values
+    d = Dev(b)
+    d.n[1:] = torch.tensor([1, 321], dtype=torch.int32)
+    d.q[8:] *= -3.0
+    d.mask[8:] = -1
+    d.vc.view(-1, 2, 128)[torch.from_numpy(b.slots(2)).cuda()] = 9.0
+    assert torch.equal(a[:8], d.run()[:8])
+    assert pkv.pkv_device_errors() == 0
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
