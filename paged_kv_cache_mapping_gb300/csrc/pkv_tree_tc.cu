@@ -44,8 +44,9 @@
 //               products side by side and P V costs one pass of instructions.
 //   warp 2      finds the items, publishes them and brings their query rows:
 //               bf16 to the swizzled operand layout, or split to e4m3.
-//   warps 4-11  softmax: lane quarter w % 4 = keys, half (w - 4) / 4 = rows.
-//   warps 12-15 write O / l of finished items while the next one runs.
+//   then 8 or 16 (N = 64) warps of softmax: lane quarter w % 4 = keys, group
+//               (w - 4) / 4 = rows.
+//   and 4 warps that write O / l of finished items while the next one runs.
 #include <cuda.h>
 
 #include <algorithm>
@@ -57,7 +58,6 @@ namespace pkv {
 namespace {
 
 constexpr int kKeys = 128;  // keys per tile (M of S^T, K of P V)
-constexpr int kThreads = 512;
 constexpr int kItemSlots = 6;
 constexpr int kInfoSlots = 8;
 
@@ -102,17 +102,17 @@ struct Geo {
   static constexpr int kQB = N * kRowB * kParts;
   static constexpr int kPRow = 2 * N * kEs;                   // both parts of P of one key
   static constexpr int kPB = kKeys * (kPRow <= 128 ? 128 : 256);  // [1 or 2][128 keys][128 bytes]
-  // two P buffers, so that no tile waits for the P V before it (an S commit
-  // covers the P V issued before that S); one where shared memory is short
-  static constexpr int kPBufs = kPRow == 256 && kTileB == 32768 ? 1 : 2;
   static constexpr int kNK = kTileB == 32768 ? 2 : kTileB == 16384 ? 4 : 6;
-  static constexpr int kNV = kTileB == 32768 ? 3 : kTileB == 16384 ? (kPRow == 256 ? 4 : 5) : 6;
-  static constexpr int kNC = N / 2;                           // rows (columns of S^T) per softmax warp
+  static constexpr int kNV = kTileB == 32768 ? (kPRow == 256 ? 2 : 3) : kTileB == 16384 ? (kPRow == 256 ? 4 : 5) : 6;
+  static constexpr int kGroups = N == 64 ? 4 : 2;             // softmax: groups of four warps, each N / kGroups rows
+  static constexpr int kSoft = 4 * kGroups;                   // its warps
+  static constexpr int kThreads = 32 * (4 + kSoft + 4);
+  static constexpr int kNC = N / kGroups;                     // rows (columns of S^T) per softmax warp
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kNK * kTileB;
   static constexpr int kOffP = kOffV + kNV * kTileB;
-  static constexpr int kOffQ = kOffP + kPBufs * kPB;
-  static constexpr int kQBufs = kPBufs;  // query tiles: the next item's arrives while this one runs
+  static constexpr int kOffQ = kOffP + 2 * kPB;
+  static constexpr int kQBufs = kPRow == 256 && kTileB == 32768 ? 1 : 2;  // query tiles: the next item's arrives while this one runs
   static constexpr int kOffMisc = kOffQ + kQBufs * kQB;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
   // tensor memory: S 2 x N columns, then O 2 x (hi N, lo N)
@@ -136,12 +136,12 @@ struct alignas(16) Item {
 enum : int {
   kBKFull = 0, kBKEmpty = 6, kBVFull = 12, kBVEmpty = 18, kBSFull = 24, kBPFull = 26 /* 2 */, kBOFull = 28,
   kBOFree = 30, kBQFull = 32, kBQEmpty = 34, kBQsFull = 36, kBLFull = 40, kBLEmpty = 42, kBItemFull = 44,
-  kBItemEmpty = 50, kBODone = 56, kBDrain = 57, kBGroup = 58, kSTmem = 60, kSAbort = 61, kSPoison = 62 /* [3] ints: 62, 63 */,
-  kOffItems = 512, kOffInfo = 800, kOffXch = 928 /* [2][4][32] */, kOffSum = 1952 /* [2][4][64] */,
-  kOffLref = 4000 /* [2][64] */, kOffRef = 4512 /* [3][64] */, kOffQs = 5280 /* e4m3: [4][64] */, kOffUnset = 6304 /* [2][4] */,
-  kOffFlag = 6336 /* [2][2] */,
+  kBItemEmpty = 50, kBODone = 56, kBDrain = 57, kBGroup = 58 /* 4 */, kSTmem = 62, kSAbort = 63, kSPoison = 64 /* [3] ints: 64, 65 */,
+  kOffItems = 528, kOffInfo = 816, kOffXch = 944 /* [groups][4][rows] */, kOffSum = 1968 /* [2][4][64] */,
+  kOffLref = 4016 /* [2][64] */, kOffRef = 4528 /* [3][64] */, kOffQs = 5296 /* e4m3: [4][64] */,
+  kOffUnset = 6320 /* [groups][4] */, kOffFlag = 6384 /* [groups][2] */,
 };
-static_assert(kOffFlag + 16 <= kMiscBytes, "shared memory");
+static_assert(kOffFlag + 32 <= kMiscBytes, "shared memory");
 static_assert(kOffItems + kItemSlots * (int)sizeof(Item) <= kOffInfo, "item ring");
 
 // ---------------------------------------------------------------- PTX
@@ -425,7 +425,7 @@ __device__ __noinline__ void add_poison(const TcArgs& a, const Item& it, int d) 
 }
 
 template <int D, int N, bool F8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
   using G_ = Geo<D, N, F8>;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 8 * kSTmem);
   Item* items = reinterpret_cast<Item*>(misc + kOffItems);
   uint32_t* info = reinterpret_cast<uint32_t*>(misc + kOffInfo);  // [kInfoSlots][4]: keys without a page
-  float* xch = reinterpret_cast<float*>(misc + kOffXch);          // [2 halves][4 quarters][32]
+  float* xch = reinterpret_cast<float*>(misc + kOffXch);          // [groups][4 quarters][32]
   float* sums = reinterpret_cast<float*>(misc + kOffSum);         // [2][4 quarters][64]: rows' sums of p
   float* lref = reinterpret_cast<float*>(misc + kOffLref);        // [2][64]: their references, as kept
   float* refs = reinterpret_cast<float*>(misc + kOffRef);         // [3][64]
@@ -475,21 +475,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBQEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBLFull + i), 8);
+      mbar_init(bar(kBLFull + i), G_::kSoft);
       mbar_init(bar(kBLEmpty + i), 4);
-      mbar_init(bar(kBGroup + i), 4);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(bar(kBPFull + i), 8);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kBPFull + i), G_::kSoft);
     mbar_init(bar(kBODone), 1);
+    for (int i = 0; i < G_::kGroups; ++i) mbar_init(bar(kBGroup + i), 4);
     for (int i = 0; i < 4; ++i) mbar_init(bar(kBQsFull + i), 1);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(bar(kBItemFull + i), 1);
-      mbar_init(bar(kBItemEmpty + i), 15);  // every warp but the first
+      mbar_init(bar(kBItemEmpty + i), 3 + G_::kSoft + 4);  // every warp but the finder
     }
     mbar_init(bar(kBDrain), 1);
     *abort_flag = 0;
     for (int i = 0; i < 3; ++i) poison[i] = 0;
-    for (int i = 0; i < 4; ++i) reinterpret_cast<volatile int*>(misc + kOffFlag)[i] = 0;
+    for (int i = 0; i < 8; ++i) reinterpret_cast<volatile int*>(misc + kOffFlag)[i] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane < 2)
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // are never read.
         constexpr int KS = G_::kKeyStep;
         const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
-        const uint64_t dp = sdesc(sP + (G_::kPBufs == 2 ? (g & 1) * G_::kPB : 0), kKeys * 128, 1024, 128);
+        const uint64_t dp = sdesc(sP + (g & 1) * G_::kPB, kKeys * 128, 1024, 128);
         const uint32_t to = tmem + G_::kColO + ob * G_::kOCols;
         if (elect_one()) {
           mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv, dp, kIdO, t > 0);
@@ -863,10 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp < 12) {
+  } else if (warp < 4 + G_::kSoft) {
     // ======================= softmax =======================
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int tg = quarter * 32 + lane;  // thread of the half's group: this lane's key in a tile
+    const int quarter = warp & 3, grp = (warp - 4) >> 2;
+    const int tg = quarter * 32 + lane;  // thread of the group: this lane's key in a tile
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     // p may pass 2^0 (e4m3: 2^kUp, times which p is kept) by 2^kTau before a
     // row's reference moves.  bf16 parts keep their precision over the whole
@@ -877,19 +877,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // an e4m3 row's reference is set this far above the largest score seen, so
     // that it rarely has to move again in a chunk
     constexpr float kMargin = F8 ? 2.5f : 0.f;
-    float* xh = xch + half * 128;
-    // A vote of the half's four warps, cast and counted apart so that work can
+    float* xh = xch + grp * 4 * NC;
+    // A vote of the group's four warps, cast and counted apart so that work can
     // go between: count() tells all four alike whether any of them wanted.
-    volatile int* flag = reinterpret_cast<volatile int*>(misc + kOffFlag) + 2 * half;  // [2]: number of the vote that wants
+    volatile int* flag = reinterpret_cast<volatile int*>(misc + kOffFlag) + 2 * grp;  // [2]: number of the vote that wants
     int votes = 0;
     auto cast = [&](bool want) {
       if (lane == 0) {
         if (want) flag[votes & 1] = votes + 1;
-        mbar_arrive(bar(kBGroup + half));
+        mbar_arrive(bar(kBGroup + grp));
       }
     };
     auto count = [&](bool& wanted) -> bool {
-      const bool r = wait_bar(bar(kBGroup + half), votes & 1);
+      const bool r = wait_bar(bar(kBGroup + grp), votes & 1);
       wanted = flag[votes & 1] == votes + 1;
       ++votes;
       return r;
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cast(false);
       return count(w);
     };
-    if (tg < NC) refs[half * 32 + tg] = kUp;  // item 0's
+    if (tg < NC) refs[grp * NC + tg] = kUp;  // item 0's
     Ring ir;
     int g = 0;
     bool ok = sync();
@@ -909,12 +909,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = take(ir, it);
       if (!ok || it.nt == 0) break;
       const int nt = it.nt, rows = it.q_s * G, ctx = it.n - it.q_s;
-      const int ra = it.r0 + half * NC;  // first row of this half
-      const float* qs = qscale + (j % 4) * 64 + half * NC;
+      const int ra = it.r0 + grp * NC;  // first row of this group
+      const float* qs = qscale + (j % 4) * 64 + grp * NC;
       // the rows' references, kept as kUp - reference; the next item's start at
-      // reference 0 (three sets: warps of the half may still read the last item's)
-      float* rh = refs + (j % 3) * 64 + half * 32;
-      if (tg < NC) refs[((j + 1) % 3) * 64 + half * 32 + tg] = kUp;
+      // reference 0 (three sets: warps of the group may still read the last item's)
+      float* rh = refs + (j % 3) * 64 + grp * NC;
+      if (tg < NC) refs[((j + 1) % 3) * 64 + grp * NC + tg] = kUp;
       if (F8) {
         ok = wait_bar(bar(kBQsFull + j % 4), (j >> 2) & 1);
         if (!ok) break;
@@ -922,12 +922,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned long long l2[NC / 2];  // the rows' sums over this lane's keys, in pairs
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) l2[c] = 0ull;
-      uint32_t vmask = 0;  // rows of the half without a reference yet (stored as 0), once the first tile has set them
+      uint32_t vmask = 0;  // rows of the group without a reference yet (stored as 0), once the first tile has set them
       for (int t = 0; t < nt; ++t, ++g) {
         ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
         fence_after();
-        const uint32_t ts = tmem + (g & 1) * N + half * NC + lane_off;  // this tile's q.k of the stored values
+        const uint32_t ts = tmem + (g & 1) * N + grp * NC + lane_off;  // this tile's q.k of the stored values
         const uint4 bad = *reinterpret_cast<const uint4*>(info + (g % kInfoSlots) * 4);
         const int kt = it.k0 + t * kKeys;  // first key of the tile
         const bool masked = kt + kKeys > ctx || (bad.x | bad.y | bad.z | bad.w) != 0;
@@ -959,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ch = lane % kLn, rr = lane / kLn;
           bool found = false;
 #pragma unroll 1
-          for (int b = 0; b < 16; b += kRs) {
-            const int kk = (warp - 4) * 16 + b + rr, ky = kt + kk;
+          for (int b = 0; b < kKeys / G_::kSoft; b += kRs) {
+            const int kk = (warp - 4) * (kKeys / G_::kSoft) + b + rr, ky = kt + kk;
             const uint32_t bm = kk < 32 ? bad.x : kk < 64 ? bad.y : kk < 96 ? bad.z : bad.w;
             const bool gone = ky >= it.k1 || ((bm >> (kk & 31)) & 1u);
             if (!gone && ky < ctx) continue;
@@ -994,23 +994,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t u[8];
           float m = -INFINITY;
           constexpr int kSample = NC / 4 < 8 ? NC / 4 : 8;
-          tm_ld(tmem + (g & 1) * N + lane_off + (half * NC + quarter * (NC / 4)) / 8 * 8, u);
+          tm_ld(tmem + (g & 1) * N + lane_off + (grp * NC + quarter * (NC / 4)) / 8 * 8, u);
           wait_ld();
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const int cc = c - (half * NC + quarter * (NC / 4)) % 8;  // row of the quarter
+            const int cc = c - (grp * NC + quarter * (NC / 4)) % 8;  // row of the quarter
             const float x = redux_max(__uint_as_float(u[c]) * qs[(quarter * (NC / 4)) / 8 * 8 + c]);
             m = lane == cc && cc < kSample ? x : m;
           }
           const bool none = lane < NC / 4 && m == -INFINITY;
           if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - kMargin - m;
           const uint32_t unset = __ballot_sync(0xffffffffu, none) << (quarter * (NC / 4));
-          if (lane == 0) unset4[half * 4 + quarter] = unset;
+          if (lane == 0) unset4[grp * 4 + quarter] = unset;
           __syncwarp();
           cast(unset != 0);
           bool some;
           if (!count(some)) { ok = false; break; }
-          if (some) vmask = unset4[half * 4] | unset4[half * 4 + 1] | unset4[half * 4 + 2] | unset4[half * 4 + 3];
+          if (some) vmask = unset4[grp * 4] | unset4[grp * 4 + 1] | unset4[grp * 4 + 2] | unset4[grp * 4 + 3];
         }
         // first try: all of the tile's work against the references there are;
         // careful: new references; last: the work against those
@@ -1095,13 +1095,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m = redux_max(y[c]);  // NaN is passed over
             mine = lane == c ? m : mine;
           }
-          if (lane < NC) xh[quarter * 32 + lane] = mine;
+          if (lane < NC) xh[quarter * NC + lane] = mine;
           if (!sync()) { ok = false; break; }
           // lane c: row c's new reference; the stored value is kUp - reference
           float alpha = 1.f, nref = 0.f;
           bool moved = false, none = false;
           if (lane < NC) {
-            const float top = fmaxf(fmaxf(xh[lane], xh[32 + lane]), fmaxf(xh[64 + lane], xh[96 + lane]));
+            const float top = fmaxf(fmaxf(xh[lane], xh[NC + lane]), fmaxf(xh[2 * NC + lane], xh[3 * NC + lane]));
             const float old = rh[lane];
             nref = old;
             if ((t == 0 && (!F8 || masked)) || ((vmask >> lane) & 1u)) {  // none yet, 0 stands in
@@ -1118,14 +1118,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           // every warp has read the references
           if (!sync()) { ok = false; break; }
           if (quarter == 0 && lane < NC) rh[lane] = nref;
-          if (any) {  // the same in the half's four warps
+          if (any) {  // the same in the group's four warps
 #pragma unroll
             for (int c = 0; c < NC; c += 2)
               l2[c / 2] = mul2(l2[c / 2], pk2(__shfl_sync(0xffffffffu, alpha, c), __shfl_sync(0xffffffffu, alpha, c + 1)));
             // t > 0: every P V so far has run after this wait
             if (!wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
             fence_after();
-            const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + half * NC;
+            const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + grp * NC;
 #pragma unroll 1
             for (int b = 0; b < NC; b += 8) {
               uint32_t o[8], o2[8];
@@ -1150,13 +1150,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < NC; c += 2) l2[c / 2] = add2(l2[c / 2], pk2(y[c], y[c + 1]));
-        // the buffer is free once P V of the tile that last used it has run: the
-        // previous one, or, with two buffers, the one before it, which this
-        // tile's S came after
-        if (G_::kPBufs == 1 && g > 0 && !wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
+        // the P buffer is free: P V of the tile before the last came before this tile's S
         auto put = [&](const uint32_t* x, int col) {  // NC columns of this key's row, from column col
           const int at = col * G_::kEs;               // byte in the row
-          const uint32_t base = sP + (G_::kPBufs == 2 ? (g & 1) * G_::kPB : 0) + (at >> 7) * (kKeys * 128);
+          const uint32_t base = sP + (g & 1) * G_::kPB + (at >> 7) * (kKeys * 128);
           if constexpr (NC * G_::kEs == 8) {
             st_s64(base + swz<128>(tg, (at & 127) >> 4) + (at & 8), x[0], x[1]);
           } else {
@@ -1165,8 +1162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               st_s128(base + swz<128>(tg, ((at & 127) >> 4) + q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           }
         };
-        put(hi, half * NC);
-        put(lo, N + half * NC);
+        put(hi, grp * NC);
+        put(lo, N + grp * NC);
         fence_proxy_async_smem();
         fence_before();
         __syncwarp();
@@ -1180,8 +1177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; c += 2) up2(l2[c / 2], m[c], m[c + 1]);
         const float mine = col_sum<NC>(m, lane);
-        const int at = (j & 1) * 64 + half * NC;
-        if (lane % (32 / NC) == 0) sums[(j & 1) * 256 + quarter * 64 + half * NC + lane / (32 / NC)] = mine;
+        const int at = (j & 1) * 64 + grp * NC;
+        if (lane % (32 / NC) == 0) sums[(j & 1) * 256 + quarter * 64 + grp * NC + lane / (32 / NC)] = mine;
         if (tg < NC) lref[at + tg] = rh[tg];
       }
       __syncwarp();
@@ -1212,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* q = sums + (j & 1) * 256 + c;
         const float l = (q[0] + q[64]) + (q[128] + q[192]);
         inv[k] = l == 0.f ? 0.f : p.v_scale / l;
-        if (warp == 12 && it.nchunks > 1 && r < rows && lane + 32 * k < N) {
+        if (warp == 4 + G_::kSoft && it.nchunks > 1 && r < rows && lane + 32 * k < N) {
           const int i = quot(r, a.by_g);
           a.part_lse[((int64_t)it.s * a.rows_per_seq + i * it.nchunks + it.c) * p.Hq + it.h * G + r - i * G] =
               l == 0.f ? -INFINITY : __log2f(l) - lref[(j & 1) * 64 + (c / NC) * NC + c % NC];  // reference + log2(sum) - kUp
@@ -1405,7 +1402,7 @@ cudaError_t launch_t(TcArgs a, int64_t max_items, int num_sms, cudaStream_t st) 
   cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kern), G_::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(num_sms, max_items);
-  return launch_ex(kern, dim3((unsigned)grid), dim3(kThreads), G_::kSmem, st, true, a, mk, mv);
+  return launch_ex(kern, dim3((unsigned)grid), dim3(G_::kThreads), G_::kSmem, st, true, a, mk, mv);
 }
 
 }  // namespace
