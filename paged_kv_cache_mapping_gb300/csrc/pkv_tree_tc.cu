@@ -229,17 +229,19 @@ __device__ __forceinline__ uint64_t l2_normal_policy() {
   return pol;
 }
 
-// A bounded wait, at most 2^20 tries (tens of milliseconds and more; a try
-// suspends the warp for a while), and the same by a whole warp.  The code is
-// kept short, here and below: sixteen warps in six roles share the SM's
-// instruction cache, and while the roles' code did not fit (105 to 166 KB in
-// all, 42 % of its requests missed) it set the pace, not the pipes.
+// A bounded wait, and the same by a whole warp: at most 2^18 tries, each of
+// which may suspend the warp for up to 20 us (5 s in all).  Without the time
+// hint a try comes back after some tens of clocks, and the waiting warps' tries
+// took half of the SM's issue slots.  The code is kept short, here and below:
+// sixteen and more warps in six roles share the SM's instruction cache, and
+// while the roles' code did not fit (105 to 166 KB in all, 42 % of its requests
+// missed) it set the pace, not the pipes.
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-      "W:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
-      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 1048576;\n\t@q bra W;\n"
+      "W:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t@p bra D;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 262144;\n\t@q bra W;\n"
       "D:\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -900,6 +902,9 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
       cast(false);
       return count(w);
     };
+    // this lane's row of P, at the first of the warp's columns in the hi part; a
+    // further 16-byte chunk's place, and the lo part's, differ by an exclusive or
+    const uint32_t p_at = sP + swz<128>(tg, grp * NC * G_::kEs / 16) + (grp * NC * G_::kEs) % 16;
     if (tg < NC) refs[grp * NC + tg] = kUp;  // item 0's
     Ring ir;
     int g = 0;
@@ -1082,9 +1087,11 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
               }
             }
             if (mode == kLast) break;
-            bool wanted;
-            ok = count(wanted);
-            if (!ok || !wanted) break;
+            const bool in = poll(bar(kBGroup + grp), votes & 1), calm = flag[votes & 1] != votes + 1;
+            ++votes;
+            if (__all_sync(0xffffffffu, in && calm)) break;
+            ok = __all_sync(0xffffffffu, in);
+            if (!ok) break;
             mode = kCareful;
             continue;
           }
@@ -1151,19 +1158,19 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; c += 2) l2[c / 2] = add2(l2[c / 2], pk2(y[c], y[c + 1]));
         // the P buffer is free: P V of the tile before the last came before this tile's S
-        auto put = [&](const uint32_t* x, int col) {  // NC columns of this key's row, from column col
-          const int at = col * G_::kEs;               // byte in the row
-          const uint32_t base = sP + (g & 1) * G_::kPB + (at >> 7) * (kKeys * 128);
+        {
+          const uint32_t at = p_at + (g & 1) * G_::kPB, at_lo = G_::kPRow == 256 ? at + kKeys * 128 : at ^ (N * G_::kEs);
           if constexpr (NC * G_::kEs == 8) {
-            st_s64(base + swz<128>(tg, (at & 127) >> 4) + (at & 8), x[0], x[1]);
+            st_s64(at, hi[0], hi[1]);
+            st_s64(at_lo, lo[0], lo[1]);
           } else {
 #pragma unroll
-            for (int q = 0; q < NC * G_::kEs / 16; ++q)
-              st_s128(base + swz<128>(tg, ((at & 127) >> 4) + q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            for (int q = 0; q < NC * G_::kEs / 16; ++q) {
+              st_s128(at ^ (q << 4), hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+              st_s128(at_lo ^ (q << 4), lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+            }
           }
-        };
-        put(hi, grp * NC);
-        put(lo, N + grp * NC);
+        }
         fence_proxy_async_smem();
         fence_before();
         __syncwarp();
