@@ -1,21 +1,26 @@
-"""Build libpkv.so in-tree for sm_103a (GB300).
+"""Build libpkv.so and its Python binding in-tree for sm_103a (GB300).
 
 Each CUDA translation unit under csrc/ is compiled with nvcc in parallel,
 then linked into paged_kv_cache_mapping_gb300/libpkv.so (static CUDA
 runtime, so the library loads without a GPU; the driver is opened at the
-first CUDA call).  Run ``python -m paged_kv_cache_mapping_gb300.build``.
+first CUDA call).  Beside them g++ compiles csrc/pkv_binding.cpp, the CPython
+module that marshals PyTorch tensors for the calls made once per layer of a
+speculative step.  Run ``python -m paged_kv_cache_mapping_gb300.build``.
 """
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
+BINDING_SRC = os.path.join(CSRC, "pkv_binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["pkv_api.cu", "pkv_append.cu", "pkv_plan.cu", "pkv_decode.cu", "pkv_prefill.cu", "pkv_f32.cu", "pkv_static_ws.cu", "pkv_prefill_tc.cu", "pkv_blocks.cu",
            "pkv_spec_api.cu", "pkv_rope.cu", "pkv_tree.cu", "pkv_tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -28,6 +33,19 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def binding_command(out: str):
+    """g++ on the binding, against the headers and libraries of the PyTorch that is installed."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    system = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{os.path.join(ROOT, 'include')}",
+            *(f"-isystem{d}" for d in system), BINDING_SRC, "-o", out, f"-L{os.path.join(root, 'lib')}",
+            f"-Wl,-rpath,{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 def _stale(out, deps):
@@ -51,7 +69,11 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             if ptxas_info:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    bind_tmp = BINDING + f".tmp{os.getpid()}"
+    new_binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pkv.h"), __file__])
+    if new_binding:
+        jobs.append(binding_command(bind_tmp))
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
     failed = False
     for cmd, r in zip(jobs, results):
@@ -59,8 +81,10 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         failed |= r.returncode != 0
     if failed:
-        raise RuntimeError("nvcc failed")
-    if force or jobs or _stale(LIB, objs):
+        raise RuntimeError("the compiler failed")
+    if new_binding:
+        os.replace(bind_tmp, BINDING)
+    if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)

@@ -1,21 +1,19 @@
 """Binding of the speculative decoding entry points (include/pkv.h): rotary
 append, tree mask, tree attention and path commit.
 
-Like the rest of the binding it only marshals arguments.  These calls are
-made once per layer of a step whose kernels take a few microseconds, so the
-tensors of a call are packed into one preallocated buffer per thread.
+Like the rest of the binding it only marshals arguments.  The calls that a
+step makes once per layer, whose kernels take a few microseconds, go through
+the compiled module csrc/pkv_binding.cpp; the others through ctypes.
 """
 import ctypes
-import struct
-import threading
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
-from . import _DT, PkvError, _check, load_library
+from . import PkvError, _check, _tensor, load_library
 
-_TENSOR = struct.Struct("=Qii8q")  # pkv_tensor: data, dtype, ndim, shape[4], stride[4]
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
-_MAX_TENSORS = 12
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "smooth": 4}
 
 
@@ -32,18 +30,13 @@ class _RopeParams(ctypes.Structure):
                 ("attention_factor", ctypes.c_double)]
 
 
-class _Buffer(threading.local):
-    def __init__(self):
-        self.buf = ctypes.create_string_buffer(_TENSOR.size * _MAX_TENSORS)
-        at = ctypes.addressof(self.buf)
-        self.at = [at + _TENSOR.size * i for i in range(_MAX_TENSORS)]
-
-
-_buffer = _Buffer()
+_BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 _ready = None
+_calls = None
 
 
 def _lib():
+    """The library with the argument types of these entry points."""
     global _ready
     if _ready is None:
         lib = load_library()
@@ -60,42 +53,21 @@ def _lib():
     return _ready
 
 
-def _pack(*tensors):
-    """Descriptors of (name, tensor) pairs, all on one CUDA device: that
-    device's index and the addresses of the descriptors."""
-    b = _buffer
-    dev = -1
-    for k, (name, t) in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        d = t.get_device()
-        if d != dev or d < 0:
-            if d < 0:
-                raise PkvError(1, f"{name} must be a CUDA tensor (there is no CPU path)")
-            if k:
-                raise PkvError(1, f"{name} is on cuda:{d}, {tensors[0][0]} on cuda:{dev}")
-            dev = d
-        shape = t.shape
-        n = len(shape)
-        if n > 4:
-            raise PkvError(1, f"{name} has more than 4 dimensions")
-        dt = _DT.get(t.dtype)
-        if dt is None:
-            raise PkvError(2, f"{name}: unsupported dtype {t.dtype}")
-        pad = _PAD[n]
-        _TENSOR.pack_into(b.buf, k * _TENSOR.size, t.data_ptr(), dt, n, *shape, *pad, *t.stride(), *pad)
-    return dev, b.at
-
-
-def _call(dev, fn, *args):
-    """fn(*args, stream) on dev's current stream, with dev current."""
-    if torch.cuda.current_device() == dev:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    if rc:
-        _check(rc)
+def _binding():
+    """The compiled marshalling module, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        lib = _lib()
+        if not os.path.exists(_BINDING_PATH):
+            raise PkvError(-1, f"{_BINDING_PATH} is missing: build it with "
+                               "`python -m paged_kv_cache_mapping_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", _BINDING_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(m)
+        at = lambda fn: ctypes.cast(fn, ctypes.c_void_p).value  # noqa: E731
+        m.bind(PkvError, at(lib.pkv_rope_append), at(lib.pkv_tree_mask), at(lib.pkv_tree_attention), at(lib.pkv_tree_commit))
+        _calls = m
+    return _calls
 
 
 def pkv_rope_init(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
@@ -119,30 +91,26 @@ def pkv_rope_append(q, k, v, positions, slot_mapping, rope: Rope, k_cache, v_cac
     into their slots, and returns the rotated q (q_out, or a new tensor)."""
     if q_out is None:
         q_out = torch.empty_like(q)
-    dev, a = _pack(("q", q), ("k", k), ("v", v), ("positions", positions), ("slot_mapping", slot_mapping),
-                   ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache))
-    _call(dev, _lib().pkv_rope_append, a[0], a[1], a[2], a[3], a[4], rope, a[5], a[6], a[7], k_scale, v_scale)
+    rc = (_calls or _binding()).rope_append(q, k, v, positions, slot_mapping, rope, q_out, k_cache, v_cache, k_scale, v_scale)
+    if rc:
+        _check(rc)
     return q_out
 
 
 def pkv_tree_mask(parents, cu_seqlens_q, seq_lens, max_q_len: int, tree_mask=None, positions=None):
     """Mask words [T, ceil(max_q_len / 32)] and rotary positions [T] (int32) of
     drafted trees given as parent indices [T]."""
-    if tree_mask is None:
-        tree_mask = torch.empty((parents.shape[0], max(1, -(-int(max_q_len) // 32))), dtype=torch.int32,
-                                device=parents.device)
-    if positions is None:
-        positions = torch.empty_like(parents)
-    dev, a = _pack(("parents", parents), ("cu_seqlens_q", cu_seqlens_q), ("seq_lens", seq_lens),
-                   ("tree_mask", tree_mask), ("positions", positions))
-    _call(dev, _lib().pkv_tree_mask, a[0], a[1], a[2], a[3], a[4])
+    rc, tree_mask, positions = (_calls or _binding()).tree_mask(parents, cu_seqlens_q, seq_lens, max_q_len, tree_mask,
+                                                                positions)
+    if rc:
+        _check(rc)
     return tree_mask, positions
 
 
 def pkv_tree_attention_workspace_size(q, block_tables, k_cache, max_q_len: int = 0) -> int:
-    _, a = _pack(("q", q), ("block_tables", block_tables), ("k_cache", k_cache))
+    a = [_tensor(q, "q"), _tensor(block_tables, "block_tables"), _tensor(k_cache, "k_cache")]
     n = ctypes.c_size_t(0)
-    _check(_lib().pkv_tree_attention_workspace_size(a[0], a[1], a[2], int(max_q_len), ctypes.byref(n)))
+    _check(_lib().pkv_tree_attention_workspace_size(*(ctypes.addressof(t) for t in a), int(max_q_len), ctypes.byref(n)))
     return int(n.value)
 
 
@@ -153,12 +121,10 @@ def pkv_tree_attention(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache
     if workspace is None:
         workspace = torch.empty(pkv_tree_attention_workspace_size(q, block_tables, k_cache, max_q_len),
                                 dtype=torch.uint8, device=q.device)
-    dev, a = _pack(("q", q), ("cu_seqlens_q", cu_seqlens_q), ("seq_lens", seq_lens), ("block_tables", block_tables),
-                   ("k_cache", k_cache), ("v_cache", v_cache), ("tree_mask", tree_mask), ("out", out))
-    if workspace.get_device() != dev:
-        raise PkvError(1, f"workspace must be on cuda:{dev}")
-    _call(dev, _lib().pkv_tree_attention, a[0], a[1], a[2], a[3], a[4], a[5], a[6], scale, k_scale, v_scale,
-          int(max_q_len), a[7], workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    rc = (_calls or _binding()).tree_attention(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, tree_mask, scale,
+                                               k_scale, v_scale, max_q_len, out, workspace)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -169,8 +135,8 @@ def pkv_tree_commit(accepted, accepted_lens, cu_seqlens_q, seq_lens, block_table
     new lengths [B]."""
     if new_seq_lens is None:
         new_seq_lens = torch.empty_like(seq_lens)
-    dev, a = _pack(("accepted", accepted), ("accepted_lens", accepted_lens), ("cu_seqlens_q", cu_seqlens_q),
-                   ("seq_lens", seq_lens), ("block_tables", block_tables), ("k_cache", k_cache),
-                   ("v_cache", v_cache), ("new_seq_lens", new_seq_lens))
-    _call(dev, _lib().pkv_tree_commit, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7])
+    rc = (_calls or _binding()).tree_commit(accepted, accepted_lens, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache,
+                                            new_seq_lens)
+    if rc:
+        _check(rc)
     return new_seq_lens

@@ -138,4 +138,4 @@ def test_binding_refuses_cpu_tensors_and_bad_types():
         with pytest.raises(pkv.PkvError):
             call()
     with pytest.raises(TypeError):
-        spec._pack(("x", [1]))
+        pkv.pkv_tree_mask([0], i, i, 1, tree_mask=i, positions=i)
