@@ -801,20 +801,29 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
       // its query rows; the buffer is free once the scores of the item that
       // used it last are there
       const int qb = qbuf(j), rows = it.q_s * G;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ch * 8;
       const uint32_t dst = sQ + qb * G_::kQB;
+      // lane c (and c + 32) finds row c; 0: past the last
+      unsigned long long row[(N + 31) / 32];
+#pragma unroll
+      for (int k = 0; k < (N + 31) / 32; ++k) {
+        const int r = it.r0 + lane + 32 * k, i = quot(r, a.by_g);
+        const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(p.q) + (it.t0 + i) * p.q_st + (it.h * G + r - i * G) * p.q_sh;
+        row[k] = r < rows ? reinterpret_cast<unsigned long long>(at) : 0;
+      }
       ok = wait_bar(bar(kBQEmpty + qb), qpass(j) ^ 1);
       if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < (N + 31) / 32; ++k)
 #pragma unroll 4
-      for (int b = 0; b < kStepsQ; ++b) {
-        const int rt = b * kPer + rr, r = it.r0 + rt, i = quot(r, a.by_g);  // row of the tile, of the sequence; its node
-        const __nv_bfloat16* src = q + (it.t0 + i) * p.q_st + (it.h * G + r - i * G) * p.q_sh;
-        // straight to shared memory; a row past the last is zeros
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (ch * 16 / AT) * N * AT +
-                                                                            swz<AT>(rt, ch % (AT / 16))),
-                     "l"(r < rows ? src : q), "r"(r < rows ? 16 : 0)
-                     : "memory");
-      }
+        for (int b = 0; b < (N < 32 ? N : 32); b += kPer) {
+          const int rt = 32 * k + b + rr;  // row of the tile
+          const unsigned long long src = __shfl_sync(0xffffffffu, row[k], b + rr);
+          // straight to shared memory; a row past the last is zeros
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (ch * 16 / AT) * N * AT +
+                                                                              swz<AT>(rt, ch % (AT / 16))),
+                       "l"(src ? src + ch * 16 : reinterpret_cast<unsigned long long>(p.q)), "r"(src ? 16 : 0)
+                       : "memory");
+        }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
       if constexpr (F8) {
