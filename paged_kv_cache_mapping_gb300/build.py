@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libpkv.so")
 BINDING_SRC = os.path.join(CSRC, "pkv_binding.cpp")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["pkv_api.cu", "pkv_append.cu", "pkv_plan.cu", "pkv_decode.cu", "pkv_prefill.cu", "pkv_f32.cu", "pkv_static_ws.cu", "pkv_prefill_tc.cu", "pkv_blocks.cu",
-           "pkv_spec_api.cu", "pkv_rope.cu", "pkv_tree.cu", "pkv_tree_tc.cu"]
+           "pkv_spec_api.cu", "pkv_rope.cu", "pkv_tree.cu", "pkv_tree_tc.cu", "pkv_tree_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}"]

@@ -116,7 +116,7 @@ cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st);
 // sequence's nodes; max_ctx: tokens a block table can hold.  The workspace
 // holds tree_tc_rows_per_seq() partial rows (D + 1 floats per head) for each
 // sequence.
-int64_t tree_tc_rows_per_seq(int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_ctx);
+int64_t tree_tc_rows_per_seq(int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_ctx, bool f8);
 cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t max_q, int64_t max_ctx, void* workspace,
                            int num_sms, cudaStream_t st);
 

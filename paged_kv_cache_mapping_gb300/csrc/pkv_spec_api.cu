@@ -287,7 +287,7 @@ pkv_status pkv_tree_attention_workspace_size(const pkv_tensor* q, const pkv_tens
   if (k_cache->dtype == PKV_F32) return PKV_OK;
   const int64_t B = block_tables->shape[0], Hkv = k_cache->shape[2], G = Hkv > 0 ? q->shape[1] / Hkv : 1;
   const int64_t rows = B * tree_tc_rows_per_seq(B, Hkv, G, max_nodes_of(max_q_len, q->shape[0]),
-                                                block_tables->shape[1] * k_cache->shape[1]);
+                                                block_tables->shape[1] * k_cache->shape[1], k_cache->dtype == PKV_FP8_E4M3);
   *bytes = align_up(sizeof(float) * rows * q->shape[1] * (q->shape[2] + 1), 256);
   return PKV_OK;
 }

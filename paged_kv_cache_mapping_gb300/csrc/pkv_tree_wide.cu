@@ -1,0 +1,486 @@
+// pkv_tree_wide.cu -- attention of wide drafted trees (more than 64 query rows
+// for each KV head) over bf16 caches, on the fifth-generation tensor cores.
+//
+// What it computes is what pkv_tree_tc.cu computes, over the same items; here a
+// tile holds 128 query rows, enough to fill the MMA's M side, and the products
+// stand the usual way round:
+//     S = Q K^T     (M 128 rows, N 128 keys, K = D)
+//     O += P V      (M 128 rows, N = D, K 128 keys; P as bf16 hi + lo)
+// With 64 rows the other form moves 48 KB of operands through shared memory for
+// every 64 rows and 128 keys of K, V and P; here P stays in tensor memory, where
+// it replaces S, and K and V tiles serve twice the rows.
+//
+// Softmax: two groups of four warps take the tiles in turn, group g & 1 tile g,
+// and a thread owns a row: its largest score, its sum, and an accumulator of O of
+// its group's own.  So there is nothing to agree on between threads: a row's
+// reference moves (when its largest score passes it by 2^kTau) and its O is
+// rescaled by the one thread that holds it.  The two groups' O are joined where
+// the item is written, each with weight 2^(reference - larger reference).  S is
+// read twice, for the largest score and for P, since 128 scores do not fit a
+// thread's registers beside the rest.
+//
+// Bound: the tensor cores.  A tile of 128 rows and 128 keys at D 128 takes 4.2
+// MFLOP for S and 8.4 for the two parts of P, about 1,540 clocks.
+//
+// CTA: 16 warps: K, MMA, items and query rows, V, 2 x 4 of softmax, 4 that write.
+#include "pkv_tree_tc.cuh"
+
+namespace pkv {
+namespace {
+
+template <int D>
+struct Wide {
+  static constexpr int kD = D, kN = 128;
+  static constexpr bool kF8 = false;
+  static constexpr int kEs = 2, kRowB = 2 * D, kAtomB = 128;
+  static constexpr int kSub = kRowB / kAtomB;
+  static constexpr int kTileB = kKeys * kRowB;
+  static constexpr int kNK = D == 128 ? 2 : 4, kNV = kNK;
+  static constexpr int kQB = kN * kRowB;
+  static constexpr int kQBufs = 2;
+  __device__ static int qbuf(int j) { return j & 1; }
+  __device__ static uint32_t qpass(int j) { return (uint32_t)(j >> 1) & 1u; }
+  static constexpr int kSoft = 8;  // softmax warps
+  static constexpr int kThreads = 32 * (4 + kSoft + 4);
+  static constexpr int kOffK = 0, kOffV = kNK * kTileB, kOffQ = kOffV + kNV * kTileB, kOffMisc = kOffQ + kQBufs * kQB;
+  static constexpr int kSmem = kOffMisc + kMiscBytes;
+  // tensor memory: S and then P of the tile in hand, for each group; then the
+  // groups' O, twice where two fit
+  static constexpr int kOBufs = D == 128 ? 1 : 2;
+  static constexpr uint32_t kColO = 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kColO + kOBufs * 2 * D <= 512, "tensor memory");
+  static_assert(kNK + 2 <= kInfoSlots, "tile info ring");
+};
+
+// kBPFull + group: P of a tile's keys 0 .. 63; kBPRest + group: of the rest
+enum : int { kBPRest = kBGroup, kOffStat = kOffOwn /* [2][2 groups][128] sum and reference */ };
+static_assert(kOffStat + 2 * 2 * 128 * 8 <= kMiscBytes, "shared memory");
+
+// kSteps k steps of 16 keys with A in tensor memory: 8 columns for the hi part,
+// and 8 for the lo part 16 columns on
+template <int kSteps>
+__device__ __forceinline__ void mma_p_steps(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                   "r"(a + (k >> 1) * 32 + (k & 1) * 8 + part * 16), "l"(b + k * 128), "r"(id), "r"(k || part ? 1u : acc));
+}
+
+__device__ __forceinline__ void tm_st(uint32_t a, const uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(a),
+      "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]),
+      "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]));
+}
+
+// A drafted key's V value is not finite: the softmax warps took it out of the
+// product, and here it goes to the row of this thread if that sees the key, on
+// top of what this thread has just stored.
+template <int D>
+__device__ __noinline__ void add_poison_row(const TcArgs& a, const Item& it, int r) {
+  const TreeParams& p = a.p;
+  const int ctx = it.n - it.q_s, i = r / p.G, hq = it.h * p.G + r - i * p.G;
+  for (int k = max(ctx, it.k0); k < it.k1; ++k) {
+    const int lb = k / p.bs, jj = k - ctx;
+    const int32_t blk = __ldg(p.bt + (int64_t)it.s * p.bt_stride + lb);
+    if ((uint32_t)blk >= (uint64_t)p.num_blocks) continue;
+    if (!((static_cast<uint32_t>(__ldg(p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj >> 5))) >> (jj & 31)) & 1u)) continue;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) + (((int64_t)blk * p.bs + (k - lb * p.bs)) * p.Hkv + it.h) * D;
+    for (int d = 0; d < D; ++d) {
+      const float x = __bfloat162float(v[d]);
+      if (fabsf(x) < INFINITY) continue;
+      if (it.nchunks > 1) {
+        a.part_o[(((int64_t)it.s * a.rows_per_seq + (int64_t)i * it.nchunks + it.c) * p.Hq + hq) * D + d] += x;
+      } else {
+        const int64_t at = (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh + d;
+        if (a.out_bf16) {
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + at;
+          *y = __float2bfloat16_rn(__bfloat162float(*y) + x);
+        } else {
+          static_cast<float*>(p.out)[at] += x;
+        }
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(Wide<D>::kThreads, 1)
+    tree_wide_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v) {
+  using G_ = Wide<D>;
+  constexpr int NK = G_::kNK, NV = G_::kNV, AT = G_::kAtomB;
+  const TreeParams& p = a.p;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* misc = smem + G_::kOffMisc;
+  const uint32_t s0 = smem_u32(smem), b0 = smem_u32(misc);
+  auto bar = [&](int i) -> uint32_t { return b0 + 8 * i; };
+  const uint32_t sK = s0 + G_::kOffK, sV = s0 + G_::kOffV, sQ = s0 + G_::kOffQ;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 8 * kSAbort);
+  volatile int* poison = reinterpret_cast<volatile int*>(misc + 8 * kSPoison);  // [3]: item + 1
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 8 * kSTmem);
+  uint32_t* info = reinterpret_cast<uint32_t*>(misc + kOffInfo);
+  float2* stat = reinterpret_cast<float2*>(misc + kOffStat);
+  // as in the narrow kernel: the warp index, and so a role, is the warp's
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int G = p.G;
+  const Cta cta{b0, abort_flag, reinterpret_cast<Item*>(misc + kOffItems), info, lane};
+
+  if (s0 & 1023) {  // the swizzled tiles need their base on 1024 bytes
+    if (threadIdx.x == 0) atomicOr(p.err, kErrWaitTimeout);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(bar(kBKFull + i), 1);
+      mbar_init(bar(kBKEmpty + i), 1);
+      mbar_init(bar(kBVFull + i), 1);
+      mbar_init(bar(kBVEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBSFull + i), 2);
+      mbar_init(bar(kBPFull + i), 4);
+      mbar_init(bar(kBPRest + i), 4);
+      mbar_init(bar(kBOFull + i), 1);
+      mbar_init(bar(kBOFree + i), 4);
+      mbar_init(bar(kBQFull + i), 1);
+      mbar_init(bar(kBQEmpty + i), 1);
+      mbar_init(bar(kBLFull + i), G_::kSoft);
+      mbar_init(bar(kBLEmpty + i), 4);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(bar(kBItemFull + i), 1);
+      mbar_init(bar(kBItemEmpty + i), 3 + G_::kSoft + 4);  // every warp but the finder
+    }
+    mbar_init(bar(kBDrain), 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 3; ++i) poison[i] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tm_v : &tm_k)) : "memory");
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tslot;
+  grid_dep_wait();
+  launch_dependents();
+
+  // item j's O buffer, and the parity of its pass
+  auto obuf = [](int j) { return G_::kOBufs == 2 ? j & 1 : 0; };
+  auto opass = [](int j) { return (uint32_t)(G_::kOBufs == 2 ? j >> 1 : j) & 1u; };
+
+  if (warp == 0 || warp == 3) {
+    copy_tiles<G_>(a, cta, warp == 3, warp == 3 ? sV : sK, warp == 3 ? &tm_v : &tm_k);
+  } else if (warp == 1) {
+    // ======================= MMA =======================
+    constexpr uint32_t kIdS = idesc(128, false, false, false), kIdO = idesc(D, false, false, true);
+    Ring ir, kr, vr;
+    int j = 0, g = 0, nt = 0;
+    // S of tile gg from the next K tile.  Its group's P of the tile before last
+    // stands there until that P V, issued earlier, has run.
+    auto issue_s = [&](int gg, int qb) -> bool {
+      if (!wait_bar(bar(kBKFull) + 8 * kr.at, kr.pass)) return false;
+      fence_after();
+      const uint64_t dk = sdesc(sK + kr.at * G_::kTileB, 16, 8 * AT, AT);
+      const uint64_t dq = sdesc(sQ + qb * G_::kQB, 16, 8 * AT, AT);
+      if (elect_one()) {
+#pragma unroll
+        for (int u = 0; u < G_::kSub; ++u)
+          mma_steps<false, 4, 2, 2>(tmem + (gg & 1) * 128, dq + (uint32_t)(u * 128 * AT >> 4), dk + (uint32_t)(u * kKeys * AT >> 4),
+                                    kIdS, u != 0);
+        commit(bar(kBSFull + (gg & 1)));
+        commit(bar(kBKEmpty) + 8 * kr.at);
+        // the second arrival hands on what the tile's producer wrote (info)
+        mbar_arrive(bar(kBSFull + (gg & 1)));
+      }
+      __syncwarp();
+      kr.next(NK);
+      return true;
+    };
+    bool ok = true;
+    for (int t = 0;; ++t, ++g) {  // t: tile of item j - 1, whose S has been issued
+      if (t == nt - 1 && elect_one()) commit(bar(kBQEmpty + G_::qbuf(j - 1)));
+      int nt2 = nt;
+      if (t + 1 >= nt) {  // the tile whose S goes next is the next item's first
+        Item it;
+        ok = cta.take(ir, it);
+        nt2 = it.nt;
+        if (!ok || (nt2 == 0 && nt == 0)) break;
+        ok = nt2 == 0 || wait_bar(bar(kBQFull + G_::qbuf(j)), G_::qpass(j));
+        if (!ok) break;
+      }
+      const int gs = nt == 0 ? g : g + 1, qb = G_::qbuf(t + 1 >= nt ? j : j - 1);
+      if (nt2 > 0 || t + 1 < nt) ok = issue_s(gs, qb);
+      if (nt > 0 && ok) {
+        const int ob = obuf(j - 1), grp = g & 1;
+        ok = wait_bar(bar(kBVFull) + 8 * vr.at, vr.pass) && (t > 1 || wait_bar(bar(kBOFree + ob), opass(j - 1) ^ 1)) &&
+             wait_bar(bar(kBPFull + grp), (g >> 1) & 1);
+        if (!ok) break;
+        fence_after();
+        // V: d contiguous, 8 keys = 8 AT bytes, sub-tiles of d kKeys AT apart
+        const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
+        const uint32_t tp = tmem + grp * 128, to = tmem + G_::kColO + (ob * 2 + grp) * D;
+        if (elect_one()) mma_p_steps<4>(to, tp, dv, kIdO, t > 1);
+        __syncwarp();
+        ok = wait_bar(bar(kBPRest + grp), (g >> 1) & 1);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          mma_p_steps<4>(to, tp + 64, dv + 4 * 128, kIdO, 1);
+          commit(bar(kBVEmpty) + 8 * vr.at);
+          if (t + 1 == nt) commit(bar(kBOFull + ob));
+        }
+        __syncwarp();
+        vr.next(NV);
+      }
+      if (!ok) break;
+      if (t + 1 >= nt) {
+        if (nt == 0) --g;  // no tile was finished
+        if (nt2 == 0) break;
+        nt = nt2;
+        t = -1;
+        ++j;
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    // every MMA issued so far is finished before TMEM is freed
+    if (elect_one()) commit(bar(kBDrain));
+    __syncwarp();
+    wait_bar(bar(kBDrain), 0);
+  } else if (warp == 2) {
+    find_items<G_>(a, cta, sQ, nullptr);
+  } else if (warp < 4 + G_::kSoft) {
+    // ======================= softmax: lane = row =======================
+    const int quarter = warp & 3, grp = (warp - 4) >> 2, row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const uint32_t ts = tmem + grp * 128 + lane_off;
+    // p may pass 1 by 2^kTau before a row's reference moves; bf16 parts keep
+    // their precision over the whole exponent range
+    constexpr float kTau = 16.f;
+    const unsigned long long scale2 = pk2(p.qk_scale_log2, p.qk_scale_log2);
+    Ring ir;
+    int g = 0;  // first tile of the item
+    bool ok = true;
+    for (int j = 0;; ++j) {
+      Item it;
+      ok = cta.take(ir, it);
+      if (!ok || it.nt == 0) break;
+      const int nt = it.nt, ctx = it.n - it.q_s, r = it.r0 + row;
+      float ref = -INFINITY;  // none yet
+      unsigned long long l2 = 0ull;
+      for (int t = (g ^ grp) & 1; t < nt; t += 2) {
+        const int gg = g + t;
+        ok = wait_bar(bar(kBSFull + grp), (gg >> 1) & 1);
+        if (!ok) break;
+        fence_after();
+        const uint4 bad = *reinterpret_cast<const uint4*>(info + (gg % kInfoSlots) * 4);
+        const int kt = it.k0 + t * kKeys;  // first key of the tile
+        const bool masked = kt + kKeys > ctx || (bad.x | bad.y | bad.z | bad.w) != 0;
+        if (masked) {
+          // scores that this row does not see become -inf, in place
+          const int i = quot(r, a.by_g), words = i < it.q_s ? (it.q_s + 31) >> 5 : 0;
+          const int32_t* m = p.mask + (int64_t)(it.t0 + i) * p.mask_stride;
+#pragma unroll 1
+          for (int b = 0; b < kKeys; b += 16) {
+            const int k = kt + b, jj = k - ctx;
+            // bit x: key k + x is seen
+            uint32_t see = 0xffffu;
+            if (jj > -16) {
+              const int w = jj < 0 ? 0 : jj >> 5;
+              const uint32_t w0 = w < words ? static_cast<uint32_t>(__ldg(m + w)) : 0u;
+              const uint32_t w1 = w + 1 < words ? static_cast<uint32_t>(__ldg(m + w + 1)) : 0u;
+              see = jj < 0 ? (w0 << -jj) | ((1u << -jj) - 1u) : __funnelshift_r(w0, w1, jj & 31);
+            }
+            const int left = it.k1 - k;
+            if (left < 16) see &= left > 0 ? (1u << left) - 1u : 0u;
+            const uint32_t badw = b < 32 ? bad.x : b < 64 ? bad.y : b < 96 ? bad.z : bad.w;
+            see &= ~(badw >> (b & 31));
+            uint32_t u[16];
+            tm_ld(ts + b, u);
+            wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) u[c] = (see >> c) & 1u ? u[c] : 0xff800000u;
+            tm_st(ts + b, u);
+          }
+          wait_st();
+          const int vs = gg % NV;
+          if (!wait_bar(bar(kBVFull + vs), (gg / NV) & 1)) { ok = false; break; }
+          if (clean_v<G_>(sV + vs * G_::kTileB, quarter, 4, lane, kt, ctx, it.k1, bad)) poison[j % 3] = j + 1;
+          fence_proxy_async_smem();
+        }
+        uint32_t u[2][32];
+        float top = -INFINITY;
+        tm_ld(ts, u[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          wait_ld();
+          tm_ld(ts + ((c + 1) & 3) * 32, u[(c + 1) & 1]);  // the last: the first again, for P
+          uint32_t(&x)[32] = u[c & 1];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));  // NaN is passed over
+        }
+        top *= p.qk_scale_log2;
+        float alpha = 1.f;
+        if (ref == -INFINITY) {
+          ref = top;
+        } else if (top > ref + kTau) {
+          alpha = ex2(ref - top);
+          ref = top;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          // O of the group's tiles so far; the P V that made it came before this
+          // tile's S
+          wait_ld();
+          l2 = mul2(l2, pk2(alpha, alpha));
+          const uint32_t to = tmem + G_::kColO + (obuf(j) * 2 + grp) * D + lane_off;
+#pragma unroll 1
+          for (int b = 0; b < D; b += 16) {
+            uint32_t o[16];
+            tm_ld(to + b, o);
+            wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tm_st(to + b, o);
+          }
+          wait_st();
+        }
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        const unsigned long long neg2 = pk2(neg, neg);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          wait_ld();
+          if (c < 3) tm_ld(ts + (c + 1) * 32, u[(c + 1) & 1]);
+          uint32_t(&x)[32] = u[c & 1];
+          // P = 2^y in two parts: hi by cutting the low bits off, lo exactly what was cut off, then cut itself
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float y0, y1, r0, r1;
+            up2(fma2(pk2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg2), y0, y1);
+            const float p0 = ex2(y0), p1 = ex2(y1);
+            const unsigned long long pp = pk2(p0, p1);
+            l2 = add2(l2, pp);
+            const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+            hi[e / 2] = __byte_perm(u0, u1, 0x7632);
+            up2(sub2(pp, pk2(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))), r0, r1);
+            lo[e / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+          }
+          // over the scores of the same keys, which have been read
+          tm_st(ts + c * 32, hi);
+          tm_st(ts + c * 32 + 16, lo);
+          if (c & 1) {
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar((c == 1 ? kBPFull : kBPRest) + grp));
+          }
+        }
+      }
+      if (!ok) break;
+      g += nt;
+      ok = wait_bar(bar(kBLEmpty + (j & 1)), ((j >> 1) & 1) ^ 1);
+      if (!ok) break;
+      float l0, l1;
+      up2(l2, l0, l1);
+      stat[((j & 1) * 2 + grp) * 128 + row] = make_float2(l0 + l1, ref);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBLFull + (j & 1)));
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ======================= O / l: lane = row =======================
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    Ring ir;
+    bool ok = true;
+    for (int j = 0;; ++j) {
+      Item it;
+      ok = cta.take(ir, it);
+      if (!ok || it.nt == 0) break;
+      ok = wait_bar(bar(kBLFull + (j & 1)), (j >> 1) & 1);
+      if (!ok) break;
+      // a group that had no tile, or nothing to see, has sum 0
+      const float2 s0 = stat[(j & 1) * 256 + row], s1 = stat[(j & 1) * 256 + 128 + row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBLEmpty + (j & 1)));
+      const bool has0 = !(s0.x == 0.f), has1 = !(s1.x == 0.f);
+      const float ref0 = s0.y == -INFINITY ? 0.f : s0.y, ref1 = s1.y == -INFINITY ? 0.f : s1.y;  // all NaN: against 0
+      const float M = !has1 ? ref0 : !has0 ? ref1 : fmaxf(ref0, ref1);
+      const float w0 = has0 ? ex2(ref0 - M) : 0.f, w1 = has1 ? ex2(ref1 - M) : 0.f;
+      const float l = (has0 ? w0 * s0.x : 0.f) + (has1 ? w1 * s1.x : 0.f);
+      const float inv = l == 0.f ? 0.f : p.v_scale / l, f0 = w0 * inv, f1 = w1 * inv;
+      const int r = it.r0 + row, i = quot(r, a.by_g), hq = it.h * G + r - i * G;
+      const bool here = i < it.q_s, split = it.nchunks > 1;
+      const int64_t prow = ((int64_t)it.s * a.rows_per_seq + (int64_t)i * it.nchunks + it.c) * p.Hq + hq;
+      if (split && here) a.part_lse[prow] = l == 0.f ? -INFINITY : __log2f(l) + M;
+      ok = wait_bar(bar(kBOFull + obuf(j)), opass(j));
+      if (!ok) break;
+      fence_after();
+      const uint32_t to = tmem + G_::kColO + obuf(j) * 2 * D + lane_off;
+#pragma unroll 1
+      for (int b = 0; b < D; b += 32) {
+        uint32_t o[32], o2[32];
+        tm_ld(to + b, o);
+        tm_ld(to + D + b, o2);
+        wait_ld();
+        if (b + 32 == D) {  // the accumulators have been read
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBOFree + obuf(j)));
+        }
+        float v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float x = has0 ? __uint_as_float(o[c]) * f0 : 0.f;
+          v[c] = has1 ? fmaf(__uint_as_float(o2[c]), f1, x) : x;
+        }
+        if (here && split) {
+          float* y = a.part_o + prow * D + b;
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + c), "f"(v[c]), "f"(v[c + 1]),
+                         "f"(v[c + 2]), "f"(v[c + 3]), "f"(v[c + 4]), "f"(v[c + 5]), "f"(v[c + 6]), "f"(v[c + 7])
+                         : "memory");
+        } else if (here && a.out_bf16) {  // rows lie on 8 bytes
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh + b;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<uint2*>(y + c) = make_uint2(pack_bf16(v[c], v[c + 1]), pack_bf16(v[c + 2], v[c + 3]));
+        } else if (here) {
+          float* y = static_cast<float*>(p.out) + (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh + b;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) *reinterpret_cast<float2*>(y + c) = make_float2(v[c], v[c + 1]);
+        }
+        __syncwarp();
+      }
+      if (here && poison[j % 3] == j + 1) add_poison_row<D>(a, it, r);
+      __syncwarp();
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  // ---- teardown
+  fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrWaitTimeout);
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_wide(const TcArgs& a, int64_t max_items, int num_sms, cudaStream_t st) {
+  return a.p.D == 128 ? launch_items<Wide<128>>(tree_wide_kernel<128>, a, max_items, num_sms, st)
+                      : launch_items<Wide<64>>(tree_wide_kernel<64>, a, max_items, num_sms, st);
+}
+
+}  // namespace pkv
