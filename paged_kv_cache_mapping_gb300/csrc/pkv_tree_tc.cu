@@ -55,7 +55,7 @@ namespace {
 // ---------------------------------------------------------------- geometry
 template <int D, int N, bool F8>
 struct Geo {
-  static constexpr int kD = D, kN = N;
+  static constexpr int kD = D, kN = N, kPair = 1;
   static constexpr bool kF8 = F8;
   static constexpr int kEs = F8 ? 1 : 2;
   static constexpr int kRowB = D * kEs;                       // one K or V row
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, cons
 static int tree_tile_rows(int64_t rows, bool f8) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || f8 ? 64 : 128; }
 static Chunking call_chunking(int64_t B, int64_t Hkv, int64_t rows, bool f8) {
   const int64_t N = tree_tile_rows(rows, f8);
-  return tree_chunking(B * Hkv * ((rows + N - 1) / N));
+  return tree_chunking(B * Hkv * ((rows + N - 1) / N), (int)N);
 }
 
 int64_t tree_tc_rows_per_seq(int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_ctx, bool f8) {
@@ -803,7 +803,7 @@ cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t m
    : N == 32 ? launch_items<Geo<D, 32, F8>>(tree_tc_kernel<D, 32, F8>, a, most, num_sms, st)    \
              : launch_items<Geo<D, 64, F8>>(tree_tc_kernel<D, 64, F8>, a, most, num_sms, st))
   if (N == 128)
-    e = launch_tree_wide(a, most, num_sms, st);
+    e = launch_tree_wide(a, rows, most, num_sms, st);
   else if (p.D == 128)
     e = f8 ? PKV_TC1(128, true) : PKV_TC1(128, false);
   else

@@ -28,9 +28,17 @@
 namespace pkv {
 namespace {
 
-template <int D>
+// kBPFull + group: P of a tile's keys 0 .. 63; kBPRest + group: of the rest
+enum : int {
+  kBPRest = kBGroup, kBMax = kOffOwn / 8 /* [2 groups][4 warps] */,
+  kOffRef = kOffOwn + 64 /* [2][128] */, kOffStat = kOffRef + 1024 /* [2][2 groups][128] sum and reference */,
+  kOffStage = 6144 /* [4 warps][32 rows][128 bytes] */, kWideMisc = kOffStage + 4 * 4096,
+};
+static_assert(kOffStat + 2 * 2 * 128 * 8 <= kOffStage, "shared memory");
+
+template <int D, int P>
 struct Wide {
-  static constexpr int kD = D, kN = 128;
+  static constexpr int kD = D, kN = 128, kPair = P;
   static constexpr bool kF8 = false;
   static constexpr int kEs = 2, kRowB = 2 * D, kAtomB = 128;
   static constexpr int kSub = kRowB / kAtomB;
@@ -43,19 +51,12 @@ struct Wide {
   static constexpr int kSoft = 8;  // softmax warps
   static constexpr int kThreads = 32 * (4 + kSoft + 4);
   static constexpr int kOffK = 0, kOffV = kNK * kTileB, kOffQ = kOffV + kNV * kTileB, kOffMisc = kOffQ + kQBufs * kQB;
-  static constexpr int kSmem = kOffMisc + kMiscBytes;
-  // tensor memory: S and then P of the tile in hand, for each group; then the
-  // groups' O, twice where two fit
-  static constexpr int kOBufs = D == 128 ? 1 : 2;
-  static constexpr uint32_t kColO = 256;
+  static constexpr int kSmem = kOffMisc + kWideMisc;
+  static constexpr uint32_t kColO = 256;  // tensor memory: S and then P of each group's tile; then O, twice
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(kColO + kOBufs * 2 * D <= 512, "tensor memory");
+  static_assert(kColO + 2 * D <= 512, "tensor memory");
   static_assert(kNK + 2 <= kInfoSlots, "tile info ring");
 };
-
-// kBPFull + group: P of a tile's keys 0 .. 63; kBPRest + group: of the rest
-enum : int { kBPRest = kBGroup, kOffStat = kOffOwn /* [2][2 groups][128] sum and reference */ };
-static_assert(kOffStat + 2 * 2 * 128 * 8 <= kMiscBytes, "shared memory");
 
 // kSteps k steps of 16 keys with A in tensor memory: 8 columns for the hi part,
 // and 8 for the lo part 16 columns on
@@ -107,11 +108,11 @@ __device__ __noinline__ void add_poison_row(const TcArgs& a, const Item& it, int
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(Wide<D>::kThreads, 1)
+template <int D, int kPair>
+__global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
     tree_wide_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v) {
-  using G_ = Wide<D>;
+  using G_ = Wide<D, kPair>;
   constexpr int NK = G_::kNK, NV = G_::kNV, AT = G_::kAtomB;
   const TreeParams& p = a.p;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
   volatile int* poison = reinterpret_cast<volatile int*>(misc + 8 * kSPoison);  // [3]: item + 1
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 8 * kSTmem);
   uint32_t* info = reinterpret_cast<uint32_t*>(misc + kOffInfo);
+  float* refs = reinterpret_cast<float*>(misc + kOffRef);  // [2][128]: the rows' references
   float2* stat = reinterpret_cast<float2*>(misc + kOffStat);
   // as in the narrow kernel: the warp index, and so a role, is the warp's
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -136,9 +138,9 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(bar(kBKFull + i), 1);
-      mbar_init(bar(kBKEmpty + i), 1);
+      mbar_init(bar(kBKEmpty + i), kPair);  // both CTAs have read their copies
       mbar_init(bar(kBVFull + i), 1);
-      mbar_init(bar(kBVEmpty + i), 1);
+      mbar_init(bar(kBVEmpty + i), kPair);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBSFull + i), 2);
@@ -151,6 +153,8 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
       mbar_init(bar(kBLFull + i), G_::kSoft);
       mbar_init(bar(kBLEmpty + i), 4);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(bar(kBMax + i), 1);
+    mbar_init(bar(kBODone), 1);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(bar(kBItemFull + i), 1);
       mbar_init(bar(kBItemEmpty + i), 3 + G_::kSoft + 4);  // every warp but the finder
@@ -168,86 +172,98 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
   }
   fence_before();
   __syncthreads();
+  if (kPair > 1) cluster_sync();  // the other CTA's barriers stand
   fence_after();
   const uint32_t tmem = *tslot;
   grid_dep_wait();
   launch_dependents();
-
-  // item j's O buffer, and the parity of its pass
-  auto obuf = [](int j) { return G_::kOBufs == 2 ? j & 1 : 0; };
-  auto opass = [](int j) { return (uint32_t)(G_::kOBufs == 2 ? j >> 1 : j) & 1u; };
 
   if (warp == 0 || warp == 3) {
     copy_tiles<G_>(a, cta, warp == 3, warp == 3 ? sV : sK, warp == 3 ? &tm_v : &tm_k);
   } else if (warp == 1) {
     // ======================= MMA =======================
     constexpr uint32_t kIdS = idesc(128, false, false, false), kIdO = idesc(D, false, false, true);
+    // The tensor core takes the MMAs of a tile about as fast as they are issued
+    // and holds a few: what has to be waited for is waited for behind MMAs that
+    // are still to run, so that S of tile g + 2 follows P V of tile g at once.
     Ring ir, kr, vr;
-    int j = 0, g = 0, nt = 0;
-    // S of tile gg from the next K tile.  Its group's P of the tile before last
-    // stands there until that P V, issued earlier, has run.
-    auto issue_s = [&](int gg, int qb) -> bool {
-      if (!wait_bar(bar(kBKFull) + 8 * kr.at, kr.pass)) return false;
+    int js = -1, ns = 0, is = 0, gs = 0;  // S that goes next: item, its tiles, tile, tile of all
+    int n1 = 0, n2 = 0;                   // tiles of the items after the one whose P V runs (S may be two items on)
+    int j = 0, nt = 0;                    // P V: item, its tiles
+    // finds the tile whose S goes next; its K tile remains to be waited for
+    auto find_s = [&](bool& more) -> bool {
+      if (is == ns) {
+        Item it;
+        if (!cta.take(ir, it)) return false;
+        ++js;
+        is = 0;
+        ns = it.nt;
+        (js == j ? nt : js == j + 1 ? n1 : n2) = ns;
+        more = ns > 0;
+        if (!more) return true;
+        if (!wait_bar(bar(kBQFull + G_::qbuf(js)), G_::qpass(js))) return false;
+      }
+      return true;
+    };
+    // S replaces the P of its group's last tile, whose P V was issued earlier
+    auto issue_s = [&]() {
       fence_after();
       const uint64_t dk = sdesc(sK + kr.at * G_::kTileB, 16, 8 * AT, AT);
-      const uint64_t dq = sdesc(sQ + qb * G_::kQB, 16, 8 * AT, AT);
+      const uint64_t dq = sdesc(sQ + G_::qbuf(js) * G_::kQB, 16, 8 * AT, AT);
+      const int grp = gs & 1;
       if (elect_one()) {
 #pragma unroll
         for (int u = 0; u < G_::kSub; ++u)
-          mma_steps<false, 4, 2, 2>(tmem + (gg & 1) * 128, dq + (uint32_t)(u * 128 * AT >> 4), dk + (uint32_t)(u * kKeys * AT >> 4),
+          mma_steps<false, 4, 2, 2>(tmem + grp * 128, dq + (uint32_t)(u * 128 * AT >> 4), dk + (uint32_t)(u * kKeys * AT >> 4),
                                     kIdS, u != 0);
-        commit(bar(kBSFull + (gg & 1)));
-        commit(bar(kBKEmpty) + 8 * kr.at);
+        commit(bar(kBSFull + grp));
+        kPair > 1 ? commit_pair(bar(kBKEmpty) + 8 * kr.at) : commit(bar(kBKEmpty) + 8 * kr.at);
+        if (is + 1 == ns) commit(bar(kBQEmpty + G_::qbuf(js)));
         // the second arrival hands on what the tile's producer wrote (info)
-        mbar_arrive(bar(kBSFull + (gg & 1)));
+        mbar_arrive(bar(kBSFull + grp));
       }
       __syncwarp();
       kr.next(NK);
-      return true;
+      ++is;
+      ++gs;
     };
-    bool ok = true;
-    for (int t = 0;; ++t, ++g) {  // t: tile of item j - 1, whose S has been issued
-      if (t == nt - 1 && elect_one()) commit(bar(kBQEmpty + G_::qbuf(j - 1)));
-      int nt2 = nt;
-      if (t + 1 >= nt) {  // the tile whose S goes next is the next item's first
-        Item it;
-        ok = cta.take(ir, it);
-        nt2 = it.nt;
-        if (!ok || (nt2 == 0 && nt == 0)) break;
-        ok = nt2 == 0 || wait_bar(bar(kBQFull + G_::qbuf(j)), G_::qpass(j));
+    bool more = true, ok = find_s(more) && (!more || wait_bar(bar(kBKFull) + 8 * kr.at, kr.pass));
+    for (int g = -1, t = 0; ok && (nt > 0 || more); ++g) {
+      if (more) issue_s();  // of tile g + 1
+      const int ob = j & 1, grp = g & 1;
+      // V: d contiguous, 8 keys = 8 AT bytes, sub-tiles of d kKeys AT apart
+      const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // the halves of P V; before them what they and the next S need
+        if (h == 1 && more) ok = find_s(more);
         if (!ok) break;
-      }
-      const int gs = nt == 0 ? g : g + 1, qb = G_::qbuf(t + 1 >= nt ? j : j - 1);
-      if (nt2 > 0 || t + 1 < nt) ok = issue_s(gs, qb);
-      if (nt > 0 && ok) {
-        const int ob = obuf(j - 1), grp = g & 1;
-        ok = wait_bar(bar(kBVFull) + 8 * vr.at, vr.pass) && (t > 1 || wait_bar(bar(kBOFree + ob), opass(j - 1) ^ 1)) &&
-             wait_bar(bar(kBPFull + grp), (g >> 1) & 1);
-        if (!ok) break;
-        fence_after();
-        // V: d contiguous, 8 keys = 8 AT bytes, sub-tiles of d kKeys AT apart
-        const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
-        const uint32_t tp = tmem + grp * 128, to = tmem + G_::kColO + (ob * 2 + grp) * D;
-        if (elect_one()) mma_p_steps<4>(to, tp, dv, kIdO, t > 1);
-        __syncwarp();
-        ok = wait_bar(bar(kBPRest + grp), (g >> 1) & 1);
+        const bool k = lane == 3 && h == 1 && more, v = lane == 1, o = lane == 2 && t == 0;
+        if (g < 0) {  // no tile yet: the next S alone
+          if (h == 1 && more) ok = wait_bar(bar(kBKFull) + 8 * kr.at, kr.pass);
+          continue;
+        }
+        ok = wait_bar(k ? bar(kBKFull) + 8 * kr.at : v ? bar(kBVFull) + 8 * vr.at : o ? bar(kBOFree + ob) : bar((h ? kBPRest : kBPFull) + grp),
+                      k ? kr.pass : v ? vr.pass : o ? ((j >> 1) & 1) ^ 1 : (g >> 1) & 1);
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          mma_p_steps<4>(to, tp + 64, dv + 4 * 128, kIdO, 1);
-          commit(bar(kBVEmpty) + 8 * vr.at);
-          if (t + 1 == nt) commit(bar(kBOFull + ob));
+          mma_p_steps<4>(tmem + G_::kColO + ob * D, tmem + grp * 128 + h * 64, dv + h * (4 * 128), kIdO, t > 0 || h > 0);
+          if (h == 1) {
+            commit(bar(kBODone));
+            kPair > 1 ? commit_pair(bar(kBVEmpty) + 8 * vr.at) : commit(bar(kBVEmpty) + 8 * vr.at);
+            if (t + 1 == nt) commit(bar(kBOFull + ob));
+          }
         }
         __syncwarp();
-        vr.next(NV);
       }
-      if (!ok) break;
-      if (t + 1 >= nt) {
-        if (nt == 0) --g;  // no tile was finished
-        if (nt2 == 0) break;
-        nt = nt2;
-        t = -1;
+      if (!ok || g < 0) continue;
+      vr.next(NV);
+      if (++t == nt) {
+        t = 0;
         ++j;
+        nt = n1;
+        n1 = n2;
+        n2 = 0;
       }
     }
     if (!ok) *abort_flag = 1;
@@ -274,41 +290,48 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
       ok = cta.take(ir, it);
       if (!ok || it.nt == 0) break;
       const int nt = it.nt, ctx = it.n - it.q_s, r = it.r0 + row;
-      float ref = -INFINITY;  // none yet
+      // the row's reference as this group used it last; -infinity: none yet
+      float ref = -INFINITY;
+      float* const shared_ref = refs + (j & 1) * 128 + row;
       unsigned long long l2 = 0ull;
       for (int t = (g ^ grp) & 1; t < nt; t += 2) {
         const int gg = g + t;
+        const int kt = it.k0 + t * kKeys, jj = kt - ctx;  // first key of the tile, and its place among the drafted
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // keys of the tile that this row sees
+        if (jj > -kKeys) {
+          const int i = quot(r, a.by_g), words = i < it.q_s ? (it.q_s + 31) >> 5 : 0;
+          const int32_t* m = p.mask + (int64_t)(it.t0 + i) * p.mask_stride;
+          uint32_t w[5];
+#pragma unroll
+          for (int c = 0; c < 5; ++c) {
+            const int at = (jj >> 5) + c;
+            w[c] = at < 0 ? ~0u : at < words ? static_cast<uint32_t>(__ldg(m + at)) : 0u;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int left = it.k1 - (kt + 32 * c);
+            see[c] = __funnelshift_r(w[c], w[c + 1], jj & 31) & (left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u);
+          }
+        }
         ok = wait_bar(bar(kBSFull + grp), (gg >> 1) & 1);
         if (!ok) break;
         fence_after();
         const uint4 bad = *reinterpret_cast<const uint4*>(info + (gg % kInfoSlots) * 4);
-        const int kt = it.k0 + t * kKeys;  // first key of the tile
-        const bool masked = kt + kKeys > ctx || (bad.x | bad.y | bad.z | bad.w) != 0;
-        if (masked) {
+        if (jj > -kKeys || (bad.x | bad.y | bad.z | bad.w) != 0) {
           // scores that this row does not see become -inf, in place
-          const int i = quot(r, a.by_g), words = i < it.q_s ? (it.q_s + 31) >> 5 : 0;
-          const int32_t* m = p.mask + (int64_t)(it.t0 + i) * p.mask_stride;
+          see[0] &= ~bad.x;
+          see[1] &= ~bad.y;
+          see[2] &= ~bad.z;
+          see[3] &= ~bad.w;
 #pragma unroll 1
-          for (int b = 0; b < kKeys; b += 16) {
-            const int k = kt + b, jj = k - ctx;
-            // bit x: key k + x is seen
-            uint32_t see = 0xffffu;
-            if (jj > -16) {
-              const int w = jj < 0 ? 0 : jj >> 5;
-              const uint32_t w0 = w < words ? static_cast<uint32_t>(__ldg(m + w)) : 0u;
-              const uint32_t w1 = w + 1 < words ? static_cast<uint32_t>(__ldg(m + w + 1)) : 0u;
-              see = jj < 0 ? (w0 << -jj) | ((1u << -jj) - 1u) : __funnelshift_r(w0, w1, jj & 31);
-            }
-            const int left = it.k1 - k;
-            if (left < 16) see &= left > 0 ? (1u << left) - 1u : 0u;
-            const uint32_t badw = b < 32 ? bad.x : b < 64 ? bad.y : b < 96 ? bad.z : bad.w;
-            see &= ~(badw >> (b & 31));
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t w = (c < 4 ? c < 2 ? see[0] : see[1] : c < 6 ? see[2] : see[3]) >> (c & 1) * 16;
             uint32_t u[16];
-            tm_ld(ts + b, u);
+            tm_ld(ts + 16 * c, u);
             wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) u[c] = (see >> c) & 1u ? u[c] : 0xff800000u;
-            tm_st(ts + b, u);
+            for (int e = 0; e < 16; ++e) u[e] = (w >> e) & 1u ? u[e] : 0xff800000u;
+            tm_st(ts + 16 * c, u);
           }
           wait_st();
           const int vs = gg % NV;
@@ -319,28 +342,37 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
         uint32_t u[2][32];
         float top = -INFINITY;
         tm_ld(ts, u[0]);
+        // (loops of two chunks: the code of all roles shares the instruction cache)
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          wait_ld();
-          tm_ld(ts + ((c + 1) & 3) * 32, u[(c + 1) & 1]);  // the last: the first again, for P
-          uint32_t(&x)[32] = u[c & 1];
+          for (int c = 0; c < 2; ++c) {
+            wait_ld();
+            tm_ld(ts + (2 * h + c + 1) % 4 * 32, u[c ^ 1]);  // the last: the first again, for P
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));  // NaN is passed over
-        }
+            for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1]));  // NaN is passed over
+          }
         top *= p.qk_scale_log2;
-        float alpha = 1.f;
-        if (ref == -INFINITY) {
-          ref = top;
-        } else if (top > ref + kTau) {
-          alpha = ex2(ref - top);
-          ref = top;
+        // the other group has settled the tile before this one
+        if (gg > 0 && !wait_bar(bar(kBMax + (grp ^ 1) * 4 + quarter), ((gg - 1) >> 1) & 1)) { ok = false; break; }
+        const float old = t == 0 ? -INFINITY : *shared_ref;
+        const bool moved = old != -INFINITY && top > old + kTau;
+        const float now = old == -INFINITY || moved ? top : old;
+        *shared_ref = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBMax + grp * 4 + quarter));
+        if (__any_sync(0xffffffffu, ref != now)) {  // this group's sum follows
+          const float f = ref == -INFINITY || ref == now ? 1.f : ex2(ref - now);
+          l2 = mul2(l2, pk2(f, f));
+          ref = now;
         }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-          // O of the group's tiles so far; the P V that made it came before this
-          // tile's S
+        if (__any_sync(0xffffffffu, moved)) {
+          // and O, which every P V before this tile's has to have reached
+          if (!wait_bar(bar(kBODone), (gg - 1) & 1)) { ok = false; break; }
+          fence_after();
           wait_ld();
-          l2 = mul2(l2, pk2(alpha, alpha));
-          const uint32_t to = tmem + G_::kColO + (obuf(j) * 2 + grp) * D + lane_off;
+          const float alpha = moved ? ex2(old - now) : 1.f;
+          const uint32_t to = tmem + G_::kColO + (j & 1) * D + lane_off;
 #pragma unroll 1
           for (int b = 0; b < D; b += 16) {
             uint32_t o[16];
@@ -354,34 +386,36 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
         }
         const float neg = ref == -INFINITY ? 0.f : -ref;
         const unsigned long long neg2 = pk2(neg, neg);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          wait_ld();
-          if (c < 3) tm_ld(ts + (c + 1) * 32, u[(c + 1) & 1]);
-          uint32_t(&x)[32] = u[c & 1];
-          // P = 2^y in two parts: hi by cutting the low bits off, lo exactly what was cut off, then cut itself
-          uint32_t hi[16], lo[16];
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t at = ts + h * 64 + c * 32;
+            wait_ld();
+            if (c == 0 || h == 0) tm_ld(at + 32, u[c ^ 1]);
+            uint32_t(&x)[32] = u[c];
+            // P = 2^y in two parts: hi by cutting the low bits off, lo exactly what was cut off, then cut itself
+            uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float y0, y1, r0, r1;
-            up2(fma2(pk2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg2), y0, y1);
-            const float p0 = ex2(y0), p1 = ex2(y1);
-            const unsigned long long pp = pk2(p0, p1);
-            l2 = add2(l2, pp);
-            const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-            hi[e / 2] = __byte_perm(u0, u1, 0x7632);
-            up2(sub2(pp, pk2(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))), r0, r1);
-            lo[e / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            for (int e = 0; e < 32; e += 2) {
+              float y0, y1, r0, r1;
+              up2(fma2(pk2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg2), y0, y1);
+              const float p0 = ex2(y0), p1 = ex2(y1);
+              const unsigned long long pp = pk2(p0, p1);
+              l2 = add2(l2, pp);
+              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+              hi[e / 2] = __byte_perm(u0, u1, 0x7632);
+              up2(sub2(pp, pk2(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))), r0, r1);
+              lo[e / 2] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+            }
+            // over the scores of the same keys, which have been read
+            tm_st(at, hi);
+            tm_st(at + 16, lo);
           }
-          // over the scores of the same keys, which have been read
-          tm_st(ts + c * 32, hi);
-          tm_st(ts + c * 32 + 16, lo);
-          if (c & 1) {
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar((c == 1 ? kBPFull : kBPRest) + grp));
-          }
+          wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar((h == 0 ? kBPFull : kBPRest) + grp));
         }
       }
       if (!ok) break;
@@ -399,6 +433,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
     // ======================= O / l: lane = row =======================
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t stage = b0 + kOffStage + (warp & 3) * 4096;
     Ring ir;
     bool ok = true;
     for (int j = 0;; ++j) {
@@ -407,59 +442,62 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
       if (!ok || it.nt == 0) break;
       ok = wait_bar(bar(kBLFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
-      // a group that had no tile, or nothing to see, has sum 0
+      // a group's sum stands against the reference it used last (none: the sum is
+      // 0, or NaN), O against the larger one
       const float2 s0 = stat[(j & 1) * 256 + row], s1 = stat[(j & 1) * 256 + 128 + row];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBLEmpty + (j & 1)));
-      const bool has0 = !(s0.x == 0.f), has1 = !(s1.x == 0.f);
-      const float ref0 = s0.y == -INFINITY ? 0.f : s0.y, ref1 = s1.y == -INFINITY ? 0.f : s1.y;  // all NaN: against 0
-      const float M = !has1 ? ref0 : !has0 ? ref1 : fmaxf(ref0, ref1);
-      const float w0 = has0 ? ex2(ref0 - M) : 0.f, w1 = has1 ? ex2(ref1 - M) : 0.f;
-      const float l = (has0 ? w0 * s0.x : 0.f) + (has1 ? w1 * s1.x : 0.f);
-      const float inv = l == 0.f ? 0.f : p.v_scale / l, f0 = w0 * inv, f1 = w1 * inv;
+      const float top = fmaxf(s0.y, s1.y), M = top == -INFINITY ? 0.f : top;
+      const float l = (s0.y == -INFINITY ? s0.x : s0.x * ex2(s0.y - M)) + (s1.y == -INFINITY ? s1.x : s1.x * ex2(s1.y - M));
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
       const int r = it.r0 + row, i = quot(r, a.by_g), hq = it.h * G + r - i * G;
-      const bool here = i < it.q_s, split = it.nchunks > 1;
+      const bool here = i < it.q_s, split = it.nchunks > 1, wide = split || !a.out_bf16;  // fp32 elements
       const int64_t prow = ((int64_t)it.s * a.rows_per_seq + (int64_t)i * it.nchunks + it.c) * p.Hq + hq;
       if (split && here) a.part_lse[prow] = l == 0.f ? -INFINITY : __log2f(l) + M;
-      ok = wait_bar(bar(kBOFull + obuf(j)), opass(j));
+      // where this lane's row goes
+      const int64_t el = split ? prow * D : (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh;
+      char* const mine = !here ? nullptr : (split ? reinterpret_cast<char*>(a.part_o) : static_cast<char*>(p.out)) + el * (wide ? 4 : 2);
+      ok = wait_bar(bar(kBOFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
       fence_after();
-      const uint32_t to = tmem + G_::kColO + obuf(j) * 2 * D + lane_off;
+      const uint32_t to = tmem + G_::kColO + (j & 1) * D + lane_off;
+      // 32 columns of the warp's rows at a time turn through shared memory: stored
+      // as they are, each lane would touch a line of its own
 #pragma unroll 1
       for (int b = 0; b < D; b += 32) {
-        uint32_t o[32], o2[32];
+        uint32_t o[32];
         tm_ld(to + b, o);
-        tm_ld(to + D + b, o2);
         wait_ld();
-        if (b + 32 == D) {  // the accumulators have been read
+        if (b + 32 == D) {  // the accumulator has been read
           fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBOFree + obuf(j)));
+          if (lane == 0) mbar_arrive(bar(kBOFree + (j & 1)));
         }
-        float v[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float x = has0 ? __uint_as_float(o[c]) * f0 : 0.f;
-          v[c] = has1 ? fmaf(__uint_as_float(o2[c]), f1, x) : x;
-        }
-        if (here && split) {
-          float* y = a.part_o + prow * D + b;
+        for (int c = 0; c < 32; ++c) o[c] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
 #pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + c), "f"(v[c]), "f"(v[c + 1]),
-                         "f"(v[c + 2]), "f"(v[c + 3]), "f"(v[c + 4]), "f"(v[c + 5]), "f"(v[c + 6]), "f"(v[c + 7])
-                         : "memory");
-        } else if (here && a.out_bf16) {  // rows lie on 8 bytes
-          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh + b;
-#pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<uint2*>(y + c) = make_uint2(pack_bf16(v[c], v[c + 1]), pack_bf16(v[c + 2], v[c + 3]));
-        } else if (here) {
-          float* y = static_cast<float*>(p.out) + (int64_t)(it.t0 + i) * p.o_st + (int64_t)hq * p.o_sh + b;
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) *reinterpret_cast<float2*>(y + c) = make_float2(v[c], v[c + 1]);
-        }
+        for (int q = 0; q < 8; ++q) st_s128(stage + swz<128>(lane, q), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         __syncwarp();
+        const int e = b + lane % 8 * 4;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          char* const to_row = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * k + lane / 8));
+          float4 x;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(stage + swz<128>(4 * k + lane / 8, lane % 8)));
+          if (to_row != nullptr) {
+            if (split) {
+              *reinterpret_cast<float4*>(to_row + e * 4) = x;
+            } else if (wide) {  // rows lie on 8 bytes
+              *reinterpret_cast<float2*>(to_row + e * 4) = make_float2(x.x, x.y);
+              *reinterpret_cast<float2*>(to_row + e * 4 + 8) = make_float2(x.z, x.w);
+            } else {
+              *reinterpret_cast<uint2*>(to_row + e * 2) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+            }
+          }
+          __syncwarp();
+        }
       }
       if (here && poison[j % 3] == j + 1) add_poison_row<D>(a, it, r);
       __syncwarp();
@@ -474,13 +512,16 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
+  if (kPair > 1) cluster_sync();  // nothing of the other CTA's is on its way here
 }
 
 }  // namespace
 
-cudaError_t launch_tree_wide(const TcArgs& a, int64_t max_items, int num_sms, cudaStream_t st) {
-  return a.p.D == 128 ? launch_items<Wide<128>>(tree_wide_kernel<128>, a, max_items, num_sms, st)
-                      : launch_items<Wide<64>>(tree_wide_kernel<64>, a, max_items, num_sms, st);
+cudaError_t launch_tree_wide(const TcArgs& a, int64_t rows, int64_t max_items, int num_sms, cudaStream_t st) {
+#define PKV_WIDE(D, P) launch_items<Wide<D, P>>(tree_wide_kernel<D, P>, a, max_items, num_sms, st)
+  if (rows > 128) return a.p.D == 128 ? PKV_WIDE(128, 2) : PKV_WIDE(64, 2);
+  return a.p.D == 128 ? PKV_WIDE(128, 1) : PKV_WIDE(64, 1);
+#undef PKV_WIDE
 }
 
 }  // namespace pkv
