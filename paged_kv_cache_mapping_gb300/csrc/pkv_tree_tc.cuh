@@ -21,9 +21,14 @@ constexpr int kInfoSlots = 8;
 // many (sequence, KV head, row tile) units the call has: few units are cut
 // finely so that every SM has work, many are cut coarsely, since each chunk
 // costs its rows' partials (512 bytes per row and head, written and read) and
-// an item's start and end.  At least `least` keys, at most `most` chunks, and
-// at most kTreePartRows / q_s of them, so that a sequence has at most that many
-// partial rows per head.
+// an item's start and end.  A sequence is cut into equal chunks of at most
+// `least` keys, but into no more than `most`, and no more than
+// kTreePartRows / q_s, so that it has at most that many partial rows per head.
+// Measured, us: `least` 256 / 512 / 1024 / 2048 with 8 units of 2,048 keys 11.6 /
+// 11.8 / 13.9 / 16.6; 138 wide units of up to 3,001 keys 36 / 38 / 37 / 44; 256
+// wide ones of up to 8,192 135 / 131 / 117 / 113; 512 narrow ones of up to 4,096
+// 118 / 116 / 111 / 110.  `most` with 64 units of 32K to 131K keys: 16 303, 19
+// (8 items per SM) 288, 24 319, 48 337.
 constexpr int kTreeMaxChunks = 64;
 constexpr int kTreePartRows = 1024;
 struct Chunking {
@@ -31,8 +36,8 @@ struct Chunking {
 };
 inline Chunking tree_chunking(int64_t units, int rows) {
   Chunking c;
-  c.least = units >= (rows == 128 ? 256 : 512) ? 1024 : units >= 128 ? 512 : 256;
-  const int64_t m = 2432 / (units < 1 ? 1 : units);  // 16 items per SM
+  c.least = rows == 128 && units >= 256 ? 2048 : units >= 512 ? 1024 : units >= 128 ? 512 : 256;
+  const int64_t m = 1216 / (units < 1 ? 1 : units);  // 8 items per SM
   c.most = static_cast<int32_t>(m < 8 ? 8 : m > kTreeMaxChunks ? kTreeMaxChunks : m);
   return c;
 }
@@ -40,8 +45,9 @@ inline Chunking tree_chunking(int64_t units, int rows) {
 __host__ __device__ inline int tree_chunk(int n, int q_s, Chunking k) {
   const int rows = kTreePartRows / q_s;
   const int most = rows < 1 ? 1 : rows < k.most ? rows : k.most;
-  const int c = ((n - 1) / most / kKeys + 1) * kKeys;  // ceil(n / most) in whole tiles; n < 2^31 - 128
-  return most > 1 && c < k.least ? k.least : c;
+  const int tiles = (n - 1) / kKeys + 1, least = k.least / kKeys;
+  const int chunks = tiles <= least ? 1 : tiles <= (int64_t)least * most ? (tiles - 1) / least + 1 : most;
+  return ((tiles - 1) / chunks + 1) * kKeys;  // n < 2^31 - 128
 }
 
 struct alignas(16) Item {
@@ -664,11 +670,12 @@ __device__ __forceinline__ bool clean_v(uint32_t tile, int w_of, int warps, int 
   const int ch = lane % kLn, rr = lane / kLn;
   bool found = false;
   // the context's rows stay as they are, unless pages are out of range
-  const int from = (bad.x | bad.y | bad.z | bad.w) ? 0 : max(0, ctx - kt - w_of * (kKeys / warps)) / kRs * kRs;
-#pragma unroll 1
+  const uint32_t bm = w_of * (kKeys / warps) < 64 ? w_of * (kKeys / warps) < 32 ? bad.x : bad.y
+                                                  : w_of * (kKeys / warps) < 96 ? bad.z : bad.w;  // this warp's rows lie in one word
+  const int first = w_of * (kKeys / warps), from = bm ? 0 : max(0, ctx - kt - first) / kRs * kRs;
+#pragma unroll 2
   for (int b = from; b < kKeys / warps; b += kRs) {
-    const int kk = w_of * (kKeys / warps) + b + rr, ky = kt + kk;
-    const uint32_t bm = kk < 32 ? bad.x : kk < 64 ? bad.y : kk < 96 ? bad.z : bad.w;
+    const int kk = first + b + rr, ky = kt + kk;
     const bool gone = ky >= k1 || ((bm >> (kk & 31)) & 1u);
     if (!gone && ky < ctx) continue;
     const uint32_t at = tile + (ch * 16 / AT) * kKeys * AT + swz<AT>(kk, ch % (AT / 16));

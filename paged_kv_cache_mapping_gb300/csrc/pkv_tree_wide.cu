@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
       const int ob = j & 1, grp = g & 1;
       // V: d contiguous, 8 keys = 8 AT bytes, sub-tiles of d kKeys AT apart
       const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
-#pragma unroll 1
+#pragma unroll
       for (int h = 0; h < 2; ++h) {  // the halves of P V; before them what they and the next S need
         if (h == 1 && more) ok = find_s(more);
         if (!ok) break;
