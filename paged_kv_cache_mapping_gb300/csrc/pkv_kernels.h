@@ -41,6 +41,23 @@ cudaError_t launch_csr_tables(const int32_t* indptr, const int32_t* indices, int
 cudaError_t launch_append(const AppendParams& p, int src_kind, bool fp8, bool slots_i64,
                           cudaStream_t stream);
 
+// Division of 0 <= x < 2^31 by a constant d >= 1 of the call: one multiply-high
+// and a shift.  M = floor(2^(32 + s) / d) + 1 with 2^s < d <= 2^(s + 1): M fits
+// 32 bits, x M / 2^(32 + s) passes x / d by at most x / 2^(32 + s) < 1 / d, so
+// the floor is exact.  d = 1 is x itself.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while (f.s < 31 && (2u << f.s) < d) ++f.s;
+  if (d > 1) f.m = static_cast<uint32_t>(((uint64_t)1 << (32 + f.s)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int quot(int x, const FastDiv& f) {
+  return f.d == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), f.m) >> f.s);
+}
+
 // ---------------------------------------------------------------- rotary append
 struct RopeParams {
   const void* q;
@@ -59,6 +76,7 @@ struct RopeParams {
   float k_inv_scale, v_inv_scale;
   // units of work of a token, set by the launcher (see pkv_rope.cu)
   int32_t rot_units, pass_units, v_units, units, units_per_part;
+  FastDiv by_row, by_v;  // units of a q or k row, of a v row
   unsigned int* err;
   pkv_rope rope;
 };

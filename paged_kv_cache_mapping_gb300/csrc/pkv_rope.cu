@@ -13,10 +13,16 @@
 // Bound: memory.  Each row of q, k and v is read once and written once; a
 // decode step's few rows are bound by latency.  One CTA takes one token (or a
 // part of its rows, when there are few tokens, so that the whole GPU works):
-// its threads first issue the loads of their row vectors, then compute the
-// token's cos / sin pairs into shared memory (shared by all Hq + Hkv heads),
-// and rotate after the barrier, so that the sine's latency hides under the
-// loads'.
+// its threads issue their first loads, then compute the token's cos / sin pairs
+// into shared memory (shared by all Hq + Hkv heads), and rotate after the
+// barrier, so that the sine's latency hides under the loads'.  A thread holds
+// one unit at a time: three in flight took 79 registers instead of 39 and left
+// six CTAs on an SM, which cost more than the loads' latency saved (8,192 tokens
+// of 32 + 8 + 8 heads at D 128: 40 us with three, 34 with one; with 64, 192 and
+// 256 threads 36, 39 and 51).
+// Measured: those 8,192 bf16 tokens 33.7 us (6.0 TB/s of 201 MB, 88 % of a plain
+// copy's rate); a decode step of 64 tokens 2.4 us; 777 drafted tokens of 20 + 5 +
+// 5 heads at D 64 into e4m3 caches 3.5 us.
 #include <math.h>
 
 #include "pkv_kernels.h"
@@ -97,7 +103,7 @@ __device__ __forceinline__ Unit unit_of(int u, const RopeParams& p) {
   const int per_rot = p.rot_units + p.pass_units;
   const int n_rot = (p.Hq + p.Hkv) * per_rot;
   if (u < n_rot) {
-    r.row = u / per_rot;
+    r.row = quot(u, p.by_row);
     const int c = u - r.row * per_rot;
     r.rotated = c < p.rot_units;
     if (r.rotated) {
@@ -114,7 +120,7 @@ __device__ __forceinline__ Unit unit_of(int u, const RopeParams& p) {
     }
   } else {
     const int w = u - n_rot;
-    const int vr = w / p.v_units;
+    const int vr = quot(w, p.by_v);
     r.row = p.Hq + p.Hkv + vr;
     r.e0 = 2 * VE * (w - vr * p.v_units);
     r.e1 = r.e0 + VE < p.D ? r.e0 + VE : -1;
@@ -150,7 +156,6 @@ __device__ __forceinline__ void put(const RopeParams& p, int64_t t, int64_t slot
 }
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeBatch = 3;  // units per thread in flight: 128 x 3 cover a row set of 32 + 8 + 8 heads at D 128
 
 // Slots and positions are read as their caller's integer type.
 template <typename SlotT>
@@ -168,18 +173,38 @@ __device__ __forceinline__ int64_t token_slot(const RopeParams& p, int64_t t, bo
   return slot;
 }
 
+// Place of pair i in the vector kernel's table: two pairs of padding after every
+// eight, so that the threads of a row's units, eight pairs (VE 8) apart, read 16
+// bytes each from banks of their own.
+__device__ __forceinline__ int place(int i) { return i + (i >> 3) * 2; }
+
+template <bool kPadded>
 __device__ __forceinline__ void fill_table(const RopeParams& p, int64_t t, float2* cs) {
   const unsigned long long pos = static_cast<unsigned long long>(
       p.pos_i64 ? index_at<int64_t>(p.positions, t) : index_at<int32_t>(p.positions, t));
   for (int i = threadIdx.x; i < p.rope.rot_dim / 2; i += kRopeThreads)
-    cs[i] = rope_cs(pos, p.rope.turns[i], p.rope.amplitude);
+    cs[kPadded ? place(i) : i] = rope_cs(pos, p.rope.turns[i], p.rope.amplitude);
+}
+
+// VE / 2 neighbouring pairs by their table entries (two to 16 bytes)
+template <int VE> __device__ __forceinline__ void turn_pairs(float (&x)[VE], const float2* table) {
+  const float4* c0 = reinterpret_cast<const float4*>(table);
+#pragma unroll
+  for (int i = 0; i < VE; i += 4) {
+    const float4 c = c0[i / 4];
+    const float f0 = x[i], g0 = x[i + 1], f1 = x[i + 2], g1 = x[i + 3];
+    x[i] = f0 * c.x - g0 * c.y;
+    x[i + 1] = f0 * c.y + g0 * c.x;
+    x[i + 2] = f1 * c.z - g1 * c.w;
+    x[i + 3] = f1 * c.w + g1 * c.z;
+  }
 }
 
 // grid: (tokens, parts of a token's units)
 template <typename SrcT, bool kFp8>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int VE = VecOf<SrcT>::n;
-  __shared__ float2 cs[PKV_ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float2 cs[PKV_ROPE_MAX_PAIRS / 8 * 10];
   launch_dependents();
   grid_dep_wait();
   const int64_t t = blockIdx.x;
@@ -187,66 +212,46 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int u1 = min(u0 + p.units_per_part, p.units);
   bool table = false;
   int64_t slot = -1;
-  for (int ub = u0; ub < u1; ub += kRopeThreads * kRopeBatch) {
-    Unit un[kRopeBatch];
-    uint4 a[kRopeBatch], b[kRopeBatch];
-#pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
-      const int u = ub + k * kRopeThreads + threadIdx.x;
-      if (u < u1) {
-        un[k] = unit_of<VE>(u, p);
-        const SrcT* s = src_row<SrcT>(p, t, un[k].row);
-        a[k] = *reinterpret_cast<const uint4*>(s + un[k].e0);
-        if (un[k].e1 >= 0) b[k] = *reinterpret_cast<const uint4*>(s + un[k].e1);
-      }
+  // the first unit's loads are on their way while the table is made
+  for (int u = u0 + threadIdx.x;; u += kRopeThreads) {
+    const bool some = u < u1;
+    Unit un{};
+    uint4 a{}, b{};
+    if (some) {
+      un = unit_of<VE>(u, p);
+      const SrcT* s = src_row<SrcT>(p, t, un.row);
+      a = *reinterpret_cast<const uint4*>(s + un.e0);
+      if (un.e1 >= 0) b = *reinterpret_cast<const uint4*>(s + un.e1);
     }
-    if (!table) {  // under the first batch's loads
+    if (!table) {
       slot = token_slot(p, t, threadIdx.x == 0 && blockIdx.y == 0);
-      fill_table(p, t, cs);
+      fill_table<true>(p, t, cs);
       __syncthreads();
       table = true;
     }
+    if (!some) break;
+    float x[VE], y[VE];
+    unpack<VE>(a, x);
+    unpack<VE>(b, y);
+    if (un.rotated) {
+      if (p.rope.interleaved) {
+        turn_pairs<VE>(x, cs + place(un.e0 / 2));
+        if (un.e1 >= 0) turn_pairs<VE>(y, cs + place(un.e1 / 2));
+      } else {
+        const float4* c0 = reinterpret_cast<const float4*>(cs + place(un.e0));
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
-      const int u = ub + k * kRopeThreads + threadIdx.x;
-      if (u >= u1) break;
-      float x[VE], y[VE];
-      unpack<VE>(a[k], x);
-      unpack<VE>(b[k], y);
-      if (un[k].rotated) {
-        if (p.rope.interleaved) {
-          const float2* c0 = cs + un[k].e0 / 2;
-#pragma unroll
-          for (int i = 0; i < VE / 2; ++i) {
-            const float2 c = c0[i];
-            const float f = x[2 * i], g = x[2 * i + 1];
-            x[2 * i] = f * c.x - g * c.y;
-            x[2 * i + 1] = f * c.y + g * c.x;
-          }
-          if (un[k].e1 >= 0) {
-            const float2* c1 = cs + un[k].e1 / 2;
-#pragma unroll
-            for (int i = 0; i < VE / 2; ++i) {
-              const float2 c = c1[i];
-              const float f = y[2 * i], g = y[2 * i + 1];
-              y[2 * i] = f * c.x - g * c.y;
-              y[2 * i + 1] = f * c.y + g * c.x;
-            }
-          }
-        } else {
-          const float2* c0 = cs + un[k].e0;
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const float2 c = c0[i];
-            const float f = x[i], g = y[i];
-            x[i] = f * c.x - g * c.y;
-            y[i] = f * c.y + g * c.x;
-          }
+        for (int i = 0; i < VE; i += 2) {
+          const float4 c = c0[i / 2];
+          const float f0 = x[i], g0 = y[i], f1 = x[i + 1], g1 = y[i + 1];
+          x[i] = f0 * c.x - g0 * c.y;
+          y[i] = f0 * c.y + g0 * c.x;
+          x[i + 1] = f1 * c.z - g1 * c.w;
+          y[i + 1] = f1 * c.w + g1 * c.z;
         }
       }
-      put<SrcT, kFp8, VE>(p, t, slot, un[k].row, un[k].e0, x);
-      if (un[k].e1 >= 0) put<SrcT, kFp8, VE>(p, t, slot, un[k].row, un[k].e1, y);
     }
+    put<SrcT, kFp8, VE>(p, t, slot, un.row, un.e0, x);
+    if (un.e1 >= 0) put<SrcT, kFp8, VE>(p, t, slot, un.row, un.e1, y);
   }
 }
 
@@ -278,12 +283,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_pairs_kernel(const _
   grid_dep_wait();
   const int64_t t = blockIdx.x;
   const int64_t slot = token_slot(p, t, threadIdx.x == 0 && blockIdx.y == 0);
-  fill_table(p, t, cs);
+  fill_table<false>(p, t, cs);
   __syncthreads();
   const int half = p.rope.rot_dim / 2, per = p.D / 2;
   const int u1 = min((int)(blockIdx.y + 1) * p.units_per_part, p.units);
   for (int u = blockIdx.y * p.units_per_part + threadIdx.x; u < u1; u += kRopeThreads) {
-    const int row = u / per, i = u - row * per;
+    const int row = quot(u, p.by_row), i = u - row * per;
     const bool rotated = i < half && row < p.Hq + p.Hkv;
     const int e0 = rotated && !p.rope.interleaved ? i : 2 * i;
     const int e1 = rotated && !p.rope.interleaved ? i + half : 2 * i + 1;
@@ -311,8 +316,11 @@ cudaError_t launch_t(RopeParams p, int num_sms, cudaStream_t st) {
     p.pass_units = ((p.D - rot) / VE + 1) / 2;
     p.v_units = (p.D / VE + 1) / 2;
     p.units = (p.Hq + p.Hkv) * (p.rot_units + p.pass_units) + p.Hkv * p.v_units;
+    p.by_row = fast_div(p.rot_units + p.pass_units);
+    p.by_v = fast_div(p.v_units);
   } else {
     p.units = (p.Hq + 2 * p.Hkv) * (p.D / 2);
+    p.by_row = fast_div(p.D / 2);
   }
   // few tokens: cut a token's units into parts of at least one per thread,
   // so that about two CTAs per SM share the rows

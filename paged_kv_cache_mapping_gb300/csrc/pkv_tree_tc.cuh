@@ -311,23 +311,6 @@ __device__ __forceinline__ float col_sum(float (&v)[NC], int lane) {
   return v[0];
 }
 
-// Division of 0 <= x < 2^31 by a constant d >= 1 of the call: one multiply-high
-// and a shift.  M = floor(2^(32 + s) / d) + 1 with 2^s < d <= 2^(s + 1): M fits
-// 32 bits, x M / 2^(32 + s) passes x / d by at most x / 2^(32 + s) < 1 / d, so
-// the floor is exact.  d = 1 is x itself.
-struct FastDiv {
-  uint32_t d, m, s;
-};
-inline FastDiv fast_div(uint32_t d) {
-  FastDiv f{d, 0, 0};
-  while (f.s < 31 && (2u << f.s) < d) ++f.s;
-  if (d > 1) f.m = static_cast<uint32_t>(((uint64_t)1 << (32 + f.s)) / d + 1);
-  return f;
-}
-__device__ __forceinline__ int quot(int x, const FastDiv& f) {
-  return f.d == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), f.m) >> f.s);
-}
-
 struct TcArgs {
   TreeParams p;
   FastDiv by_g, by_bs;
