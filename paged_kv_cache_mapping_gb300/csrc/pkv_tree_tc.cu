@@ -694,50 +694,31 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
 // ---------------------------------------------------------------- join
 // o = sum_c 2^(lse_c - M) o_c / sum_c 2^(lse_c - M) over a row's chunks, in
 // order.  One warp per (row, query head); lane l holds elements l D/32 ..;
-// eight chunks' loads in flight.  grid: (sequences, parts of a sequence's rows).
+// eight chunks' loads in flight, the first with those of the weights.  grid: (sequences, parts of a sequence's rows).
 template <int D, typename OutT>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, const float* part_o, const float* part_lse,
                                                         int rows_per_seq, Chunking chunking) {
-  grid_dep_wait();
-  launch_dependents();
-  constexpr int E = D / 32;
+  // what does not come from the kernel before is read while that still runs (it
+  // lets this one start only after its own predecessors have ended)
+  constexpr int E = D / 32, kAt = 8;  // chunks in flight
   const int s = blockIdx.x, lane = threadIdx.x & 31;
   const int c0 = __ldg(p.cu_q + s), c1 = __ldg(p.cu_q + s + 1), n = __ldg(p.seq_lens + s);
   const int q_s = c1 - c0;
-  if (c0 < 0 || c1 <= c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs || q_s > p.max_nodes)
-    return;
-  const int chunk = tree_chunk(n, q_s, chunking);
-  const int nc = (n - 1) / chunk + 1;
+  const bool bad = c0 < 0 || c1 <= c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs || q_s > p.max_nodes;
+  const int chunk = bad ? 1 : tree_chunk(n, q_s, chunking);
+  const int nc = bad ? 1 : (n - 1) / chunk + 1;
+  grid_dep_wait();
+  launch_dependents();
   if (nc == 1) return;
   const int64_t rows = (int64_t)q_s * p.Hq;
   for (int64_t r = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.y * 8) {
     const int i = static_cast<int>(r / p.Hq), hq = static_cast<int>(r - (int64_t)i * p.Hq);
     const int64_t at = ((int64_t)s * rows_per_seq + (int64_t)i * nc) * p.Hq + hq;
-    float lv[2], M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      lv[k] = lane + 32 * k < nc ? __ldcg(part_lse + at + (int64_t)(lane + 32 * k) * p.Hq) : -INFINITY;
-      M = fmaxf(M, lv[k]);  // a NaN stays out of M and comes back through the weights
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ms = M == -INFINITY ? 0.f : M;
-    float w[2], L = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      w[k] = lane + 32 * k < nc ? exp2f(lv[k] - ms) : 0.f;
-      L += w[k];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const float* src = part_o + at * D + lane * E;
-    float acc[E];
+    float v[kAt][E];
+    auto load = [&](int b) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int b = 0; b < nc; b += 8) {
-      float v[8][E];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kAt; ++k) {
         if (b + k < nc) {
           const float* q = src + (int64_t)(b + k) * p.Hq * D;
           if constexpr (E == 4) {
@@ -749,14 +730,39 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, cons
           }
         }
       }
+    };
+    float lv[2], M = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 2; ++k) lv[k] = lane + 32 * k < nc ? __ldcg(part_lse + at + (int64_t)(lane + 32 * k) * p.Hq) : -INFINITY;
+    load(0);  // together with the weights
+#pragma unroll
+    for (int k = 0; k < 2; ++k) M = fmaxf(M, lv[k]);  // a NaN stays out of M and comes back through the weights
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ms = M == -INFINITY ? 0.f : M;
+    float w[2], L = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      w[k] = lane + 32 * k < nc ? exp2f(lv[k] - ms) : 0.f;
+      L += w[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int b = 0;;) {
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) {
         const float wk = __shfl_sync(0xffffffffu, b < 32 ? w[0] : w[1], (b + k) & 31);
         if (b + k < nc && wk != 0.f) {  // a chunk without weight adds nothing
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[k][e], acc[e]);
         }
       }
+      b += kAt;
+      if (b >= nc) break;
+      load(b);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     OutT* dst = static_cast<OutT*>(p.out) + (int64_t)(c0 + i) * p.o_st + (int64_t)hq * p.o_sh + lane * E;
