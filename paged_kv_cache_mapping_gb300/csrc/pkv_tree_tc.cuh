@@ -459,7 +459,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
             if (!bx) {
               atomicOr(w + key_of / 32, bad << (key_of & 31));
             } else if (lane < n_box) {
-              atomicOr(w + key_of / 32, (bx == 16 ? 0xffffu : 0xffu) << (key_of & 31));
+              atomicOr(w + key_of / 32, ((1u << bx) - 1u) << (key_of & 31));
             }
           }
           __syncwarp();
@@ -728,7 +728,7 @@ inline bool encode_cache(CUtensorMap* m, const void* base, const TreeParams& p, 
 // Launches a kernel's persistent CTAs over at most max_items items.
 template <class G_, class Kern>
 cudaError_t launch_items(Kern kern, TcArgs a, int64_t max_items, int num_sms, cudaStream_t st) {
-  a.box = a.p.bs % 16 == 0 ? 16 : a.p.bs % 8 == 0 ? 8 : 0;
+  a.box = a.p.bs % 16 == 0 ? 16 : a.p.bs % 8 == 0 ? 8 : a.p.bs % 4 == 0 ? 4 : 0;
   CUtensorMap mk, mv;
   if (!encode_cache(&mk, a.p.k_cache, a.p, G_::kF8, G_::kAtomB, a.box) || !encode_cache(&mv, a.p.v_cache, a.p, G_::kF8, G_::kAtomB, a.box))
     return cudaErrorInvalidValue;
