@@ -21,11 +21,12 @@
 //
 // Work: an item is (sequence, chunk of keys, KV head, tile of N rows).  The
 // chunk length follows from the sequence's own length and node count and the
-// call's shapes, not from the other sequences (tree_chunk).  Chunks write normalised partials and log2-sum-exp2, and a second small kernel joins
-// them in order.  Items are dealt to the persistent CTAs (one per SM) in
-// strides; every CTA finds its items by scanning the lengths, 32 sequences per
-// step, so a call needs no plan, keeps nothing between calls, and its
-// workspace holds only the partials.
+// call's shapes, not from the other sequences (tree_chunk).  Chunks write
+// normalised partials and log2-sum-exp2, and a second small kernel joins them in
+// order.  Items are dealt to the persistent CTAs (one per SM) in strides; every
+// CTA finds its items by scanning the lengths, 32 sequences per step, so a call
+// needs no plan, keeps nothing between calls, and its workspace holds only the
+// partials.
 //
 // Types: bf16 caches take bf16 MMAs, P as bf16 hi + lo (about 16 bits).  e4m3
 // caches take the codes as they are (kind::f8f6f4, no conversion): a query row
@@ -35,9 +36,22 @@
 // hi and lo, lo scaled by 16 with an accumulator of its own, so that the
 // smallest codes' step is 2^-17 of the row's reference.
 //
-// CTA: 16 warps.
-//   warps 0, 3  copy the K and the V tiles of 128 keys by TMA: boxes of 16 or 8
-//               slots that lie in one block, or, for other block sizes, four
+// More than 64 rows (bf16 caches) go to pkv_tree_wide.cu, whose tiles of 128 rows
+// put the rows on the M side: up to 64 rows this kernel is the faster one (64
+// trees of 8 / 12 / 16 nodes times 4 heads over 512 to 4,096 keys: 110 / 128 / 133
+// us here, 126 / 131 / 135 there), above it the other (16 trees of 64 nodes over
+// up to 8,192 keys: 192 and 150 us when it was new, 107 now).
+//
+// Bound: the memory while there are few rows, then the softmax: with a key per
+// lane each warp runs about 290 instructions for 32 keys and 16 rows.
+// Measured, with the join: 64 trees of 8 nodes over 512 to 4,096 keys, bf16: 108
+// us (5.5 TB/s of 600 MB, 81 % of a plain copy's rate); 8 trees of 16 nodes over
+// 32K to 128K keys, e4m3: 289 us (4.3 TB/s of 1,240 MB); one tree of 8 nodes over
+// 2,048 keys: 10.7 us.
+//
+// CTA: 16 warps, 24 for N = 64.
+//   warps 0, 3  copy the K and the V tiles of 128 keys by TMA: boxes of 16, 8 or
+//               4 slots that lie in one block, or, for other block sizes, four
 //               arbitrary rows at a time (tile::gather4).
 //   warp 1      issues the MMAs: S of tile g + 1, then P V of tile g.  The two
 //               parts of P are 2 N columns of one operand, so O holds their two
@@ -307,7 +321,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     // row's reference moves.  bf16 parts keep their precision over the whole
     // exponent range, so the first reference is 0 unless the row's largest
     // score lies beyond +-kTau; e4m3 parts want the largest p near 2^kUp.
-    constexpr float kTau = F8 ? 4.5f : 60.f;
+    constexpr float kTau = F8 ? 4.5f : 16.f;
     constexpr float kUp = F8 ? 4.f : 0.f;
     // an e4m3 row's reference is set this far above the largest score seen, so
     // that it rarely has to move again in a chunk

@@ -181,12 +181,10 @@ __device__ __forceinline__ uint64_t l2_normal_policy() {
 }
 
 // A bounded wait, and the same by a whole warp: at most 2^18 tries, each of
-// which may suspend the warp for up to 20 us (5 s in all).  Without the time
-// hint a try comes back after some tens of clocks, and the waiting warps' tries
-// took half of the SM's issue slots.  The code is kept short, here and below:
-// sixteen and more warps in six roles share the SM's instruction cache, and
-// while the roles' code did not fit (105 to 166 KB in all, 42 % of its requests
-// missed) it set the pace, not the pipes.
+// which may suspend the warp for up to 20 us (5 s in all).  The code is kept
+// short, here and below: sixteen and more warps in six roles share the SM's
+// instruction cache, and while the roles' code did not fit (105 to 166 KB in
+// all, 42 % of its requests missed) it set the pace, not the pipes.
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -316,7 +314,7 @@ struct TcArgs {
   FastDiv by_g, by_bs;
   int32_t rows_per_seq;  // partial rows of a sequence
   Chunking chunking;
-  int32_t box;           // slots per TMA box, 0: gather4
+  int32_t box;           // slots per TMA box: 16, 8 or 4, so that a box lies in one block; 0: gather4
   int32_t out_bf16;
   float* part_o;         // [B * rows_per_seq, Hq, D] normalised chunk outputs
   float* part_lse;       // [B * rows_per_seq, Hq]

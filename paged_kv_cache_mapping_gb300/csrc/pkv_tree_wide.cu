@@ -6,21 +6,36 @@
 // stand the usual way round:
 //     S = Q K^T     (M 128 rows, N 128 keys, K = D)
 //     O += P V      (M 128 rows, N = D, K 128 keys; P as bf16 hi + lo)
-// With 64 rows the other form moves 48 KB of operands through shared memory for
-// every 64 rows and 128 keys of K, V and P; here P stays in tensor memory, where
-// it replaces S, and K and V tiles serve twice the rows.
+// P stays in tensor memory, where it replaces S, and K and V tiles serve twice
+// the rows that 64-row tiles served.
 //
 // Softmax: two groups of four warps take the tiles in turn, group g & 1 tile g,
-// and a thread owns a row: its largest score, its sum, and an accumulator of O of
-// its group's own.  So there is nothing to agree on between threads: a row's
-// reference moves (when its largest score passes it by 2^kTau) and its O is
-// rescaled by the one thread that holds it.  The two groups' O are joined where
-// the item is written, each with weight 2^(reference - larger reference).  S is
-// read twice, for the largest score and for P, since 128 scores do not fit a
-// thread's registers beside the rest.
+// and a thread owns a row of its tile: its largest score and its share of the
+// sum need no other thread.  The reference of a row is shared by the groups: a
+// group settles it for tile g (it moves when the tile's largest score passes it
+// by 2^kTau; then the row of O is rescaled, which is rare) after the other has
+// settled it for tile g - 1, half a tile's time earlier.  So there is one O, two
+// of them fit tensor memory, and an item's O is written out while the next item
+// runs.  (An O for each group, nothing shared, took all of it: every item's end
+// cost 4,900 clocks.)  S is read twice, for the largest score and for P, since
+// 128 scores do not fit a thread's registers beside the rest.
 //
-// Bound: the tensor cores.  A tile of 128 rows and 128 keys at D 128 takes 4.2
-// MFLOP for S and 8.4 for the two parts of P, about 1,540 clocks.
+// More than 128 rows: a cluster of two CTAs takes two neighbouring row tiles of
+// the same keys, and each copies half of every K and V tile into both (TMA
+// multicast).  One CTA alone loads 64 KB for 12.6 MFLOP, and with the products
+// and the softmax taken out (a probe) the loads alone took 103 of 133 us; in
+// pairs the 16 trees below went from 131 to 120 us.
+//
+// Bound: the tensor cores run 54 % of the time (a tile of 128 rows and 128 keys
+// at D 128 takes 4.2 MFLOP for S and 8.4 for the two parts of P, about 1,540
+// clocks; in the middle of an item a tile takes 2,200, at an item's masked end
+// about 5,000 more), the MMA warp's waits and the softmax take turns being the
+// slower.  Instruction cache: see poll(); code in one place instead of unrolled
+// took 3,000 clocks off every item's start, but the halves of P V, whose
+// descriptors want to be constants, stand twice (124 us in a loop, 116 so).
+// Measured, with the join: 16 trees of 64 nodes times 4 heads (256 rows) over
+// 1,024 to 8,192 keys, D 128: 107 us (73 GFLOP of visible pairs, 0.68 PFLOP/s);
+// 23 uneven trees of up to 37 nodes times 5 heads, D 64, pages of 12 slots: 29 us.
 //
 // CTA: 16 warps: K, MMA, items and query rows, V, 2 x 4 of softmax, 4 that write.
 #include "pkv_tree_tc.cuh"

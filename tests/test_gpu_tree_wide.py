@@ -87,6 +87,19 @@ def test_large_and_rising_scores(q):
     compare(b)
 
 
+@pytest.mark.parametrize("q", [4, 14, 20, 40])
+def test_large_values_stay_finite(q):
+    """Values near 2^100 times scores of ten powers of two: no partial sum may leave the type."""
+    b = Batch([700, 40], [q, 3], 8, 2, 128, 16, "bf16", seed=39)
+    b.q *= 2
+    big = 2.0 ** 100
+    ref, tol = b.reference()
+    b.vc = (b.vc.float() * big).to(torch.bfloat16)
+    got = Dev(b).run().cpu().double().numpy() / big
+    assert pkv.pkv_device_errors() == 0
+    assert np.abs(got - ref).max() <= tol  # a power of two scales everything exactly
+
+
 @pytest.mark.parametrize("q", [20, 40])
 @pytest.mark.parametrize("scale", [-0.09, 0.0])
 def test_scales_that_are_not_positive(q, scale):
