@@ -69,7 +69,7 @@ namespace {
 // ---------------------------------------------------------------- geometry
 template <int D, int N, bool F8>
 struct Geo {
-  static constexpr int kD = D, kN = N, kPair = 1;
+  static constexpr int kD = D, kN = N;
   static constexpr bool kF8 = F8;
   static constexpr int kEs = F8 ? 1 : 2;
   static constexpr int kRowB = D * kEs;                       // one K or V row
@@ -823,7 +823,7 @@ cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t m
    : N == 32 ? launch_items<Geo<D, 32, F8>>(tree_tc_kernel<D, 32, F8>, a, most, num_sms, st)    \
              : launch_items<Geo<D, 64, F8>>(tree_tc_kernel<D, 64, F8>, a, most, num_sms, st))
   if (N == 128)
-    e = launch_tree_wide(a, rows, most, num_sms, st);
+    e = launch_tree_wide(a, most, num_sms, st);
   else if (p.D == 128)
     e = f8 ? PKV_TC1(128, true) : PKV_TC1(128, false);
   else

@@ -101,13 +101,6 @@ __device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, ui
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// the same barrier of both CTAs of a cluster
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3) : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -139,40 +132,21 @@ __device__ __forceinline__ void tm_ld(uint32_t a, uint32_t (&x)[32]) {
   tm_ld(a, lo);
   tm_ld(a + 16, hi);
 }
-// kPair: the copy goes to the same place in both CTAs of a cluster, and counts on both's barrier
-template <int kPair>
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar,
                                         uint64_t pol) {
-  if constexpr (kPair == 1) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
-        "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(pol)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint [%0], "
-        "[%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"((uint16_t)3), "l"(pol)
-        : "memory");
-  }
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(pol)
+      : "memory");
 }
-template <int kPair>
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int c0, const int (&r)[4],
                                             uint32_t bar, uint64_t pol) {
-  if constexpr (kPair == 1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "l"(pol)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8, %9;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "h"((uint16_t)3), "l"(pol)
-        : "memory");
-  }
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar), "l"(pol)
+      : "memory");
 }
 __device__ __forceinline__ uint64_t l2_normal_policy() {
   uint64_t pol;
@@ -386,18 +360,17 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
     if (bx) {
       // past the sequence, or a page out of range: out of bounds, which TMA fills with zeros
       const int mine = sl[0] >= 0 ? sl[0] : (int)(p.num_blocks * p.bs);
-      const int per = n_box / G_::kPair, b0 = (int)(blockIdx.x % G_::kPair) * per;  // this CTA's: 4, 8 or 16
 #pragma unroll 1
-      for (int b = b0; b < b0 + per; b += 8 / G_::kPair) {
-        int s8[8 / G_::kPair];
+      for (int b = 0; b < n_box; b += 8) {
+        int s8[8];
 #pragma unroll
-        for (int k = 0; k < 8 / G_::kPair; ++k) s8[k] = __shfl_sync(0xffffffffu, mine, b + k);
+        for (int k = 0; k < 8; ++k) s8[k] = __shfl_sync(0xffffffffu, mine, b + k);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8 / G_::kPair; ++k)
+          for (int k = 0; k < 8; ++k)
 #pragma unroll
             for (int u = 0; u < G_::kSub; ++u)
-              tma_box<G_::kPair>(dst + u * kKeys * AT + (b + k) * bx * AT, map, u * (AT / G_::kEs), h, s8[k], full, pol);
+              tma_box(dst + u * kKeys * AT + (b + k) * bx * AT, map, u * (AT / G_::kEs), h, s8[k], full, pol);
         }
         __syncwarp();
       }
@@ -407,7 +380,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
       for (int e = 0; e < 4; ++e) r[e] = sl[e] >= 0 ? sl[e] * Hkv + h : h;  // any row: the softmax drops it
       // four at a time: with a shuffle before every copy each took 150 clocks
 #pragma unroll 1
-      for (int b = (int)(blockIdx.x % G_::kPair) * (32 / G_::kPair), e = b + 32 / G_::kPair; b < e; b += 4) {
+      for (int b = 0; b < 32; b += 4) {
         int q[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -418,7 +391,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
           for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int u = 0; u < G_::kSub; ++u)
-              tma_gather4<G_::kPair>(dst + u * kKeys * AT + (b + k) * 4 * AT, map, u * (AT / G_::kEs), q[k], full, pol);
+              tma_gather4(dst + u * kKeys * AT + (b + k) * 4 * AT, map, u * (AT / G_::kEs), q[k], full, pol);
         }
         __syncwarp();
       }
@@ -436,7 +409,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
     Item it;
     ok = c.take(ir, it);
     if (!ok || it.nt == 0) break;
-    const uint64_t pol = it.q_s * G <= N * G_::kPair ? pol_once : pol_keep;
+    const uint64_t pol = it.q_s * G <= N ? pol_once : pol_keep;
     int32_t blk[4], nb[4];
     pages(it, 0, blk);
     for (int t = 0; t < it.nt; ++t, ++g) {
@@ -470,14 +443,6 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
     }
     if (!ok) break;
   }
-  // the other CTA's MMAs arrive on this one's barriers: the last ones are awaited
-  if (G_::kPair > 1 && ok) {
-    Ring q = r;
-    for (int k = 0; k < ns; ++k) {
-      ok = wait_bar(empty + 8 * q.at, q.pass ^ 1) && ok;
-      q.next(ns);
-    }
-  }
   if (!ok) *c.abort_flag = 1;
   if (c.aborted())  // let the copies issued so far land before the CTA exits
     for (int k = 0; k < ns && k < g; ++k) {
@@ -509,7 +474,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   Ring ir;
   bool ok = true;
   gb = -32;
-  for (int j = 0, x = blockIdx.x / G_::kPair;; ++j, x += gridDim.x / G_::kPair) {
+  for (int j = 0, x = blockIdx.x;; ++j, x += gridDim.x) {
     // item number x of the call
     while (x - base >= total && gb < p.B) {
       base += total;
@@ -527,7 +492,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
         if (!bad && q_s > 0) {
           chunk = tree_chunk(n, q_s, a.chunking);
           nchunks = (n - 1) / chunk + 1;
-          rts = (q_s * G - 1) / (N * G_::kPair) + 1;
+          rts = (q_s * G - 1) / N + 1;
           cnt = nchunks * Hkv * rts;
         }
       }
@@ -550,7 +515,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       it.nchunks = __shfl_sync(0xffffffffu, nchunks, o);
       const int rt_n = __shfl_sync(0xffffffffu, rts, o), len = __shfl_sync(0xffffffffu, chunk, o);
       const int z = y / rt_n;
-      it.r0 = ((y - z * rt_n) * G_::kPair + (int)(blockIdx.x % G_::kPair)) * N;
+      it.r0 = (y - z * rt_n) * N;
       it.c = z / Hkv;
       it.h = z - it.c * Hkv;
       it.k0 = it.c * len;
@@ -732,25 +697,10 @@ cudaError_t launch_items(Kern kern, TcArgs a, int64_t max_items, int num_sms, cu
     return cudaErrorInvalidValue;
   cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kern), G_::kSmem);
   if (e != cudaSuccess) return e;
-  if (G_::kPair == 1)
-    return launch_ex(kern, dim3((unsigned)std::min<int64_t>(num_sms, max_items)), dim3(G_::kThreads), G_::kSmem, st, true, a, mk, mv);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(num_sms / G_::kPair, max_items) * G_::kPair));
-  cfg.blockDim = dim3(G_::kThreads);
-  cfg.dynamicSmemBytes = G_::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = G_::kPair;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, mk, mv);
+  return launch_ex(kern, dim3((unsigned)std::min<int64_t>(num_sms, max_items)), dim3(G_::kThreads), G_::kSmem, st, true, a, mk, mv);
 }
 
-// 128 rows a tile, bf16 caches (pkv_tree_wide.cu).  rows: most of a sequence, for each KV head
-cudaError_t launch_tree_wide(const TcArgs& a, int64_t rows, int64_t max_items, int num_sms, cudaStream_t st);
+// 128 rows a tile, bf16 caches (pkv_tree_wide.cu)
+cudaError_t launch_tree_wide(const TcArgs& a, int64_t max_items, int num_sms, cudaStream_t st);
 
 }  // namespace pkv

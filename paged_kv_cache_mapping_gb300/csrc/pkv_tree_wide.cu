@@ -20,11 +20,10 @@
 // cost 4,900 clocks.)  S is read twice, for the largest score and for P, since
 // 128 scores do not fit a thread's registers beside the rest.
 //
-// More than 128 rows: a cluster of two CTAs takes two neighbouring row tiles of
-// the same keys, and each copies half of every K and V tile into both (TMA
-// multicast).  One CTA alone loads 64 KB for 12.6 MFLOP, and with the products
-// and the softmax taken out (a probe) the loads alone took 103 of 133 us; in
-// pairs the 16 trees below went from 131 to 120 us.
+// Not kept: clusters of two CTAs that share K and V tiles by TMA multicast.  They
+// took 107 us for the 16 trees below instead of 110, and gave up more wherever
+// the row tiles are odd (65 nodes instead of 64: 139 us instead of 107) or uneven
+// (29 instead of 26 us for the 23 trees).
 //
 // Bound: the tensor cores run 54 % of the time (a tile of 128 rows and 128 keys
 // at D 128 takes 4.2 MFLOP for S and 8.4 for the two parts of P, about 1,540
@@ -51,9 +50,9 @@ enum : int {
 };
 static_assert(kOffStat + 2 * 2 * 128 * 8 <= kOffStage, "shared memory");
 
-template <int D, int P>
+template <int D>
 struct Wide {
-  static constexpr int kD = D, kN = 128, kPair = P;
+  static constexpr int kD = D, kN = 128;
   static constexpr bool kF8 = false;
   static constexpr int kEs = 2, kRowB = 2 * D, kAtomB = 128;
   static constexpr int kSub = kRowB / kAtomB;
@@ -123,11 +122,11 @@ __device__ __noinline__ void add_poison_row(const TcArgs& a, const Item& it, int
   }
 }
 
-template <int D, int kPair>
-__global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
+template <int D>
+__global__ void __launch_bounds__(Wide<D>::kThreads, 1)
     tree_wide_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v) {
-  using G_ = Wide<D, kPair>;
+  using G_ = Wide<D>;
   constexpr int NK = G_::kNK, NV = G_::kNV, AT = G_::kAtomB;
   const TreeParams& p = a.p;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -153,9 +152,9 @@ __global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(bar(kBKFull + i), 1);
-      mbar_init(bar(kBKEmpty + i), kPair);  // both CTAs have read their copies
+      mbar_init(bar(kBKEmpty + i), 1);
       mbar_init(bar(kBVFull + i), 1);
-      mbar_init(bar(kBVEmpty + i), kPair);
+      mbar_init(bar(kBVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBSFull + i), 2);
@@ -187,7 +186,6 @@ __global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
   }
   fence_before();
   __syncthreads();
-  if (kPair > 1) cluster_sync();  // the other CTA's barriers stand
   fence_after();
   const uint32_t tmem = *tslot;
   grid_dep_wait();
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
           mma_steps<false, 4, 2, 2>(tmem + grp * 128, dq + (uint32_t)(u * 128 * AT >> 4), dk + (uint32_t)(u * kKeys * AT >> 4),
                                     kIdS, u != 0);
         commit(bar(kBSFull + grp));
-        kPair > 1 ? commit_pair(bar(kBKEmpty) + 8 * kr.at) : commit(bar(kBKEmpty) + 8 * kr.at);
+        commit(bar(kBKEmpty) + 8 * kr.at);
         if (is + 1 == ns) commit(bar(kBQEmpty + G_::qbuf(js)));
         // the second arrival hands on what the tile's producer wrote (info)
         mbar_arrive(bar(kBSFull + grp));
@@ -265,7 +263,7 @@ __global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
           mma_p_steps<4>(tmem + G_::kColO + ob * D, tmem + grp * 128 + h * 64, dv + h * (4 * 128), kIdO, t > 0 || h > 0);
           if (h == 1) {
             commit(bar(kBODone));
-            kPair > 1 ? commit_pair(bar(kBVEmpty) + 8 * vr.at) : commit(bar(kBVEmpty) + 8 * vr.at);
+            commit(bar(kBVEmpty) + 8 * vr.at);
             if (t + 1 == nt) commit(bar(kBOFull + ob));
           }
         }
@@ -527,16 +525,13 @@ __global__ void __launch_bounds__(Wide<D, kPair>::kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
-  if (kPair > 1) cluster_sync();  // nothing of the other CTA's is on its way here
 }
 
 }  // namespace
 
-cudaError_t launch_tree_wide(const TcArgs& a, int64_t rows, int64_t max_items, int num_sms, cudaStream_t st) {
-#define PKV_WIDE(D, P) launch_items<Wide<D, P>>(tree_wide_kernel<D, P>, a, max_items, num_sms, st)
-  if (rows > 128) return a.p.D == 128 ? PKV_WIDE(128, 2) : PKV_WIDE(64, 2);
-  return a.p.D == 128 ? PKV_WIDE(128, 1) : PKV_WIDE(64, 1);
-#undef PKV_WIDE
+cudaError_t launch_tree_wide(const TcArgs& a, int64_t max_items, int num_sms, cudaStream_t st) {
+  return a.p.D == 128 ? launch_items<Wide<128>>(tree_wide_kernel<128>, a, max_items, num_sms, st)
+                      : launch_items<Wide<64>>(tree_wide_kernel<64>, a, max_items, num_sms, st);
 }
 
 }  // namespace pkv

@@ -1,7 +1,7 @@
 """Trees wide enough for 128-row tiles (more than 64 query rows for each KV
-head; more than 128 take CTA pairs): odd sizes around the tiles, masks, scores
-that move a row's reference late, pages out of range, and scales that are not
-positive, against the plain 64-bit reference."""
+head): odd sizes around the tiles, masks, scores that move a row's reference
+late, pages out of range, and scales that are not positive, against the plain
+64-bit reference."""
 import numpy as np
 import pytest
 import torch
