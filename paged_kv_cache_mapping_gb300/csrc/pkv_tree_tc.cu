@@ -40,7 +40,7 @@
 // put the rows on the M side: up to 64 rows this kernel is the faster one (64
 // trees of 8 / 12 / 16 nodes times 4 heads over 512 to 4,096 keys: 110 / 128 / 133
 // us here, 126 / 131 / 135 there), above it the other (16 trees of 64 nodes over
-// up to 8,192 keys: 192 and 150 us when it was new, 107 now).
+// up to 8,192 keys: 192 and 150 us when it was new, 110 now).
 //
 // Bound: the memory while there are few rows, then the softmax: with a key per
 // lane each warp runs about 290 instructions for 32 keys and 16 rows.

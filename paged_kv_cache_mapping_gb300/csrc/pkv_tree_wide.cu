@@ -25,16 +25,17 @@
 // the row tiles are odd (65 nodes instead of 64: 139 us instead of 107) or uneven
 // (29 instead of 26 us for the 23 trees).
 //
-// Bound: the tensor cores run 54 % of the time (a tile of 128 rows and 128 keys
-// at D 128 takes 4.2 MFLOP for S and 8.4 for the two parts of P, about 1,540
-// clocks; in the middle of an item a tile takes 2,200, at an item's masked end
-// about 5,000 more), the MMA warp's waits and the softmax take turns being the
-// slower.  Instruction cache: see poll(); code in one place instead of unrolled
-// took 3,000 clocks off every item's start, but the halves of P V, whose
-// descriptors want to be constants, stand twice (124 us in a loop, 116 so).
+// Bound: the K and V tiles, of which each row tile reads all (64 KB for 12.6
+// MFLOP), then the tensor cores (55 % active; a tile takes them about 1,540 clocks
+// of the 2,300 that it takes in all).  Probes of the 16 trees below, 110 us whole:
+// without the softmax 104, without the MMAs 97, without either 93; half of the
+// MMAs 107; the softmax's loops rolled or unrolled 110.  The instruction cache
+// (see poll()): code in one place instead of unrolled took 3,000 clocks off every
+// item's start, but the halves of P V, whose descriptors want to be constants,
+// stand twice (124 us in a loop, 116 so, at the time).
 // Measured, with the join: 16 trees of 64 nodes times 4 heads (256 rows) over
-// 1,024 to 8,192 keys, D 128: 107 us (73 GFLOP of visible pairs, 0.68 PFLOP/s);
-// 23 uneven trees of up to 37 nodes times 5 heads, D 64, pages of 12 slots: 29 us.
+// 1,024 to 8,192 keys, D 128: 110 us (73 GFLOP of visible pairs, 0.67 PFLOP/s);
+// 23 uneven trees of up to 37 nodes times 5 heads, D 64, pages of 12 slots: 26 us.
 //
 // CTA: 16 warps: K, MMA, items and query rows, V, 2 x 4 of softmax, 4 that write.
 #include "pkv_tree_tc.cuh"
