@@ -94,7 +94,7 @@ __device__ __forceinline__ void tm_st(uint32_t a, const uint32_t (&x)[16]) {
 
 // A drafted key's V value is not finite: the softmax warps took it out of the
 // product, and here it goes to the row of this thread if that sees the key, on
-// top of what this thread has just stored.
+// top of what its warp has just stored.
 template <int D>
 __device__ __noinline__ void add_poison_row(const TcArgs& a, const Item& it, int r) {
   const TreeParams& p = a.p;
