@@ -378,17 +378,19 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
       int r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[e] = sl[e] >= 0 ? sl[e] * Hkv + h : h;  // any row: the softmax drops it
-      // four at a time: with a shuffle before every copy each took 150 clocks
+      // eight at a time: with a shuffle before every copy each took 150 clocks (by
+      // twos, fours and eights 123, 104 and 100 us for 7 sequences of up to 40,000
+      // keys in pages of one slot)
 #pragma unroll 1
-      for (int b = 0; b < 32; b += 4) {
-        int q[4][4];
+      for (int b = 0; b < 32; b += 8) {
+        int q[8][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
 #pragma unroll
           for (int x = 0; x < 4; ++x) q[k][x] = __shfl_sync(0xffffffffu, r[x], b + k);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k)
 #pragma unroll
             for (int u = 0; u < G_::kSub; ++u)
               tma_gather4(dst + u * kKeys * AT + (b + k) * 4 * AT, map, u * (AT / G_::kEs), q[k], full, pol);
