@@ -541,11 +541,14 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
           // every warp has read the references
           if (!sync()) { ok = false; break; }
           if (quarter == 0 && lane < NC) rh[lane] = nref;
-          if (any) {  // the same in the group's four warps
+          // the same in the group's four warps.  In an item's first tile there is
+          // nothing to rescale: the sums are zero and the first P V overwrites O,
+          // which until kBOFree belongs to the item before the last
+          if (any && t > 0) {
 #pragma unroll
             for (int c = 0; c < NC; c += 2)
               l2[c / 2] = mul2(l2[c / 2], pk2(__shfl_sync(0xffffffffu, alpha, c), __shfl_sync(0xffffffffu, alpha, c + 1)));
-            // t > 0: every P V so far has run after this wait
+            // every P V so far has run after this wait
             if (!wait_bar(bar(kBODone), (g - 1) & 1)) { ok = false; break; }
             fence_after();
             const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + grp * NC;
