@@ -626,6 +626,9 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
       if (!ok || it.nt == 0) break;
       ok = wait_bar(bar(kBLFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
+      // read before kBLEmpty hands the item on: the softmax warps may then run as
+      // far as item j + 3, which takes this flag's place
+      const bool spoilt = poison[j % 3] == j + 1;
       const int rows = it.q_s * G;
       // lane c (and c + 32): 1 / (row c's sum), and its log2-sum-exp2 for the join
       float inv[kOff];
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
           }
         }
       }
-      if (poison[j % 3] == j + 1 && (D == 128 || d < D)) add_poison<D, N, F8>(a, it, d);
+      if (spoilt && (D == 128 || d < D)) add_poison<D, N, F8>(a, it, d);
     }
     if (!ok) *abort_flag = 1;
   }

@@ -459,6 +459,9 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
       // a group's sum stands against the reference it used last (none: the sum is
       // 0, or NaN), O against the larger one
       const float2 s0 = stat[(j & 1) * 256 + row], s1 = stat[(j & 1) * 256 + 128 + row];
+      // read before kBLEmpty hands the item on: the softmax warps may then run as
+      // far as item j + 3, which takes this flag's place
+      const bool spoilt = poison[j % 3] == j + 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBLEmpty + (j & 1)));
       const float top = fmaxf(s0.y, s1.y), M = top == -INFINITY ? 0.f : top;
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (here && poison[j % 3] == j + 1) add_poison_row<D>(a, it, r);
+      if (here && spoilt) add_poison_row<D>(a, it, r);
       __syncwarp();
     }
     if (!ok) *abort_flag = 1;

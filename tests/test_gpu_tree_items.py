@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests.spec_ref import Batch
-from tests.test_gpu_tree import compare
+from tests.test_gpu_tree import compare, poison
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,17 @@ def test_first_key_leads(kv, q, G, D):
     as_bytes(rows)[first] = as_bytes(lead)
     as_bytes(flat).copy_(as_bytes(rows))
     compare(b)
+
+
+@pytest.mark.parametrize("every", [1, 3])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q,G", ROWS)
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_values_that_are_not_finite_in_many_items(kv, q, G, D, every):
+    """Drafted V rows with NaN in all items, or in every third sequence: each row that sees one shows it."""
+    b = batch(kv, q, G, D, seed=90 + q)
+    for s in range(0, b.B, every):
+        poison(b.vc, int(b.slots(s)[b.ctx[s]]), float("nan"), 3 + s % 7)
+    d = compare(b)
+    want = np.isnan(b.reference()[0])
+    assert want.any() and np.array_equal(torch.isnan(d.out).cpu().numpy(), want)
