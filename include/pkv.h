@@ -481,11 +481,14 @@ PKV_API pkv_status pkv_tree_mask(const pkv_tensor* parents, const pkv_tensor* cu
  * q_s > N_s or N_s beyond its table is recorded (bit 4) and its rows are left
  * as they are; so are rows at or beyond cu_seqlens_q[B].  A key whose block id
  * is out of range is recorded (bit 2) and adds nothing.  Values of keys that a
- * row does not see never reach it, infinities and NaN included.  A row's result
- * depends on its own sequence (lengths, pages' contents, queries, masks) and on
- * the call's shapes (B, Hq, Hkv, max_q_len: they choose how a long sequence is
- * split), not on block size, placement, the other sequences' lengths or their
- * contents.
+ * row does not see never reach it, infinities and NaN included (an infinity in
+ * a context row of V may reach its rows as NaN).  Scores, sums and outputs are
+ * held in fp32; a key's weight enters its product with V with 16 bits on bf16
+ * caches, and on e4m3 caches as f16, 11 bits, down to 2^-33 of the largest.
+ * A row's result depends on its own sequence (lengths, pages' contents,
+ * queries, masks) and on the call's shapes (B, Hq, Hkv, max_q_len: they choose
+ * how a long sequence is split), not on block size, placement, the other
+ * sequences' lengths or their contents.
  *
  * Supported: bf16 q with bf16 or e4m3 caches at D = 64 and 128, f32 q with
  * f32 caches at D a multiple of 32 up to 256; any block size, any Hq / Hkv,

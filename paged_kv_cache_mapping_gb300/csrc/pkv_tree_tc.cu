@@ -29,12 +29,20 @@
 // partials.
 //
 // Types: bf16 caches take bf16 MMAs, P as bf16 hi + lo (about 16 bits).  e4m3
-// caches take the codes as they are (kind::f8f6f4, no conversion): a query row
-// is scaled to a largest element in [128, 256) and split into two e4m3 parts
+// caches: S takes K's codes as they are (kind::f8f6f4, no conversion): a query
+// row is scaled to a largest element in [128, 256) and split into two e4m3 parts
 // (a bf16 element has 8 significant bits, an e4m3 code 4: hi + lo is exact down
-// to 2^-18 of the row's largest element), and P = 16 * 2^(s - ref) <= 2^8.5 into
-// hi and lo, lo scaled by 16 with an accumulator of its own, so that the
-// smallest codes' step is 2^-17 of the row's reference.
+// to 2^-18 of the row's largest element).  P V is in f16: the softmax warps
+// widen V's codes (exactly), and P = 2^8 * 2^(s - ref) <= 2^15.75 is one f16, as
+// in decode: 11 bits, and keys as far as 2^-33 below the reference, which is a
+// score that was seen, still weigh something.  (P as two e4m3 codes saved
+// the widening and lost what lay 15.5 powers of two below the reference: behind
+// one leading key the mass of thousands of small ones went missing, several per
+// cent of an output.  The widening costs: 8 trees of 16 nodes over 32K to 128K
+// keys 341 us instead of 291, 64 trees of 4 / 8 / 16 nodes times 4 heads over
+// 4,096 to 16,384 (16 nodes: 512 to 4,096) keys 277 / 329 / 148 instead of 266 /
+// 283 / 137.  With the V codes' loads behind the wait for S, one after the other
+// between conversions, it was 361.)
 //
 // More than 64 rows (bf16 caches) go to pkv_tree_wide.cu, whose tiles of 128 rows
 // put the rows on the M side: up to 64 rows this kernel is the faster one (64
@@ -61,6 +69,8 @@
 //   then 8 or 16 (N = 64) warps of softmax: lane quarter w % 4 = keys, group
 //               (w - 4) / 4 = rows.
 //   and 4 warps that write O / l of finished items while the next one runs.
+#include <type_traits>
+
 #include "pkv_tree_tc.cuh"
 
 namespace pkv {
@@ -71,24 +81,30 @@ template <int D, int N, bool F8>
 struct Geo {
   static constexpr int kD = D, kN = N;
   static constexpr bool kF8 = F8;
-  static constexpr int kEs = F8 ? 1 : 2;
+  static constexpr int kEs = F8 ? 1 : 2;                      // of a cache element; those of P V have two bytes
   static constexpr int kRowB = D * kEs;                       // one K or V row
   static constexpr int kAtomB = kRowB < 128 ? kRowB : 128;    // swizzle width
   static constexpr int kSub = kRowB / kAtomB;                 // sub-tiles along d
   static constexpr int kTileB = kKeys * kRowB;
   static constexpr int kParts = F8 ? 2 : 1;                   // parts of Q
   static constexpr int kQB = N * kRowB * kParts;
-  static constexpr int kPRow = 2 * N * kEs;                   // both parts of P of one key
+  static constexpr int kVRowB = 2 * D;                        // a V row in the product (e4m3: widened)
+  static constexpr int kVSub = kVRowB / 128;
+  static constexpr int kWideB = F8 ? kKeys * kVRowB : 0;      // a widened V tile; there are two, as of P
+  static constexpr int kParts2 = F8 ? 1 : 2;                  // parts of P
+  static constexpr int kPRow = 2 * N * kParts2;               // P of one key
   static constexpr int kPB = kKeys * (kPRow <= 128 ? 128 : 256);  // [1 or 2][128 keys][128 bytes]
-  static constexpr int kNK = kTileB == 32768 ? 2 : kTileB == 16384 ? 4 : 6;
-  static constexpr int kNV = kTileB == 32768 ? (kPRow == 256 ? 2 : 3) : kTileB == 16384 ? (kPRow == 256 ? 4 : 5) : 6;
+  // tiles of K and of V in flight (of V codes fewer: they are free once they are widened)
+  static constexpr int kNK = F8 ? (D == 128 ? (N == 16 ? 4 : 3) : 6) : D == 128 ? 2 : 4;
+  static constexpr int kNV = F8 ? (D == 128 ? (N == 64 ? 2 : 3) : 6) : D == 128 ? (kPRow == 256 ? 2 : 3) : (kPRow == 256 ? 4 : 5);
   static constexpr int kGroups = N == 64 ? 4 : 2;             // softmax: groups of four warps, each N / kGroups rows
   static constexpr int kSoft = 4 * kGroups;                   // its warps
   static constexpr int kThreads = 32 * (4 + kSoft + 4);
   static constexpr int kNC = N / kGroups;                     // rows (columns of S^T) per softmax warp
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kNK * kTileB;
-  static constexpr int kOffP = kOffV + kNV * kTileB;
+  static constexpr int kOffWide = kOffV + kNV * kTileB;
+  static constexpr int kOffP = kOffWide + 2 * kWideB;
   static constexpr int kOffQ = kOffP + 2 * kPB;
   static constexpr int kQBufs = kPRow == 256 && kTileB == 32768 ? 1 : 2;  // query tiles: the next item's arrives while this one runs
   // item j's query buffer, and the parity of its pass
@@ -96,10 +112,9 @@ struct Geo {
   __device__ static uint32_t qpass(int j) { return (uint32_t)(kQBufs == 2 ? j >> 1 : j) & 1u; }
   static constexpr int kOffMisc = kOffQ + kQBufs * kQB;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
-  // tensor memory: S 2 x N columns, then O 2 x (hi N, lo N)
+  // tensor memory: S 2 x N columns, then O 2 x (hi N, lo N), or 2 x N
   static constexpr uint32_t kColO = 2 * N;
-  static constexpr uint32_t kOCols = 2 * N;
-  static constexpr int kKeyStep = F8 ? 32 : 16;               // keys per MMA k step of P V
+  static constexpr uint32_t kOCols = kParts2 * N;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kNK + 2 <= kInfoSlots, "tile info ring");
   static_assert(kColO + 2 * kOCols <= 512, "tensor memory");
@@ -148,6 +163,76 @@ __device__ __noinline__ void add_poison(const TcArgs& a, const Item& it, int d) 
     }
   }
 }
+
+// A softmax warp's share of a tile of V codes, widened to f16 for the product.  A
+// lane takes 16 codes of a row at a time, 16 bytes in and twice 16 out; the rows
+// of eight neighbouring lanes are chosen so that neither side has bank
+// conflicts.  load() and store() are apart so that waits go between them.
+template <class G_>
+struct WidenV {
+  static constexpr int AT = G_::kAtomB, kRows = kKeys / G_::kSoft;
+  static constexpr int kSteps = kRows / (AT == 128 ? 4 : 8);
+  static_assert(kRows % 8 == 0 && G_::kSub == 1, "codes of a row in one swizzle atom");
+  int row;            // the lane's row in the first step
+  uint32_t from, from_x, to, to_x;  // its place in both tiles: offset, and the swizzled chunk
+  uint32_t w[kSteps][4];
+  __device__ __forceinline__ WidenV(int w_of, int lane) {
+    // D = 128: eight lanes hold four chunks of rows r and r ^ 5; D = 64: all four of rows r and r ^ 1
+    const int ch = AT == 128 ? (lane & 3) | (lane & 8) >> 1 : lane & 3;
+    const int r = AT == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+    row = w_of * kRows + r;
+    from = row * AT;
+    from_x = (ch ^ (AT == 128 ? r : r >> 1)) << 4;
+    to = (ch >> 2) * (kKeys * 128) + row * 128;
+    to_x = (((2 * ch) & 7) ^ r) << 4;
+  }
+  // rows further down, and the change of the swizzle: D = 128: steps take rows 0,
+  // 1, 4, 5 and 2, 3, 6, 7 of eight
+  __device__ static constexpr int down(int b) { return AT == 128 ? (b & 1) * 2 + (b >> 1) * 8 : b * 8; }
+  __device__ static constexpr uint32_t turn(int b) { return (AT == 128 ? (b & 1) * 2 : 0) << 4; }
+  __device__ __forceinline__ void load(uint32_t codes) {
+#pragma unroll
+    for (int b = 0; b < kSteps; ++b)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[b][0]), "=r"(w[b][1]), "=r"(w[b][2]), "=r"(w[b][3])
+                   : "r"(codes + from + down(b) * AT + (from_x ^ turn(b))));
+  }
+  // what clean_v does to a bf16 tile; true: a drafted value is not finite
+  __device__ __forceinline__ bool clean(int kt, int ctx, int k1, const uint4& bad) {
+    bool found = false;
+    const int first = row & ~31;
+    const uint32_t bm = first == 0 ? bad.x : first == 32 ? bad.y : first == 64 ? bad.z : bad.w;  // a warp's rows lie in one word
+#pragma unroll
+    for (int b = 0; b < kSteps; ++b) {
+      const int kk = row + down(b), ky = kt + kk;
+      const bool gone = ky >= k1 || ((bm >> (kk & 31)) & 1u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // NaN, the only code that is not finite: ones all over but for the sign,
+        // which carry into the sign's place
+        const uint32_t t = ky >= ctx ? ((w[b][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : 0u;
+        found |= t != 0 && !gone;
+        w[b][e] = gone ? 0u : w[b][e] & ~((t >> 7) * 0xffu);
+      }
+    }
+    return found;
+  }
+  __device__ __forceinline__ void store(uint32_t wide) const {
+#pragma unroll
+    for (int b = 0; b < kSteps; ++b) {
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) e4m3x4_to_f16(w[b][e], h[2 * e], h[2 * e + 1]);
+      const uint32_t at = wide + to + down(b) * 128 + (to_x ^ turn(b));
+      st_s128(at, h[0], h[1], h[2], h[3]);
+      st_s128(at ^ 16, h[4], h[5], h[6], h[7]);
+    }
+  }
+};
+struct NoWiden {
+  __device__ __forceinline__ NoWiden(int, int) {}
+};
+
 template <int D, int N, bool F8>
 __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap tm_k,
@@ -159,7 +244,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
   unsigned char* misc = smem + G_::kOffMisc;
   const uint32_t s0 = smem_u32(smem), b0 = smem_u32(misc);
   auto bar = [&](int i) -> uint32_t { return b0 + 8 * i; };
-  const uint32_t sK = s0 + G_::kOffK, sV = s0 + G_::kOffV, sP = s0 + G_::kOffP, sQ = s0 + G_::kOffQ;
+  const uint32_t sK = s0 + G_::kOffK, sV = s0 + G_::kOffV, sP = s0 + G_::kOffP, sQ = s0 + G_::kOffQ, sW = s0 + G_::kOffWide;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 8 * kSAbort);
   volatile int* poison = reinterpret_cast<volatile int*>(misc + 8 * kSPoison);  // [3]: item + 1
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 8 * kSTmem);
@@ -189,7 +274,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(bar(kBVFull + i), 1);
-      mbar_init(bar(kBVEmpty + i), 1);
+      mbar_init(bar(kBVEmpty + i), F8 ? G_::kSoft : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBSFull + i), 2);
@@ -233,7 +318,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     copy_tiles<G_>(a, cta, warp == 3, warp == 3 ? sV : sK, warp == 3 ? &tm_v : &tm_k);
   } else if (warp == 1) {
     // ======================= MMA =======================
-    constexpr uint32_t kIdS = idesc(N, F8, false, false), kIdO = idesc(2 * N, F8, true, true);
+    constexpr uint32_t kIdS = idesc(N, F8, false, false), kIdO = idesc(G_::kParts2 * N, F8, true, true);
     Ring ir, kr, vr;
     int j = 0, g = 0, nt = 0;
     // S of tile gg from the next K tile
@@ -275,22 +360,22 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
       if (nt2 > 0 || t + 1 < nt) ok = issue_s(gs, qb);
       if (nt > 0 && ok) {
         const int ob = ~j & 1;
-        ok = wait_bar(bar(kBVFull) + 8 * vr.at, vr.pass) && (t > 0 || wait_bar(bar(kBOFree + ob), (((j - 1) >> 1) & 1) ^ 1)) &&
+        // (e4m3: the arrivals on P's barrier tell of the widened V tile too)
+        ok = (F8 || wait_bar(bar(kBVFull) + 8 * vr.at, vr.pass)) && (t > 0 || wait_bar(bar(kBOFree + ob), (((j - 1) >> 1) & 1) ^ 1)) &&
              wait_bar(bar(kBPFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
         fence_after();
-        // V^T: d contiguous, 8 keys = 8 AT bytes, sub-tiles kKeys AT apart.  With
-        // D = 64 the M side's upper 64 rows repeat shifted keys; their lanes
+        // V^T: d contiguous, 8 keys = 1,024 bytes, sub-tiles of d kKeys * 128 apart.
+        // With D = 64 the M side's upper 64 rows repeat shifted keys; their lanes
         // are never read.
-        constexpr int KS = G_::kKeyStep;
-        const uint64_t dv = sdesc(sV + vr.at * G_::kTileB, G_::kSub > 1 ? kKeys * AT : 8 * AT, 8 * AT, AT);
+        const uint32_t v_at = F8 ? sW + (g & 1) * G_::kWideB : sV + vr.at * G_::kTileB;
+        const uint64_t dv = sdesc(v_at, G_::kVSub > 1 ? kKeys * 128 : 1024, 1024, 128);
         const uint64_t dp = sdesc(sP + (g & 1) * G_::kPB, kKeys * 128, 1024, 128);
         const uint32_t to = tmem + G_::kColO + ob * G_::kOCols;
         if (elect_one()) {
-          mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv, dp, kIdO, t > 0);
-          if constexpr (!F8) mma_steps<F8, 4, KS * AT / 16, KS * 8>(to, dv + 4 * KS * AT / 16, dp + 4 * KS * 8, kIdO, 1);
+          mma_steps<false, 8, 128, 128>(to, dv, dp, kIdO, t > 0);  // 16 keys of 128 bytes a step
           commit(bar(kBODone));
-          commit(bar(kBVEmpty) + 8 * vr.at);
+          if (!F8) commit(bar(kBVEmpty) + 8 * vr.at);
           if (t + 1 == nt) commit(bar(kBOFull + ob));
         }
         __syncwarp();
@@ -320,12 +405,11 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     // p may pass 2^0 (e4m3: 2^kUp, times which p is kept) by 2^kTau before a
     // row's reference moves.  bf16 parts keep their precision over the whole
     // exponent range, so the first reference is 0 unless the row's largest
-    // score lies beyond +-kTau; e4m3 parts want the largest p near 2^kUp.
-    constexpr float kTau = F8 ? 4.5f : 16.f;
-    constexpr float kUp = F8 ? 4.f : 0.f;
-    // an e4m3 row's reference is set this far above the largest score seen, so
-    // that it rarely has to move again in a chunk
-    constexpr float kMargin = F8 ? 2.5f : 0.f;
+    // score lies beyond +-kTau.  f16 ends at 2^16 and below 2^-25: half of its
+    // range on either side of 2^kUp leaves 33 powers of two downwards, and few
+    // rows whose reference has to move again.
+    constexpr float kTau = F8 ? 7.75f : 16.f;
+    constexpr float kUp = F8 ? 8.f : 0.f;
     float* xh = xch + grp * 4 * NC;
     // A vote of the group's four warps, cast and counted apart so that work can
     // go between: count() tells all four alike whether any of them wanted.
@@ -351,9 +435,10 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     };
     // this lane's row of P, at the first of the warp's columns in the hi part; a
     // further 16-byte chunk's place, and the lo part's, differ by an exclusive or
-    const uint32_t p_at = sP + swz<128>(tg, grp * NC * G_::kEs / 16) + (grp * NC * G_::kEs) % 16;
+    const uint32_t p_at = sP + swz<128>(tg, grp * NC / 8);
     if (tg < NC) refs[grp * NC + tg] = kUp;  // item 0's
-    Ring ir;
+    Ring ir, vr;                // (vr, wv: e4m3)
+    typename std::conditional<F8, WidenV<G_>, NoWiden>::type wv(warp - 4, lane);
     int g = 0;
     bool ok = sync();
     for (int j = 0; ok; ++j) {
@@ -376,6 +461,14 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
       for (int c = 0; c < NC / 2; ++c) l2[c] = 0ull;
       uint32_t vmask = 0;  // rows of the group without a reference yet (stored as 0), once the first tile has set them
       for (int t = 0; t < nt; ++t, ++g) {
+        if constexpr (F8) {
+          ok = wait_bar(bar(kBVFull) + 8 * vr.at, vr.pass);
+          if (!ok) break;
+          wv.load(sV + vr.at * G_::kTileB);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBVEmpty) + 8 * vr.at);
+          vr.next(NV);
+        }
         ok = wait_bar(bar(kBSFull + (g & 1)), (g >> 1) & 1);
         if (!ok) break;
         fence_after();
@@ -403,12 +496,18 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
               }
             }
           }
+        }
+        if constexpr (F8) {
+          if (masked && wv.clean(kt, ctx, it.k1, bad)) poison[j % 3] = j + 1;
+          // the widened tile before the last has been read: its P V came before this tile's S
+          wv.store(sW + (g & 1) * G_::kWideB);
+        } else if (masked) {
           if (!wait_bar(bar(kBVFull + g % NV), (g / NV) & 1)) { ok = false; break; }
           if (clean_v<G_>(sV + (g % NV) * G_::kTileB, warp - 4, G_::kSoft, lane, kt, ctx, it.k1, bad)) poison[j % 3] = j + 1;
         }
         // y = score in base 2 less the row's reference, plus kUp
         float y[NC];
-        uint32_t hi[F8 ? NC / 4 : NC / 2], lo[F8 ? NC / 4 : NC / 2];
+        uint32_t hi[NC / 2], lo[NC / 2];  // (lo: bf16)
         if (F8 && t == 0 && !masked) {
           // the first reference, from the row's largest score among 32 of the
           // tile's keys (each warp takes a quarter of the rows over its own keys)
@@ -424,7 +523,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
             m = lane == cc && cc < kSample ? x : m;
           }
           const bool none = lane < NC / 4 && m == -INFINITY;
-          if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - kMargin - m;
+          if (lane < NC / 4) rh[quarter * (NC / 4) + lane] = none ? kUp : kUp - m;
           const uint32_t unset = __ballot_sync(0xffffffffu, none) << (quarter * (NC / 4));
           if (lane == 0) unset4[grp * 4 + quarter] = unset;
           __syncwarp();
@@ -472,29 +571,17 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
             cast(__any_sync(0xffffffffu, want));
           }
           if (mode != kCareful) {
-            // P = 2^y in two parts, row = key, hi in columns 0 .. N - 1, lo in N .. 2 N - 1
-            // (while the vote is out: if it asks for care, all of this is done again)
+            // P = 2^y, row = key: one f16, or bf16 hi in columns 0 .. N - 1 and lo in N ..
+            // 2 N - 1 (while the vote is out: if it asks for care, all of this is done again)
 #pragma unroll
             for (int c = 0; c < NC; c += 2) {
               const float p0 = ex2(y[c]), p1 = ex2(y[c + 1]);
-              const unsigned long long pp = pk2(p0, p1);
               y[c] = p0;
               y[c + 1] = p1;
               if constexpr (F8) {
-                // through f16 (11 bits, two values at a time): hi its e4m3 code, lo
-                // that of 16 times the exact remainder
-                const __half2 h = __floats2half2_rn(p0, p1);
-                const uint16_t h2 = f16x2_to_e4m3x2(h);
-                const uint32_t hb = e4m3x2_to_f16x2(h2);
-                const uint16_t l8 = f16x2_to_e4m3x2(__hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&hb)), __float2half2_rn(16.f)));
-                if (c & 2) {
-                  hi[c / 4] |= (uint32_t)h2 << 16;
-                  lo[c / 4] |= (uint32_t)l8 << 16;
-                } else {
-                  hi[c / 4] = h2;
-                  lo[c / 4] = l8;
-                }
+                hi[c / 2] = pack_f16(p0, p1);
               } else {
+                const unsigned long long pp = pk2(p0, p1);
                 const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                 hi[c / 2] = __byte_perm(u0, u1, 0x7632);
                 float r0, r1;  // p - hi exactly: the truncated-away low bits
@@ -529,10 +616,10 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
             nref = old;
             if ((t == 0 && (!F8 || masked)) || ((vmask >> lane) & 1u)) {  // none yet, 0 stands in
               none = top == -INFINITY;
-              if (!none && (F8 || fabsf(top) > kTau)) nref = old + kUp - kMargin - top;
+              if (!none && (F8 || fabsf(top) > kTau)) nref = old + kUp - top;
             } else if (top > kTau + kUp) {
-              nref = old + kUp - kMargin - top;
-              alpha = ex2(kUp - kMargin - top);
+              nref = old + kUp - top;
+              alpha = ex2(kUp - top);
               moved = true;
             }
           }
@@ -554,18 +641,18 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
             const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + grp * NC;
 #pragma unroll 1
             for (int b = 0; b < NC; b += 8) {
-              uint32_t o[8], o2[8];
+              uint32_t o[8], o2[8];  // (o2: bf16)
               tm_ld(to + b, o);
-              tm_ld(to + N + b, o2);
+              if (!F8) tm_ld(to + N + b, o2);
               wait_ld();
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const float f = __shfl_sync(0xffffffffu, alpha, b + c);
                 o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                o2[c] = __float_as_uint(__uint_as_float(o2[c]) * f);
+                if (!F8) o2[c] = __float_as_uint(__uint_as_float(o2[c]) * f);
               }
               tm_st(to + b, o);
-              tm_st(to + N + b, o2);
+              if (!F8) tm_st(to + N + b, o2);
             }
             wait_st();
           }
@@ -578,16 +665,11 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
         for (int c = 0; c < NC; c += 2) l2[c / 2] = add2(l2[c / 2], pk2(y[c], y[c + 1]));
         // the P buffer is free: P V of the tile before the last came before this tile's S
         {
-          const uint32_t at = p_at + (g & 1) * G_::kPB, at_lo = G_::kPRow == 256 ? at + kKeys * 128 : at ^ (N * G_::kEs);
-          if constexpr (NC * G_::kEs == 8) {
-            st_s64(at, hi[0], hi[1]);
-            st_s64(at_lo, lo[0], lo[1]);
-          } else {
+          const uint32_t at = p_at + (g & 1) * G_::kPB, at_lo = G_::kPRow == 256 ? at + kKeys * 128 : at ^ (2 * N);
 #pragma unroll
-            for (int q = 0; q < NC * G_::kEs / 16; ++q) {
-              st_s128(at ^ (q << 4), hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-              st_s128(at_lo ^ (q << 4), lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
-            }
+          for (int q = 0; q < NC / 8; ++q) {
+            st_s128(at ^ (q << 4), hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+            if (!F8) st_s128(at_lo ^ (q << 4), lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
           }
         }
         fence_proxy_async_smem();
@@ -615,7 +697,6 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
     // ======================= O / l: lane = d, register = row =======================
     const int d = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    constexpr float kLo = F8 ? 0.0625f : 1.f;  // the low part's weight
     constexpr int kCols = 16;            // rows at a time
     constexpr int kOff = (N + 31) / 32;  // row offsets held by a lane
     Ring ir;
@@ -667,7 +748,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
         const uint32_t to = tmem + G_::kColO + (j & 1) * G_::kOCols + lane_off + b;
         uint32_t o[kCols], o2[kCols];
         tm_ld(to, o);
-        tm_ld(to + N, o2);
+        if (!F8) tm_ld(to + N, o2);
         float v[kCols];
         wait_ld();
         if (b + kCols == N) {  // the accumulator has been read
@@ -679,8 +760,8 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           const float sc = __shfl_sync(0xffffffffu, si, (b & 31) + c);
-          const float x = fmaf(__uint_as_float(o2[c]), kLo, __uint_as_float(o[c])) * sc;
-          v[c] = sc == 0.f ? 0.f : x;
+          const float x = __uint_as_float(o[c]) + (F8 ? 0.f : __uint_as_float(o2[c]));
+          v[c] = sc == 0.f ? 0.f : x * sc;
         }
         long long at[kCols];
         const long long from = kOff > 1 && b >= 32 ? off[kOff - 1] : off[0];

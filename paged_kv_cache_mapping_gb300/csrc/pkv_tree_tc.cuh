@@ -75,7 +75,8 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
          ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | ((uint64_t)(atom == 128 ? 2 : 4) << 61);
 }
 
-// instruction descriptor: fp32 accumulator, A and B bf16 (or e4m3), M 128, N n
+// instruction descriptor: fp32 accumulator, A and B bf16 (f8: e4m3, or in kind::f16
+// f16, which have the same code), M 128, N n
 __host__ __device__ constexpr uint32_t idesc(int n, bool f8, bool a_mn, bool b_mn) {
   return (1u << 4) | ((f8 ? 0u : 1u) << 7) | ((f8 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -245,11 +246,6 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
 __device__ __forceinline__ float redux_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(__half2 h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
   return r;
 }
 
