@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "pkv.h"
@@ -77,24 +78,47 @@ struct Tensors {
   }
 };
 
+struct WithoutLock {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~WithoutLock() { PyEval_RestoreThread(state); }
+};
+
 // Runs f(stream) with the device current, without the interpreter lock.
 template <typename F>
 PyObject* run(int dev, F f) {
+  pkv_status rc;
+  {
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+    cudaStream_t st = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+    const WithoutLock unlocked;
+    rc = f(st);
+  }
+  return PyLong_FromLong(rc);
+}
+
+// A method as Python calls it.  PyTorch throws, for a tensor without storage
+// (sparse, or under vmap) already when its address is asked for, and no C++
+// exception may leave through the interpreter's frames: it becomes a Python one.
+template <PyObject* (*kBody)(PyObject* const*, Py_ssize_t)>
+PyObject* method(PyObject*, PyObject* const* a, Py_ssize_t n) {
   try {
-    pkv_status rc;
-    {
-      const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-      cudaStream_t st = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-      Py_BEGIN_ALLOW_THREADS;
-      rc = f(st);
-      Py_END_ALLOW_THREADS;
-    }
-    return PyLong_FromLong(rc);
+    return kBody(a, n);
+  } catch (python_error& e) {
+    e.restore();
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
   }
+  return nullptr;
 }
+
+// A reference that is given up when it goes out of scope.
+struct Held {
+  PyObject* o;
+  explicit Held(PyObject* p) : o(p) {}
+  Held(const Held&) = delete;
+  Held& operator=(const Held&) = delete;
+  ~Held() { Py_XDECREF(o); }
+};
 
 bool want(Py_ssize_t n, Py_ssize_t expected) {
   if (n != expected) PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", expected, n);
@@ -107,7 +131,7 @@ bool real(PyObject* o, float& x) {
 }
 
 // bind(PkvError, rope_append, tree_mask, tree_attention, tree_commit): addresses as integers
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   if (!want(n, 5)) return nullptr;
   void* p[4];
   for (int i = 0; i < 4; ++i) {
@@ -124,7 +148,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // rope_append(q, k, v, positions, slot_mapping, rope, q_out, k_cache, v_cache, k_scale, v_scale)
-PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
   if (!want(n, 11)) return nullptr;
   Tensors t;
   float ks, vs;
@@ -132,58 +156,43 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !t.add(a[4], "slot_mapping") || !t.add(a[6], "q_out") || !t.add(a[7], "k_cache") || !t.add(a[8], "v_cache") ||
       !real(a[9], ks) || !real(a[10], vs))
     return nullptr;
-  Py_buffer b;
+  struct Buffer : Py_buffer {
+    ~Buffer() { PyBuffer_Release(this); }
+  } b;
+  b.obj = nullptr;  // nothing to release until it is filled
   if (PyObject_GetBuffer(a[5], &b, PyBUF_SIMPLE) != 0) return nullptr;
   if (b.len != sizeof(pkv_rope)) {
-    PyBuffer_Release(&b);
     PyErr_SetString(PyExc_TypeError, "rope must come from pkv_rope_init");
     return nullptr;
   }
-  PyObject* r = run(t.dev, [&](cudaStream_t st) {
+  return run(t.dev, [&](cudaStream_t st) {
     return f_rope_append(&t.t[0], &t.t[1], &t.t[2], &t.t[3], &t.t[4], static_cast<const pkv_rope*>(b.buf), &t.t[5], &t.t[6],
                          &t.t[7], ks, vs, st);
   });
-  PyBuffer_Release(&b);
-  return r;
 }
 
 // tree_mask(parents, cu_seqlens_q, seq_lens, max_q_len, tree_mask or None, positions or None) -> (status, tree_mask,
 // positions); what is None is allocated
-PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* tree_mask(PyObject* const* a, Py_ssize_t n) {
   if (!want(n, 6)) return nullptr;
   Tensors t;
   if (!t.add(a[0], "parents") || !t.add(a[1], "cu_seqlens_q") || !t.add(a[2], "seq_lens")) return nullptr;
   const long long max_q = PyLong_AsLongLong(a[3]);
   if (PyErr_Occurred()) return nullptr;
-  PyObject* out[2] = {a[4], a[5]};
-  Py_INCREF(out[0]);
-  Py_INCREF(out[1]);
-  PyObject* r = nullptr;
-  try {
-    const at::Tensor& parents = THPVariable_Unpack(a[0]);
-    if (out[0] == Py_None) {
-      const long long words = max_q > 32 ? (max_q + 31) / 32 : 1;
-      Py_SETREF(out[0], THPVariable_Wrap(at::empty({parents.dim() == 1 ? parents.size(0) : 0, words}, parents.options())));
-    }
-    if (out[0] != nullptr && out[1] == Py_None) Py_SETREF(out[1], THPVariable_Wrap(at::empty(parents.sizes(), parents.options())));
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    Py_XDECREF(out[0]);
-    Py_XDECREF(out[1]);
-    return nullptr;
-  }
-  if (out[0] != nullptr && out[1] != nullptr && t.add(out[0], "tree_mask") && t.add(out[1], "positions")) {
-    PyObject* rc = run(t.dev, [&](cudaStream_t st) { return f_tree_mask(&t.t[0], &t.t[1], &t.t[2], &t.t[3], &t.t[4], st); });
-    if (rc != nullptr) r = Py_BuildValue("(NOO)", rc, out[0], out[1]);
-  }
-  Py_XDECREF(out[0]);
-  Py_XDECREF(out[1]);
-  return r;
+  const at::Tensor& parents = THPVariable_Unpack(a[0]);
+  const Held mask(a[4] == Py_None ? THPVariable_Wrap(at::empty({parents.dim() == 1 ? parents.size(0) : 0, max_q > 32 ? (max_q - 1) / 32 + 1 : 1},
+                                                               parents.options()))
+                                  : Py_NewRef(a[4]));
+  if (mask.o == nullptr) return nullptr;
+  const Held positions(a[5] == Py_None ? THPVariable_Wrap(at::empty(parents.sizes(), parents.options())) : Py_NewRef(a[5]));
+  if (positions.o == nullptr || !t.add(mask.o, "tree_mask") || !t.add(positions.o, "positions")) return nullptr;
+  const Held rc(run(t.dev, [&](cudaStream_t st) { return f_tree_mask(&t.t[0], &t.t[1], &t.t[2], &t.t[3], &t.t[4], st); }));
+  return rc.o != nullptr ? Py_BuildValue("(OOO)", rc.o, mask.o, positions.o) : nullptr;
 }
 
 // tree_attention(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, tree_mask, scale, k_scale, v_scale, max_q_len,
 //                out, workspace)
-PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* tree_attention(PyObject* const* a, Py_ssize_t n) {
   if (!want(n, 13)) return nullptr;
   Tensors t;
   float scale, ks, vs;
@@ -213,7 +222,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // tree_commit(accepted, accepted_lens, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, new_seq_lens)
-PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* tree_commit(PyObject* const* a, Py_ssize_t n) {
   if (!want(n, 8)) return nullptr;
   Tensors t;
   if (!t.add(a[0], "accepted") || !t.add(a[1], "accepted_lens") || !t.add(a[2], "cu_seqlens_q") || !t.add(a[3], "seq_lens") ||
@@ -224,7 +233,7 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-#define PKV_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
+#define PKV_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(method<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PKV_METHOD(bind),           PKV_METHOD(rope_append), PKV_METHOD(tree_mask),
                          PKV_METHOD(tree_attention), PKV_METHOD(tree_commit), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
