@@ -492,7 +492,8 @@ PKV_API pkv_status pkv_tree_mask(const pkv_tensor* parents, const pkv_tensor* cu
  *
  * Supported: bf16 q with bf16 or e4m3 caches at D = 64 and 128, f32 q with
  * f32 caches at D a multiple of 32 up to 256; any block size, any Hq / Hkv,
- * any q_s; num_blocks * block_size * Hkv within int32.
+ * any q_s; num_blocks * block_size * Hkv within int32, and for bf16 q at most
+ * 2^30 query rows in all (T * Hq).
  */
 PKV_API pkv_status pkv_tree_attention_workspace_size(const pkv_tensor* q, const pkv_tensor* block_tables,
                                                      const pkv_tensor* k_cache, int32_t max_q_len, size_t* bytes);

@@ -313,8 +313,8 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
   PKV_NEED(out->dtype == PKV_F32 || out->dtype == PKV_BF16, "out must be f32 or bf16");
   PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX - kTreeKeyTile, "max_blocks * block_size beyond int32");
   PKV_NEED(NB >= 1, "the cache has no blocks");
-  if (T * Hq > INT32_MAX / 2 || B * 64 * Hq * ((T + 15) / 16) > INT32_MAX / 2)
-    return fail(PKV_ERR_UNSUPPORTED, "too many rows or sequences for 32-bit work items");
+  if (q->dtype != PKV_F32 && T > (int64_t(1) << 30) / Hq)
+    return fail(PKV_ERR_UNSUPPORTED, "T * Hq beyond 2^30 (a sequence's rows and work items are numbered in 32 bits)");
   if (NB * bs > INT32_MAX / Hkv)
     return fail(PKV_ERR_UNSUPPORTED, "num_blocks * block_size * Hkv beyond int32 (rows are numbered in 32 bits)");
   PKV_TRY(check_mask("tree_mask", tree_mask, T));

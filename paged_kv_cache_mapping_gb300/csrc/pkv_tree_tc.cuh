@@ -464,7 +464,12 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   auto bar = [&](int i) -> uint32_t { return cta.bar(i); };
   int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
   int c0 = 0, q_s = 0, n = 0, chunk = 1, nchunks = 0, rts = 0;
-  int cnt = 0, incl = 0, base = 0, total = 0;  // items: this sequence's, prefix in the group; before it; in it
+  // items: this sequence's, prefix in the group, in it; before it.  A sequence has
+  // at most Hq max(1024, q_s) / 16 + 64 Hkv of them, 2^27 since T Hq <= 2^30, and so
+  // a group's fit 32 bits, whatever the lengths are
+  int cnt = 0;
+  uint32_t incl = 0, total = 0;
+  int64_t base = 0;
   constexpr int kLanes = D / 8;          // lanes of a row (8 bf16 elements each)
   constexpr int kPer = 32 / kLanes;      // rows per step
   constexpr int kStepsQ = N / kPer;
@@ -472,7 +477,8 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   Ring ir;
   bool ok = true;
   gb = -32;
-  for (int j = 0, x = blockIdx.x;; ++j, x += gridDim.x) {
+  int64_t x = blockIdx.x;
+  for (int j = 0;; ++j, x += gridDim.x) {
     // item number x of the call
     while (x - base >= total && gb < p.B) {
       base += total;
@@ -497,15 +503,16 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       incl = cnt;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       total = __shfl_sync(0xffffffffu, incl, 31);
     }
     Item it{};
     if (x - base < total) {
-      const int o = __ffs(__ballot_sync(0xffffffffu, incl > x - base)) - 1;
-      int y = x - base - __shfl_sync(0xffffffffu, incl - cnt, o);
+      const uint32_t at = static_cast<uint32_t>(x - base);
+      const int o = __ffs(__ballot_sync(0xffffffffu, incl > at)) - 1;
+      const int y = static_cast<int>(at - __shfl_sync(0xffffffffu, incl - cnt, o));
       it.s = gb + o;
       it.t0 = __shfl_sync(0xffffffffu, c0, o);
       it.q_s = __shfl_sync(0xffffffffu, q_s, o);

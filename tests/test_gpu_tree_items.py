@@ -60,6 +60,18 @@ def test_values_that_are_not_finite_in_many_items(kv, q, G, D, every):
     b = batch(kv, q, G, D, seed=90 + q)
     for s in range(0, b.B, every):
         poison(b.vc, int(b.slots(s)[b.ctx[s]]), float("nan"), 3 + s % 7)
+    b.reference = lambda r=b.reference(): r  # computed once
     d = compare(b)
     want = np.isnan(b.reference()[0])
     assert want.any() and np.array_equal(torch.isnan(d.out).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,q,Hq,Hkv", [(1024, 8, 32, 8), (512, 32, 32, 8), (512, 4, 64, 4)])
+def test_many_sequences(B, q, Hq, Hkv, kv):
+    """Large batches of small trees: up to 4,096 units."""
+    rng = np.random.default_rng(B)
+    b = Batch([int(c) for c in rng.integers(0, 40, B)], [q] * B, Hq, Hkv, 64, 16, kv, seed=B)
+    b.reference = lambda r=b.reference(): r  # computed once
+    compare(b)
+    compare(b, max_q=0)
