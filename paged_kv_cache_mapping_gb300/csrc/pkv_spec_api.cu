@@ -13,7 +13,7 @@ using namespace pkv;
 
 namespace {
 
-constexpr int kTreeKeyTile = 128;  // chunk bounds are rounded up to key tiles in 32 bits
+constexpr int kTreeKeySlack = 256;  // key numbers, in 32 bits, run up to two tiles past a sequence (the next tile's pages)
 
 pkv_status check_index_vector(const char* name, const pkv_tensor* t, int64_t len) {
   PKV_TRY(check_tensor(name, t, 1));
@@ -311,7 +311,7 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
   PKV_NEED(Hq <= (1 << 16), "Hq beyond 65536");
   PKV_NEED(out->shape[0] == T && out->shape[1] == Hq && out->shape[2] == D, describe("out", out) + " must have q's shape");
   PKV_NEED(out->dtype == PKV_F32 || out->dtype == PKV_BF16, "out must be f32 or bf16");
-  PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX - kTreeKeyTile, "max_blocks * block_size beyond int32");
+  PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX - kTreeKeySlack, "max_blocks * block_size beyond int32");
   PKV_NEED(NB >= 1, "the cache has no blocks");
   if (q->dtype != PKV_F32 && T > (int64_t(1) << 30) / Hq)
     return fail(PKV_ERR_UNSUPPORTED, "T * Hq beyond 2^30 (a sequence's rows and work items are numbered in 32 bits)");

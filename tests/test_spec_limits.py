@@ -9,7 +9,7 @@ from paged_kv_cache_mapping_gb300 import build as pkv_build
 from paged_kv_cache_mapping_gb300 import speculative as spec
 from tests.test_abi import BF16, E4M3, F32, FAKE, I32, _t
 
-SHORT, REFUSED = 3, 2
+SHORT, REFUSED, INVALID = 3, 2, 1
 
 
 @pytest.fixture(scope="module")
@@ -44,3 +44,11 @@ def test_rows_are_numbered_in_32_bits(lib):
     assert attention(lib, 8, 8, 32, 8, 8, T=1 << 25) == SHORT, lib.pkv_last_error()
     assert attention(lib, 8, 8, 32, 8, 8, T=(1 << 25) + 1) == REFUSED
     assert b"2^30" in lib.pkv_last_error()
+
+
+@pytest.mark.parametrize("left,status", [(0, INVALID), (128, INVALID), (129, INVALID), (255, INVALID), (256, SHORT)])
+def test_keys_are_numbered_in_32_bits(lib, left, status):
+    """The kernels look two tiles of 128 keys past a sequence's end: that must not wrap."""
+    last = (2 ** 31 - 1 - left) + 127 + 127  # the largest key number: a tile's last, of a tile that starts within 127
+    assert status == INVALID or last < 2 ** 31
+    assert attention(lib, 1, 8, 32, 8, 8, blocks=2 ** 31 - 1 - left, bs=1) == status, lib.pkv_last_error()
