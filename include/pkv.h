@@ -517,7 +517,8 @@ PKV_API pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_
  *   k_cache,
  *   v_cache        any cache dtype (f32, bf16, e4m3); one layer
  *   new_seq_lens   [B] int32 (written) or NULL: N_s - q_s + L_s; must not
- *                  overlap seq_lens (every layer's call reads the step's)
+ *                  overlap any other argument (every layer's call reads the
+ *                  step's lengths)
  *
  * The row at position N_s - q_s + accepted[s][i] moves to N_s - q_s + i, bit
  * for bit; other rows stay as they are.  A sequence whose lengths, path or

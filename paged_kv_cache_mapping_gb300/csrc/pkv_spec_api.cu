@@ -4,6 +4,8 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <utility>
 
 #include "pkv.h"
 #include "pkv_kernels.h"
@@ -63,9 +65,28 @@ int64_t max_nodes_of(int32_t max_q_len, int64_t T) {
   return max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T;
 }
 
-bool bytes_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+// Whether the address ranges that two tensors span have a byte in common.
+bool spans_overlap(const pkv_tensor* a, const pkv_tensor* b) {
+  auto span = [](const pkv_tensor* t, uintptr_t& lo, uintptr_t& hi) {
+    int64_t first = 0, last = 0;
+    for (int i = 0; i < t->ndim; ++i) {
+      if (t->shape[i] == 0) return false;
+      const int64_t d = (t->shape[i] - 1) * t->stride[i];
+      (d < 0 ? first : last) += d;
+    }
+    lo = reinterpret_cast<uintptr_t>(t->data) + first * esize(t->dtype);
+    hi = reinterpret_cast<uintptr_t>(t->data) + (last + 1) * esize(t->dtype);
+    return true;
+  };
+  uintptr_t al, ah, bl, bh;
+  return span(a, al, ah) && span(b, bl, bh) && al < bh && bl < ah;
+}
+
+// What a call writes must not overlap what its CTAs still read.
+pkv_status check_apart(const char* name, const pkv_tensor* out, std::initializer_list<std::pair<const char*, const pkv_tensor*>> others) {
+  for (const auto& o : others)
+    PKV_NEED(!spans_overlap(out, o.second), std::string(name) + " must not overlap " + o.first);
+  return PKV_OK;
 }
 
 }  // namespace
@@ -247,7 +268,10 @@ pkv_status pkv_tree_commit(const pkv_tensor* accepted, const pkv_tensor* accepte
   PKV_NEED(D % 8 == 0, "commit needs D a multiple of 8");
   if (new_seq_lens != nullptr) {
     PKV_TRY(check_vector_i32("new_seq_lens", new_seq_lens, B));
-    PKV_NEED(!bytes_overlap(new_seq_lens->data, 4 * B, seq_lens->data, 4 * B), "new_seq_lens must not overlap seq_lens");
+    // a sequence's first CTA writes it while the others may still read these
+    PKV_TRY(check_apart("new_seq_lens", new_seq_lens,
+                        {{"seq_lens", seq_lens}, {"accepted", accepted}, {"accepted_lens", accepted_lens},
+                         {"cu_seqlens_q", cu_seqlens_q}, {"block_tables", block_tables}, {"k_cache", k_cache}, {"v_cache", v_cache}}));
   }
   unsigned int* err = nullptr;
   int sms = 0;
