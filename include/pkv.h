@@ -423,7 +423,8 @@ PKV_API pkv_status pkv_rope_init(const pkv_rope_params* params, pkv_rope* rope);
  *
  *   q, q_out      [T, Hq, D], same dtype; unit stride in D, 16-byte aligned
  *                 rows; q_out may be q itself, but must not overlap it
- *                 otherwise
+ *                 otherwise, nor k or v (views of one buffer whose rows
+ *                 interleave do not overlap)
  *   k, v          [T, Hkv, D], q's dtype, as in pkv_append
  *   positions     [T] int32 or int64 (device), any value
  *   slot_mapping, k_cache, v_cache, k_scale, v_scale: as in pkv_append; a

@@ -82,6 +82,32 @@ bool spans_overlap(const pkv_tensor* a, const pkv_tensor* b) {
   return span(a, al, ah) && span(b, bl, bh) && al < bh && bl < ah;
 }
 
+// Whether a row of a [T, H, D] and one of b [U, J, D] (unit stride in D) have a
+// byte in common.  Views of one buffer whose rows interleave (the q, k and v parts
+// of a fused projection) span the same addresses without sharing any: where both
+// have the same strides the rows are compared, difference of heads by difference
+// of heads; views of other strides that span the same addresses count as shared.
+bool rows_overlap(const pkv_tensor* a, const pkv_tensor* b) {
+  if (!spans_overlap(a, b)) return false;
+  const int64_t es = esize(a->dtype), row = a->shape[2] * es;
+  const bool tokens = a->shape[0] > 1 || b->shape[0] > 1, heads = a->shape[1] > 1 || b->shape[1] > 1;
+  auto stride = [&](int i) { return (a->shape[i] > 1 ? a : b)->stride[i]; };  // one row alone has no stride
+  for (int i = 0; i < 2; ++i)
+    if (a->shape[i] > 1 && b->shape[i] > 1 && a->stride[i] != b->stride[i]) return true;
+  const int64_t st = tokens ? stride(0) * es : 0, sh = heads ? stride(1) * es : 0;
+  const int64_t d0 = static_cast<const char*>(b->data) - static_cast<const char*>(a->data);
+  for (int64_t h = -(a->shape[1] - 1); h <= b->shape[1] - 1; ++h) {
+    const int64_t d = d0 + h * sh;  // from a row of a to the row of b h heads on, the same token
+    int64_t t = st == 0 ? 0 : -d / st;
+    for (int64_t u = t - 1; u <= t + 1; ++u) {
+      const int64_t at = std::min(std::max(u, -(a->shape[0] - 1)), b->shape[0] - 1);
+      const int64_t off = d + at * st;
+      if (off < row && -off < row) return true;
+    }
+  }
+  return false;
+}
+
 // What a call writes must not overlap what its CTAs still read.
 pkv_status check_apart(const char* name, const pkv_tensor* out, std::initializer_list<std::pair<const char*, const pkv_tensor*>> others) {
   for (const auto& o : others)
@@ -184,8 +210,10 @@ pkv_status pkv_rope_append(const pkv_tensor* q, const pkv_tensor* k, const pkv_t
   PKV_TRY(check_rows("q_out", q_out));
   PKV_TRY(check_rows("k", k));
   PKV_TRY(check_rows("v", v));
-  PKV_NEED(q->data != q_out->data || T == 0 || (q->stride[0] == q_out->stride[0] && q->stride[1] == q_out->stride[1]),
-           "q_out over q needs q's strides");
+  // rows are rotated by many CTAs: a row of q_out may be the same row of q, but not another one, nor of k or v
+  const bool in_place = q->data == q_out->data && (T <= 1 || q->stride[0] == q_out->stride[0]) && (Hq <= 1 || q->stride[1] == q_out->stride[1]);
+  PKV_NEED(in_place || !rows_overlap(q, q_out), "q_out may be q itself, but must not overlap it otherwise");
+  PKV_NEED(!rows_overlap(k, q_out) && !rows_overlap(v, q_out), "q_out must not overlap k or v");
   if (fp8) PKV_TRY(check_scales(k_scale, v_scale));
   unsigned int* err = nullptr;
   int sms = 0;
