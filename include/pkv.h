@@ -453,6 +453,7 @@ PKV_API pkv_status pkv_rope_append(const pkv_tensor* q, const pkv_tensor* k, con
  *                 and its ancestors
  *   positions     [T] int32 (written): N_s - q_s + the node's depth (0 for a
  *                 child of the context)
+ * The outputs must overlap neither the inputs nor each other.
  *
  * A parent outside -1 .. i - 1 is recorded (bit 4) and taken as -1.  Rows of
  * a sequence with inconsistent lengths or more than 32 W nodes are recorded

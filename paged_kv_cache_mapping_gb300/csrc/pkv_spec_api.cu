@@ -263,6 +263,10 @@ pkv_status pkv_tree_mask(const pkv_tensor* parents, const pkv_tensor* cu_seqlens
   PKV_TRY(check_vector_i32("parents", parents, T));
   PKV_TRY(check_mask("tree_mask", tree_mask, T));
   PKV_TRY(check_vector_i32("positions", positions, T));
+  // sequences are independent CTAs, and nodes read their ancestors' links
+  PKV_TRY(check_apart("tree_mask", tree_mask,
+                      {{"parents", parents}, {"cu_seqlens_q", cu_seqlens_q}, {"seq_lens", seq_lens}, {"positions", positions}}));
+  PKV_TRY(check_apart("positions", positions, {{"parents", parents}, {"cu_seqlens_q", cu_seqlens_q}, {"seq_lens", seq_lens}}));
   unsigned int* err = nullptr;
   int sms = 0;
   PKV_TRY(device_state(&err, &sms));

@@ -112,3 +112,17 @@ def test_rows_overlap_by_brute_force(lib):
         rc = append(lib, q, k, v, o, kc, T, 8)
         assert rc == (INVALID if shared else PASSED), (T, H, J, st, sh, d, lib.pkv_last_error())
     assert min(seen.values()) > 300
+
+
+# ---------------------------------------------------------------- masks
+M0 = FAKE + 0x100000
+
+
+@pytest.mark.parametrize("mask,pos", [(0, None), (-20, None), (None, 0), (None, 20), (None, 0x100000), (None, 0x200004), (0x100008, None),
+                                      (0x200000, None), (0x300000, 0x300000 + 20)])
+def test_outputs_of_a_mask(lib, mask, pos):
+    """Offsets from parents (0), cu_seqlens_q (0x100000) and seq_lens (0x200000), and one output from the other."""
+    a = [_t(M0, I32, [6]), _t(M0 + 0x100000, I32, [3]), _t(M0 + 0x200000, I32, [2]),
+         _t(M0 + (0x400000 if mask is None else mask), I32, [6, 1]), _t(M0 + (0x500000 if pos is None else pos), I32, [6])]
+    assert lib.pkv_tree_mask(*map(ptr, a), None) == INVALID
+    assert b"must not overlap" in lib.pkv_last_error()
