@@ -378,12 +378,15 @@ PKV_API pkv_status pkv_attention_static_workspace(const pkv_tensor* q, const pkv
  *                      1 over the pair indices between those that make fast
  *                      and slow turns (0: 32 and 1) over L positions, their
  *                      bounds rounded outwards; cos and sin are multiplied by
- *                      attention_factor (0: 0.1 ln(factor) + 1)
+ *                      attention_factor (0: 0.1 ln(factor) + 1, and 1 for a
+ *                      factor of at most 1)
  *   PKV_ROPE_SMOOTH    f_i w_i + f_i / factor (1 - w_i), w_i rising from 0 to
  *                      1 as the turns L f_i / (2 pi) go from slow to fast
  *                      (0: 1 and 4)
  * attention_factor applies to every scaling (0: 1 except where noted).
- * rot_dim: even, 2 .. 256; base > 1; factor > 0; L > 0 for the last two.
+ * rot_dim: even, 2 .. 256; base > 1; factor > 0; L > 0, and fast and slow >= 0,
+ * for the last two.  Settings whose base, angles or amplitude leave the numbers
+ * (a factor of 1e-309, say) are refused.
  */
 typedef enum {
   PKV_ROPE_PLAIN = 0,

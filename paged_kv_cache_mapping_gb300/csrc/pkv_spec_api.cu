@@ -1,6 +1,7 @@
 // pkv_spec_api.cu -- C entry points of a speculative decoding step (declared
 // in include/pkv.h): host-side validation and launches of the rotary append,
 // the tree mask, the tree attention and the path commit.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -133,12 +134,14 @@ pkv_status pkv_rope_init(const pkv_rope_params* a, pkv_rope* rope) {
            "original_max_position must be finite and > 0");
   PKV_NEED(a->attention_factor >= 0.0 && isfinite(a->attention_factor), "attention_factor must be finite and >= 0");
   const double pi2 = 6.283185307179586476925286766559;
+  PKV_NEED(!banded || (a->fast >= 0.0 && a->slow >= 0.0), "fast and slow must be >= 0");
   const double fast = a->fast > 0.0 ? a->fast : (a->scaling == PKV_ROPE_SMOOTH ? 4.0 : 32.0);
   const double slow = a->slow > 0.0 ? a->slow : 1.0;
   PKV_NEED(!banded || (isfinite(fast) && isfinite(slow) && fast > slow), "fast must be finite and above slow");
   const double r = a->rot_dim, L = a->original_max_position, f = a->factor;
   double base = a->base;
   if (a->scaling == PKV_ROPE_NTK && a->rot_dim > 2) base *= pow(f, r / (r - 2.0));
+  PKV_NEED(base > 0.0 && isfinite(base), "the scaled base leaves the numbers");
   double lo = 0.0, hi = 0.0;
   if (a->scaling == PKV_ROPE_BY_PARTS) {  // the pair index that makes t turns over L positions, rounded outwards
     auto at = [&](double t) { return r * log(L / (t * pi2)) / (2.0 * log(base)); };
@@ -157,11 +160,13 @@ pkv_status pkv_rope_init(const pkv_rope_params* a, pkv_rope* rope) {
       const double keep = std::min(std::max((L * w / pi2 - slow) / (fast - slow), 0.0), 1.0);
       w = w * keep + w / f * (1.0 - keep);
     }
+    PKV_NEED(isfinite(w), "an angle per position is not finite");
     const double turn = w / pi2;
     out.turns[i] = static_cast<uint64_t>(ldexp(turn - floor(turn), 64));  // a fraction below 1: fits 64 bits
   }
   double amp = a->attention_factor > 0.0 ? a->attention_factor : 1.0;
   if (a->attention_factor == 0.0 && a->scaling == PKV_ROPE_BY_PARTS) amp = f > 1.0 ? 0.1 * log(f) + 1.0 : 1.0;
+  PKV_NEED(amp <= FLT_MAX, "attention_factor beyond fp32");
   out.amplitude = static_cast<float>(amp);
   out.rot_dim = a->rot_dim;
   out.interleaved = a->interleaved != 0;
