@@ -181,6 +181,14 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
   const int64_t t = blockIdx.x;
   const int g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (g == 0) {
+    // inconsistent lengths are recorded, those of sequences without a row of their own too
+    for (int64_t i = t * blockDim.x + threadIdx.x; i < p.B; i += (int64_t)gridDim.x * blockDim.x) {
+      const int a = __ldg(p.cu_q + i), e = __ldg(p.cu_q + i + 1), m = __ldg(p.seq_lens + i);
+      if (a < 0 || e < a || (int64_t)e > p.T || e - a > m || (int64_t)m > (int64_t)p.max_blocks * p.bs || e - a > p.max_nodes)
+        atomicOr(p.err, kErrLengths);
+    }
+  }
   if (t >= __ldg(p.cu_q + p.B)) return;
   const int s = upper_index(p.cu_q, p.B, static_cast<int>(t));
   const int c0 = __ldg(p.cu_q + s);
