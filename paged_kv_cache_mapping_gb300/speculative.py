@@ -108,9 +108,12 @@ def pkv_tree_mask(parents, cu_seqlens_q, seq_lens, max_q_len: int, tree_mask=Non
 
 
 def pkv_tree_attention_workspace_size(q, block_tables, k_cache, max_q_len: int = 0) -> int:
+    max_q_len = int(max_q_len)
+    if max_q_len >= 1 << 31:  # ctypes would take its low 32 bits
+        raise PkvError(1, "max_q_len beyond int32")
     a = [_tensor(q, "q"), _tensor(block_tables, "block_tables"), _tensor(k_cache, "k_cache")]
     n = ctypes.c_size_t(0)
-    _check(_lib().pkv_tree_attention_workspace_size(*(ctypes.addressof(t) for t in a), int(max_q_len), ctypes.byref(n)))
+    _check(_lib().pkv_tree_attention_workspace_size(*(ctypes.addressof(t) for t in a), max(max_q_len, 0), ctypes.byref(n)))
     return int(n.value)
 
 

@@ -4,7 +4,9 @@ is refused.  No GPU."""
 import ctypes
 
 import pytest
+import torch
 
+import paged_kv_cache_mapping_gb300 as pkv
 from paged_kv_cache_mapping_gb300 import build as pkv_build
 from paged_kv_cache_mapping_gb300 import speculative as spec
 from tests.test_abi import BF16, E4M3, F32, FAKE, I32, _t
@@ -52,3 +54,19 @@ def test_keys_are_numbered_in_32_bits(lib, left, status):
     last = (2 ** 31 - 1 - left) + 127 + 127  # the largest key number: a tile's last, of a tile that starts within 127
     assert status == INVALID or last < 2 ** 31
     assert attention(lib, 1, 8, 32, 8, 8, blocks=2 ** 31 - 1 - left, bs=1) == status, lib.pkv_last_error()
+
+
+def test_bounds_of_nodes_beyond_32_bits_are_refused(lib):
+    i = torch.zeros(1, dtype=torch.int32)
+    for n in (2 ** 31, 2 ** 32 + 8):
+        with pytest.raises(pkv.PkvError, match="max_q_len beyond int32"):
+            pkv.pkv_tree_attention_workspace_size(i, i, i, n)
+
+
+@pytest.mark.gpu
+def test_the_workspace_follows_the_bound_of_nodes():
+    q = torch.zeros((64, 8, 128), dtype=torch.bfloat16, device="cuda")
+    bt = torch.zeros((4, 400), dtype=torch.int32, device="cuda")
+    kc = torch.zeros((1, 16, 2, 128), dtype=torch.bfloat16, device="cuda")
+    size = lambda n: pkv.pkv_tree_attention_workspace_size(q, bt, kc, n)  # noqa: E731
+    assert 0 < size(1) < size(8) <= size(64) == size(0) == size(-2 ** 40) == size(2 ** 31 - 1)
