@@ -45,8 +45,8 @@ inline int esize(pkv_dtype d) {
 
 inline std::string describe(const char* name, const pkv_tensor* t) {
   std::string s = std::string(name) + " (" + dtype_name(t->dtype) + ", shape [";
-  for (int i = 0; i < t->ndim; ++i) s += (i ? ", " : "") + std::to_string(t->shape[i]);
-  return s + "])";
+  for (int i = 0; i < t->ndim && i < 4; ++i) s += (i ? ", " : "") + std::to_string(t->shape[i]);
+  return s + (t->ndim > 4 ? ", ..])" : "])");
 }
 
 inline pkv_status need(bool ok, const std::string& msg) {

@@ -56,6 +56,14 @@ def test_keys_are_numbered_in_32_bits(lib, left, status):
     assert attention(lib, 1, 8, 32, 8, 8, blocks=2 ** 31 - 1 - left, bs=1) == status, lib.pkv_last_error()
 
 
+def test_a_tensor_of_too_many_dimensions_is_described_by_the_four_it_holds(lib):
+    a = [_t(FAKE, I32, [6]), _t(FAKE, I32, [3]), _t(FAKE, I32, [2]), _t(FAKE, I32, [6, 1]), _t(FAKE, I32, [6])]
+    for ndim in (5, 1000, 2 ** 31 - 1):
+        a[0].ndim = ndim
+        assert lib.pkv_tree_mask(*map(ctypes.addressof, a), None) == INVALID
+        assert lib.pkv_last_error() == b"parents (i32, shape [6, 0, 0, 0, ..]): expected 1 dimensions"
+
+
 def test_bounds_of_nodes_beyond_32_bits_are_refused(lib):
     i = torch.zeros(1, dtype=torch.int32)
     for n in (2 ** 31, 2 ** 32 + 8):
