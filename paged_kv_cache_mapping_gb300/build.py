@@ -8,6 +8,7 @@ module that marshals PyTorch tensors for the calls made once per layer of a
 speculative step.  Run ``python -m paged_kv_cache_mapping_gb300.build``.
 """
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,6 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
 BINDING_SRC = os.path.join(CSRC, "pkv_binding.cpp")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for.txt")  # what the binding was built against
 SOURCES = ["pkv_api.cu", "pkv_append.cu", "pkv_plan.cu", "pkv_decode.cu", "pkv_prefill.cu", "pkv_f32.cu", "pkv_static_ws.cu", "pkv_prefill_tc.cu", "pkv_blocks.cu",
            "pkv_spec_api.cu", "pkv_rope.cu", "pkv_tree.cu", "pkv_tree_tc.cu", "pkv_tree_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -48,6 +50,20 @@ def binding_command(out: str):
             f"-Wl,-rpath,{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
+def binding_target() -> str:
+    """The Python and PyTorch that a binding links against (PyTorch is not imported for this)."""
+    torch = importlib.util.find_spec("torch").origin
+    with open(os.path.join(os.path.dirname(torch), "version.py")) as f:
+        return "\n".join([sys.version, torch, f.read()])
+
+
+def _binding_stale() -> bool:
+    if _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pkv.h"), __file__]) or not os.path.exists(BINDING_FOR):
+        return True
+    with open(BINDING_FOR) as f:
+        return f.read() != binding_target()
+
+
 def _stale(out, deps):
     if not os.path.exists(out):
         return True
@@ -58,7 +74,7 @@ def _stale(out, deps):
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(ROOT, "include", "pkv.h"))
+    headers += [os.path.join(ROOT, "include", f) for f in ("pkv.h", "pkv_blocks.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
@@ -70,24 +86,27 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
     bind_tmp = BINDING + f".tmp{os.getpid()}"
-    new_binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pkv.h"), __file__])
+    new_binding = force or _binding_stale()
     if new_binding:
         jobs.append(binding_command(bind_tmp))
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
-    failed = False
     for cmd, r in zip(jobs, results):
         if verbose or r.returncode != 0 or ptxas_info:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-        failed |= r.returncode != 0
-    if failed:
-        raise RuntimeError("the compiler failed")
-    if new_binding:
-        os.replace(bind_tmp, BINDING)
+    bound = not new_binding or results.pop().returncode == 0
+    if any(r.returncode != 0 for r in results):
+        raise RuntimeError("nvcc failed")
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)
+    if not bound:  # the library does not need it
+        raise RuntimeError("the binding's compiler failed (libpkv.so is built)")
+    if new_binding:
+        os.replace(bind_tmp, BINDING)
+        with open(BINDING_FOR, "w") as f:
+            f.write(binding_target())
     return LIB
 
 
