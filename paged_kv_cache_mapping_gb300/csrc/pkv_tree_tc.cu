@@ -38,11 +38,11 @@
 // score that was seen, still weigh something.  (P as two e4m3 codes saved
 // the widening and lost what lay 15.5 powers of two below the reference: behind
 // one leading key the mass of thousands of small ones went missing, several per
-// cent of an output.  The widening costs: 8 trees of 16 nodes over 32K to 128K
-// keys 341 us instead of 291, 64 trees of 4 / 8 / 16 nodes times 4 heads over
-// 4,096 to 16,384 (16 nodes: 512 to 4,096) keys 277 / 329 / 148 instead of 266 /
-// 283 / 137.  With the V codes' loads behind the wait for S, one after the other
-// between conversions, it was 361.)
+// cent of an output.  With the widening, 8 trees of 16 nodes over 32K to 128K
+// keys take 324 us instead of 296, 64 trees of 4 / 8 / 16 nodes times 4 heads over
+// 4,096 to 16,384 (16 nodes: 512 to 4,096) keys 277 / 327 / 147 instead of 268 /
+// 285 / 137.  With the V codes' loads behind the wait for S, one after the other
+// between conversions, the first took 20 us more.)
 //
 // More than 64 rows (bf16 caches) go to pkv_tree_wide.cu, whose tiles of 128 rows
 // put the rows on the M side: up to 64 rows this kernel is the faster one (64
@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
   fence_after();
   const uint32_t tmem = *tslot;
   grid_dep_wait();
-  launch_dependents();
+  // No launch_dependents(): the join starts when the last CTAs end.  With its grid
+  // pending from here on, the 32K to 128K key case took 385 us in a loop of calls
+  // and 343 from a graph, instead of 324; 64 trees of 4 / 8 / 16 nodes, e4m3, 270 /
+  // 334 / 146 instead of 263 / 315 / 141; of 8 nodes, bf16, 108.0 and 108.2.
 
   if (warp == 0 || warp == 3) {
     copy_tiles<G_>(a, cta, warp == 3, warp == 3 ? sV : sK, warp == 3 ? &tm_v : &tm_k);
@@ -799,8 +802,8 @@ __global__ void __launch_bounds__(Geo<D, N, F8>::kThreads, 1)
 template <int D, typename OutT>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, const float* part_o, const float* part_lse,
                                                         int rows_per_seq, Chunking chunking) {
-  // what does not come from the kernel before is read while that still runs (it
-  // lets this one start only after its own predecessors have ended)
+  // what does not come from the kernel before is read while its last CTAs still
+  // run (they end after that kernel's own predecessors have)
   constexpr int E = D / 32, kAt = 4;  // chunks in flight (eight: 1 % slower in all)
   const int s = blockIdx.x, lane = threadIdx.x & 31;
   const int c0 = __ldg(p.cu_q + s), c1 = __ldg(p.cu_q + s + 1), n = __ldg(p.seq_lens + s);
