@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, cons
 static int tree_tile_rows(int64_t rows, bool f8) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || f8 ? 64 : 128; }
 static Chunking call_chunking(int64_t B, int64_t Hkv, int64_t rows, bool f8) {
   const int64_t N = tree_tile_rows(rows, f8);
-  return tree_chunking(B * Hkv * ((rows + N - 1) / N), (int)N);
+  return tree_chunking(B * Hkv * ((rows + N - 1) / N));
 }
 
 int64_t tree_tc_rows_per_seq(int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_ctx, bool f8) {

@@ -24,20 +24,29 @@ constexpr int kInfoSlots = 8;
 // an item's start and end.  A sequence is cut into equal chunks of at most
 // `least` keys, but into no more than `most`, and no more than
 // kTreePartRows / q_s, so that it has at most that many partial rows per head.
-// Measured, us: `least` 256 / 512 / 1024 / 2048 with 8 units of 2,048 keys 11.6 /
-// 11.8 / 13.9 / 16.6; 138 wide units of up to 3,001 keys 36 / 38 / 37 / 44; 256
-// wide ones of up to 8,192 135 / 131 / 117 / 113; 512 narrow ones of up to 4,096
-// 118 / 116 / 111 / 110.  `most` with 64 units of 32K to 131K keys: 16 303, 19
-// (8 items per SM) 288, 24 319, 48 337.
+// Measured, us, `least` 256 / 512 / 1024 / 2048 / 4096, 8 KV heads of 4 query heads,
+// D 128, contexts uniform up to the number given:
+//   units  8: 8 nodes, 2,100 keys  12.0 / 12.7 / 14.7 / 20.2 / 30
+//         16: 4 nodes,  8,192      18.3 / 17.9 / 16.0 / 19.8 / 31; 8 nodes, 4,096  14.9 / 13.3 / 15.0 / 20.7 / 31
+//         64: 8 nodes,  4,096      24.7 / 22.6 / 25.3 / 25.8 / 37; 64 nodes (wide tiles), 8,192  55 / 56 / 49 / 53 / 54
+//        128: 16 nodes, 16,384, e4m3  134 / 134 / 128 / 118 / 124; 64 nodes, 8,192  73 / 70 / 63 / 71 / 80
+//        192: 8 nodes,  4,096      56 / 51 / 49 / 60 / 64; 64 nodes, 8,192  104 / 98 / 88 / 93 / 91
+//        240, 256: 64 nodes, 8,192  128 / 122 / 112 / 112 / 118 and 140 / 133 / 124 / 114 / 132
+//        256: 8 nodes,  4,096      66 / 65 / 61 / 63 / 67; 16 nodes, 8,192  140 / 130 / 125 / 120 / 122
+//        512: 8 nodes,  4,096      123 / 120 / 113 / 114 / 113; 64 nodes, 8,192  267 / 257 / 240 / 219 / 231
+// `most` with 64 units of 32K to 131K keys: 16 303, 19 (8 items per SM) 288, 24 319,
+// 48 337.  (The SMs are counted here, not asked for: a workspace's size is known
+// without a device.)
 constexpr int kTreeMaxChunks = 64;
 constexpr int kTreePartRows = 1024;
+constexpr int kTreeItems = 8 * 152;
 struct Chunking {
   int32_t least, most;
 };
-inline Chunking tree_chunking(int64_t units, int rows) {
+inline Chunking tree_chunking(int64_t units) {
   Chunking c;
-  c.least = rows == 128 && units >= 256 ? 2048 : units >= 512 ? 1024 : units >= 128 ? 512 : 256;
-  const int64_t m = 1216 / (units < 1 ? 1 : units);  // 8 items per SM
+  c.least = units >= 256 ? 2048 : units >= 16 ? 1024 : 256;
+  const int64_t m = kTreeItems / (units < 1 ? 1 : units);
   c.most = static_cast<int32_t>(m < 8 ? 8 : m > kTreeMaxChunks ? kTreeMaxChunks : m);
   return c;
 }
