@@ -56,6 +56,9 @@
  * still running, and waits for that kernel to complete, with its writes
  * visible, before it reads or writes any memory.  Inputs written by the
  * previous kernel of the stream, the lengths included, are therefore safe.
+ * (Within pkv_tree_attention the kernel that joins a long sequence's chunks
+ * reads the lengths before it waits: the kernel before it, of the same call,
+ * does not change them and has waited for whatever wrote them.)
  *
  * The library keeps, per device, the addresses of its own device variables
  * (the error word, the static workspace), looked up at the first call on
@@ -434,9 +437,12 @@ PKV_API pkv_status pkv_rope_init(const pkv_rope_params* params, pkv_rope* rope);
  *                 row with a negative slot is rotated into q_out and not
  *                 written to the cache
  *
- * Angles are exact for every position: position * turns is taken modulo one
- * turn in 64-bit integers.  The rotation is computed in fp32 and rounded
- * once, to q's type and to the cache's type (an e4m3 code is that of
+ * position * turns is taken modulo one turn in 64-bit integers, which is exact
+ * for every position.  The turns hold the frequency as worked out in fp64, so
+ * the angle is off by a few position * f_i * 2^-53 (some 2^-31 radians at
+ * position 2^20), and by 2^-24 of a half turn where sine and cosine are taken.
+ * The rotation is computed in fp32 and rounded once, to q's type and to the
+ * cache's type (an e4m3 code is that of
  * (rotated k) * (1.0f / k_scale), not of a bf16 intermediate).
  * Supported: pkv_append's dtypes; D a multiple of 8 up to 256, rot_dim <= D.
  */

@@ -20,6 +20,14 @@
  * comparing the block's token ids, so two different prefixes never share a
  * block even if their hashes collide.
  *
+ * Tokens appended here stay: there is no call that gives rows back, and blocks
+ * are registered in the prefix cache as soon as they are full.  Drafted tokens
+ * (pkv_tree_attention) therefore do not belong in pkv_bm_append or
+ * pkv_bm_build_step: rejected ones would keep counting in the sequence's length,
+ * and blocks that drafted rows filled would be found by later prompts under
+ * tokens whose rows pkv_tree_commit has moved.  A server that speculates keeps the
+ * tables and lengths of its drafted rows itself.
+ *
  * The manager is plain host memory and host code: it never touches the GPU.
  * Its outputs (slot mapping, block tables, lengths) are the inputs of
  * pkv_append and pkv_attention.  A manager is not thread-safe: one thread (or

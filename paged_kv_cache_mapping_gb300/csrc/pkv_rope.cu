@@ -5,9 +5,11 @@
 // angle position * f_i:  (a cos - b sin, a sin + b cos).  Angles are kept as
 // fractions of a turn in 64-bit fixed point: turns_i = f_i / (2 pi) * 2^64
 // mod 2^64, and the low 64 bits of position * turns_i are the angle modulo
-// one turn, exactly, for any integer position; the upper 32 of them, as a
-// signed number, lie in [-1/2, 1/2) turn with an error of 2^-33 turn, so
-// sincospif never sees a large argument and no fp64 is needed.  The rotation
+// one turn, exactly, for any integer position (f_i itself has the 53 bits that the
+// host worked it out in: a position p turns it by an error of about p 2^-53 f_i);
+// the upper 32 of them, as a signed number, lie in [-1/2, 1/2) turn with an error
+// of 2^-33 turn, and 24 of them enter sincospif, which never sees a large argument
+// and needs no fp64.  The rotation
 // itself is fp32, rounded once to the destination's type.
 //
 // Bound: memory.  Each row of q, k and v is read once and written once; a

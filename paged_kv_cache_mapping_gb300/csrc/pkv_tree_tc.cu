@@ -39,23 +39,24 @@
 // the widening and lost what lay 15.5 powers of two below the reference: behind
 // one leading key the mass of thousands of small ones went missing, several per
 // cent of an output.  With the widening, 8 trees of 16 nodes over 32K to 128K
-// keys take 324 us instead of 296, 64 trees of 4 / 8 / 16 nodes times 4 heads over
-// 4,096 to 16,384 (16 nodes: 512 to 4,096) keys 277 / 327 / 147 instead of 268 /
-// 285 / 137.  With the V codes' loads behind the wait for S, one after the other
+// keys take 324 us instead of 296, and 64 trees of 4 / 8 / 16 nodes times 4 heads
+// over 4,096 to 16,384 (16 nodes: 512 to 4,096) keys, cut alike, 277 / 327 / 147
+// instead of 268 / 285 / 137.  With the V codes' loads behind the wait for S, one after the other
 // between conversions, the first took 20 us more.)
 //
 // More than 64 rows (bf16 caches) go to pkv_tree_wide.cu, whose tiles of 128 rows
 // put the rows on the M side: up to 64 rows this kernel is the faster one (64
-// trees of 8 / 12 / 16 nodes times 4 heads over 512 to 4,096 keys: 110 / 128 / 133
+// trees of 8 / 12 / 16 nodes times 4 heads over 512 to 4,096 keys: 109 / 129 / 132
 // us here, 126 / 131 / 135 there), above it the other (16 trees of 64 nodes over
-// up to 8,192 keys: 192 and 150 us when it was new, 110 now).
+// up to 8,192 keys: 192 and 150 us when it was new, 109 now).
 //
 // Bound: the memory while there are few rows, then the softmax: with a key per
-// lane each warp runs about 290 instructions for 32 keys and 16 rows.
-// Measured, with the join: 64 trees of 8 nodes over 512 to 4,096 keys, bf16: 108
+// lane each warp runs about 290 instructions for 32 keys and 16 rows; with e4m3
+// caches also the widening, which waits for V's codes and shares the issue slots.
+// Measured, with the join: 64 trees of 8 nodes over 512 to 4,096 keys, bf16: 109
 // us (5.5 TB/s of 600 MB, 81 % of a plain copy's rate); 8 trees of 16 nodes over
-// 32K to 128K keys, e4m3: 289 us (4.3 TB/s of 1,240 MB); one tree of 8 nodes over
-// 2,048 keys: 10.7 us.
+// 32K to 128K keys, e4m3: 324 us (3.8 TB/s of 1,240 MB); one tree of 8 nodes over
+// 2,048 keys: 11.1 us.
 //
 // CTA: 16 warps, 24 for N = 64.
 //   warps 0, 3  copy the K and the V tiles of 128 keys by TMA: boxes of 16, 8 or

@@ -20,10 +20,10 @@
 // cost 4,900 clocks.)  S is read twice, for the largest score and for P, since
 // 128 scores do not fit a thread's registers beside the rest.
 //
-// Not kept: clusters of two CTAs that share K and V tiles by TMA multicast.  They
-// took 107 us for the 16 trees below instead of 110, and gave up more wherever
-// the row tiles are odd (65 nodes instead of 64: 139 us instead of 107) or uneven
-// (29 instead of 26 us for the 23 trees).
+// Not kept: shared K and V tiles in a CTA pair.  They took 107 us for the 16 trees
+// below instead of 110, and gave up more wherever the row tiles are odd (65 nodes
+// instead of 64: 139 us instead of 107) or uneven (29 instead of 26 us for the 23
+// trees, at the time).
 //
 // Bound: the K and V tiles, of which each row tile reads all (64 KB for 12.6
 // MFLOP), then the tensor cores (55 % active; a tile takes them about 1,540 clocks
@@ -34,8 +34,8 @@
 // item's start, but the halves of P V, whose descriptors want to be constants,
 // stand twice (124 us in a loop, 116 so, at the time).
 // Measured, with the join: 16 trees of 64 nodes times 4 heads (256 rows) over
-// 1,024 to 8,192 keys, D 128: 110 us (73 GFLOP of visible pairs, 0.67 PFLOP/s);
-// 23 uneven trees of up to 37 nodes times 5 heads, D 64, pages of 12 slots: 26 us.
+// 1,024 to 8,192 keys, D 128: 109 us (73 GFLOP of visible pairs, 0.67 PFLOP/s);
+// 23 uneven trees of up to 37 nodes times 5 heads, D 64, pages of 12 slots: 28 us.
 //
 // CTA: 16 warps: K, MMA, items and query rows, V, 2 x 4 of softmax, 4 that write.
 #include "pkv_tree_tc.cuh"
