@@ -544,11 +544,101 @@ PKV_API pkv_status pkv_tree_commit(const pkv_tensor* accepted, const pkv_tensor*
                                    pkv_tensor* new_seq_lens, void* stream);
 
 /*
+ * Requests that grow, shrink and share prompts.  A server may keep its block
+ * tables, lengths and list of free blocks on the device and let the step's
+ * tables, slots and positions follow from the lengths there, with no copy to
+ * the host and nothing that a captured graph could not replay:
+ *
+ *   pkv_step_tables      lengths -> tables, rows, slots and positions
+ *   pkv_shared_prefixes  tables  -> which requests share a prefix
+ */
+
+/*
+ * pkv_step_tables -- block tables and slots of a step, from the requests'
+ * lengths before and after it.
+ *
+ *   seq_lens       [B] int32: a_s, tokens of request s before the step
+ *   new_seq_lens   [B] int32: b_s, after it.  b_s > a_s: q_s = b_s - a_s rows
+ *                  come (a prompt, a decode, drafted tokens); b_s < a_s: its
+ *                  last tokens go (rejected drafts, or 0: the request is
+ *                  done) and q_s = 0
+ *   shared_blocks  [B] int32 or NULL: leading entries of a table that belong
+ *                  to others too (a cached prefix); they are never given back.
+ *                  New rows must lie behind them: a request that grows has
+ *                  a_s >= shared_blocks * block_size
+ *   block_size     tokens per block, >= 1
+ *   block_tables   [B, max_blocks] int32, unit column stride (read and
+ *                  written): a request that grows gets its new blocks at
+ *                  entries ceil(a_s / block_size) .. ceil(b_s / block_size) - 1;
+ *                  every other entry stays as it is, those behind a request
+ *                  that shrinks too
+ *   free_blocks    [F] int32 (read and written): free block ids, the first
+ *                  free_count of them; a stack whose last entry goes first
+ *   free_count     [1] int32
+ *   new_free_count [1] int32 (written): may be free_count itself
+ *   cu_seqlens_q   [B+1] int32 (written): exclusive sums of q_s
+ *   slot_mapping   [T] int32 or int64 (written): slots of the new rows
+ *   positions      [T] int32 (written) or NULL: their positions a_s + i
+ *
+ * Blocks given back (request by request, in table order) join the stack
+ * before blocks are taken (in the same order) from its end, so what one request
+ * gives back another may have at once.  Rows T' .. T - 1 behind the
+ * last new row get slot -1 and position 0.  The lengths, the shared counts and
+ * the free list's contents are the caller's to keep consistent; block ids are
+ * not checked here but by the calls that use them (a negative one gives slot -1
+ * and is recorded, bit 2).
+ *
+ * All or nothing: when the blocks do not suffice (recorded, bit 32), the new
+ * rows pass T, or free_count or the list's length do not hold what it should
+ * (bit 4), no table and no list entry is written, new_free_count is free_count,
+ * cu_seqlens_q is all zeros and every slot -1, so that the step has no rows.
+ * A request whose own numbers are inconsistent (a negative length, a length
+ * beyond its table, rows among its shared blocks) is recorded (bit 4) and takes
+ * no part: no rows, no blocks.
+ *
+ * At most 8,192 requests.  What is written must not overlap what is read, but
+ * for new_free_count over free_count.
+ */
+PKV_API pkv_status pkv_step_tables(const pkv_tensor* seq_lens, const pkv_tensor* new_seq_lens,
+                                   const pkv_tensor* shared_blocks, int32_t block_size, pkv_tensor* block_tables,
+                                   pkv_tensor* free_blocks, const pkv_tensor* free_count, pkv_tensor* new_free_count,
+                                   pkv_tensor* cu_seqlens_q, pkv_tensor* slot_mapping, pkv_tensor* positions,
+                                   void* stream);
+
+/*
+ * pkv_shared_prefixes -- which neighbouring requests of a step share the first
+ * blocks of their tables ("How Easy Is It to Start Serving LLMs?", "1.
+ * Block-sparse KV memory": requests that share a prompt list the same pages).
+ *
+ *   cu_seqlens_q  [B+1] int32, seq_lens [B] int32 (N_s, new rows included)
+ *   block_tables  [B, max_blocks] int32, unit column stride
+ *   block_size    tokens per block, >= 1
+ *   min_tokens    the shortest prefix worth sharing, >= 1
+ *   groups        [B, 3] int32, contiguous (written): for each request the
+ *                 first request of its group, the request behind its last, and
+ *                 the tokens of the prefix that all of them share (0 for a
+ *                 request alone)
+ *
+ * c_s is the number of leading entries that the tables of requests s - 1 and s
+ * have in common, over the blocks that both have full of context (N_s - q_s
+ * tokens); a negative entry is common to nobody.  Request s joins the one before
+ * it when c_s * block_size >= min_tokens and 2 c_s >= c_(s-1) and c_(s+1): a
+ * group is a run of such requests, its prefix the least c_s of them, so a long
+ * prefix is not cut to less than half for one more request.  Requests that
+ * share have to be neighbours in the batch.  A request with inconsistent lengths
+ * is recorded (bit 4) and shares nothing.  At most 8,192 requests.
+ */
+PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens,
+                                       const pkv_tensor* block_tables, int32_t block_size, int32_t min_tokens,
+                                       pkv_tensor* groups, void* stream);
+
+/*
  * pkv_device_errors -- synchronise the stream, then return (in *flags) and
  * clear the record of out-of-range indices the kernels met on the current
  * device since the last call.  Bits: 1 = slot beyond the pool, 2 = block id
  * out of range, 4 = inconsistent lengths, 8 = a bounded wait gave up, 16 =
- * an attention run found no plan for its shapes in the workspace.
+ * an attention run found no plan for its shapes in the workspace, 32 = a step
+ * needs more blocks than are free.
  */
 PKV_API pkv_status pkv_device_errors(void* stream, uint32_t* flags);
 

@@ -38,7 +38,7 @@ import torch
 __all__ = ["PkvError", "pkv_slot_mapping", "pkv_csr_to_block_tables", "pkv_append", "pkv_attention", "pkv_attention_workspace_size",
            "pkv_attention_plan", "pkv_attention_run", "pkv_attention_static_workspace", "pkv_device_errors",
            "pkv_rope_init", "pkv_rope_append", "pkv_tree_mask", "pkv_tree_attention_workspace_size", "pkv_tree_attention",
-           "pkv_tree_commit", "pkv_version", "library_path", "load_library",
+           "pkv_tree_commit", "pkv_step_tables", "pkv_shared_prefixes", "pkv_version", "library_path", "load_library",
            "EXPORTED", "STATIC_WORKSPACE_BYTES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -49,7 +49,7 @@ EXPORTED = ("pkv_slot_mapping", "pkv_append", "pkv_attention_workspace_size", "p
             "pkv_version", "pkv_csr_to_block_tables", "pkv_bm_create", "pkv_bm_destroy", "pkv_bm_add_sequence", "pkv_bm_append",
             "pkv_bm_free_sequence", "pkv_bm_block_table", "pkv_bm_build_step", "pkv_bm_stats",
             "pkv_rope_init", "pkv_rope_append", "pkv_tree_mask", "pkv_tree_attention_workspace_size",
-            "pkv_tree_attention", "pkv_tree_commit")
+            "pkv_tree_attention", "pkv_tree_commit", "pkv_step_tables", "pkv_shared_prefixes")
 # PKV_STATIC_WORKSPACE_BYTES of include/pkv.h
 STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -280,7 +280,7 @@ def pkv_attention_static_workspace(q, cu_seqlens_q, seq_lens, block_tables, k_ca
 def pkv_device_errors(device=None) -> int:
     """Synchronises the current stream and returns (and clears) the device
     error bits: 1 slot range, 2 block id range, 4 lengths, 8 wait timeout,
-    16 a run without a matching plan."""
+    16 a run without a matching plan, 32 out of free blocks."""
     lib = load_library()
     flags = ctypes.c_uint32(0)
     _check(lib.pkv_device_errors(_stream(device), ctypes.byref(flags)))
@@ -289,3 +289,4 @@ def pkv_device_errors(device=None) -> int:
 
 from .speculative import (Rope, pkv_rope_append, pkv_rope_init, pkv_tree_attention,  # noqa: E402,F401
                           pkv_tree_attention_workspace_size, pkv_tree_commit, pkv_tree_mask)
+from .sharing import pkv_shared_prefixes, pkv_step_tables  # noqa: E402,F401

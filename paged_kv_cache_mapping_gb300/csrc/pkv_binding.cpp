@@ -1,5 +1,6 @@
 // pkv_binding.cpp -- the Python side of the calls that a speculative decoding
-// step makes once per layer (paged_kv_cache_mapping_gb300/speculative.py).
+// step makes once per layer (paged_kv_cache_mapping_gb300/speculative.py), and of
+// those of a step whose requests share prompts (sharing.py).
 //
 // It only marshals: tensors into pkv_tensor descriptors, the tensors' device
 // made current, its current stream, and the C ABI's status back.  Those kernels
@@ -25,6 +26,8 @@ decltype(&pkv_rope_append) f_rope_append;
 decltype(&pkv_tree_mask) f_tree_mask;
 decltype(&pkv_tree_attention) f_tree_attention;
 decltype(&pkv_tree_commit) f_tree_commit;
+decltype(&pkv_step_tables) f_step_tables;
+decltype(&pkv_shared_prefixes) f_shared_prefixes;
 
 bool refuse(int status, const std::string& what) {
   if (g_error == nullptr) {
@@ -38,7 +41,7 @@ bool refuse(int status, const std::string& what) {
 
 // Descriptors of a call's tensors, all on one CUDA device.
 struct Tensors {
-  pkv_tensor t[8];
+  pkv_tensor t[11];
   int n = 0;
   int dev = -1;
   const char* first = "";
@@ -77,6 +80,15 @@ struct Tensors {
     return true;
   }
 };
+
+// an integer argument that the C ABI takes in 32 bits
+bool whole(PyObject* o, const char* name, int32_t& x) {
+  const long long v = PyLong_AsLongLong(o);
+  if (PyErr_Occurred()) return false;
+  if (v > INT32_MAX) return refuse(PKV_ERR_INVALID_ARGUMENT, std::string(name) + " beyond int32");
+  x = static_cast<int32_t>(v < 0 ? 0 : v);
+  return true;
+}
 
 struct WithoutLock {
   PyThreadState* const state = PyEval_SaveThread();
@@ -130,11 +142,12 @@ bool real(PyObject* o, float& x) {
   return PyErr_Occurred() == nullptr;
 }
 
-// bind(PkvError, rope_append, tree_mask, tree_attention, tree_commit): addresses as integers
+// bind(PkvError, rope_append, tree_mask, tree_attention, tree_commit, step_tables, shared_prefixes): addresses as integers
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  if (!want(n, 5)) return nullptr;
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  constexpr int kCalls = 6;
+  if (!want(n, 1 + kCalls)) return nullptr;
+  void* p[kCalls];
+  for (int i = 0; i < kCalls; ++i) {
     p[i] = PyLong_AsVoidPtr(a[1 + i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -144,6 +157,8 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   f_tree_mask = reinterpret_cast<decltype(f_tree_mask)>(p[1]);
   f_tree_attention = reinterpret_cast<decltype(f_tree_attention)>(p[2]);
   f_tree_commit = reinterpret_cast<decltype(f_tree_commit)>(p[3]);
+  f_step_tables = reinterpret_cast<decltype(f_step_tables)>(p[4]);
+  f_shared_prefixes = reinterpret_cast<decltype(f_shared_prefixes)>(p[5]);
   Py_RETURN_NONE;
 }
 
@@ -233,9 +248,46 @@ PyObject* tree_commit(PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// step_tables(seq_lens, new_seq_lens, shared_blocks or None, block_size, block_tables, free_blocks, free_count,
+//             new_free_count, cu_seqlens_q, slot_mapping, positions or None)
+PyObject* step_tables(PyObject* const* a, Py_ssize_t n) {
+  if (!want(n, 11)) return nullptr;
+  Tensors t;
+  int32_t bs;
+  if (!t.add(a[0], "seq_lens") || !t.add(a[1], "new_seq_lens") || !t.add(a[4], "block_tables") || !t.add(a[5], "free_blocks") ||
+      !t.add(a[6], "free_count") || !t.add(a[7], "new_free_count") || !t.add(a[8], "cu_seqlens_q") || !t.add(a[9], "slot_mapping") ||
+      !whole(a[3], "block_size", bs))
+    return nullptr;
+  const pkv_tensor* shared = nullptr;
+  pkv_tensor* positions = nullptr;
+  if (a[2] != Py_None) {
+    if (!t.add(a[2], "shared_blocks")) return nullptr;
+    shared = &t.t[t.n - 1];
+  }
+  if (a[10] != Py_None) {
+    if (!t.add(a[10], "positions")) return nullptr;
+    positions = &t.t[t.n - 1];
+  }
+  return run(t.dev, [&](cudaStream_t st) {
+    return f_step_tables(&t.t[0], &t.t[1], shared, bs, &t.t[2], &t.t[3], &t.t[4], &t.t[5], &t.t[6], &t.t[7], positions, st);
+  });
+}
+
+// shared_prefixes(cu_seqlens_q, seq_lens, block_tables, block_size, min_tokens, groups)
+PyObject* shared_prefixes(PyObject* const* a, Py_ssize_t n) {
+  if (!want(n, 6)) return nullptr;
+  Tensors t;
+  int32_t bs, least;
+  if (!t.add(a[0], "cu_seqlens_q") || !t.add(a[1], "seq_lens") || !t.add(a[2], "block_tables") || !t.add(a[5], "groups") ||
+      !whole(a[3], "block_size", bs) || !whole(a[4], "min_tokens", least))
+    return nullptr;
+  return run(t.dev, [&](cudaStream_t st) { return f_shared_prefixes(&t.t[0], &t.t[1], &t.t[2], bs, least, &t.t[3], st); });
+}
+
 #define PKV_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(method<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PKV_METHOD(bind),           PKV_METHOD(rope_append), PKV_METHOD(tree_mask),
-                         PKV_METHOD(tree_attention), PKV_METHOD(tree_commit), {nullptr, nullptr, 0, nullptr}};
+                         PKV_METHOD(tree_attention), PKV_METHOD(tree_commit), PKV_METHOD(step_tables),
+                         PKV_METHOD(shared_prefixes), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

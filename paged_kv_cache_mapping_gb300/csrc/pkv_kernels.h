@@ -138,6 +138,41 @@ int64_t tree_tc_rows_per_seq(int64_t B, int64_t Hkv, int64_t G, int64_t max_q, i
 cudaError_t launch_tree_tc(const TreeParams& p, bool f8, int out_kind, int64_t max_q, int64_t max_ctx, void* workspace,
                            int num_sms, cudaStream_t st);
 
+// ---------------------------------------------------------------- requests that grow, shrink and share prompts
+constexpr int kMaxRequests = 8192;  // of one call: their sums are held in shared memory
+
+struct StepTablesParams {
+  const int32_t* seq_lens;
+  const int32_t* new_seq_lens;
+  const int32_t* shared_blocks;  // may be NULL: none
+  int32_t bs;
+  FastDiv by_bs;
+  int32_t* bt;
+  int64_t bt_stride;
+  int32_t max_blocks, B;
+  int32_t* free_blocks;
+  int64_t F;  // entries of the free list
+  const int32_t* free_count;
+  int32_t* new_free_count;
+  int32_t* cu_q;
+  void* slots;         // int32 or int64 [T]
+  int32_t* positions;  // may be NULL
+  int64_t T;
+  unsigned int* err;
+};
+cudaError_t launch_step_tables(const StepTablesParams& p, bool slots_i64, cudaStream_t st);
+
+struct PrefixParams {
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const int32_t* bt;
+  int64_t bt_stride;
+  int32_t max_blocks, B, bs, min_tokens;
+  int32_t* groups;  // [B, 3]
+  unsigned int* err;
+};
+cudaError_t launch_shared_prefixes(const PrefixParams& p, cudaStream_t st);
+
 // ---------------------------------------------------------------- attention
 // Device workspace of one attention call (all offsets 256-byte aligned).
 // One decode unit: a logical chunk of one sequence (all KV heads share it).

@@ -1,0 +1,104 @@
+// pkv_share_api.cu -- C entry points for requests that grow, shrink and share
+// prompts (declared in include/pkv.h): host-side validation and launches of the
+// step's tables and the shared prefixes.
+#include <algorithm>
+
+#include "pkv.h"
+#include "pkv_kernels.h"
+#include "pkv_validate.h"
+
+using namespace pkv;
+
+extern "C" {
+
+pkv_status pkv_step_tables(const pkv_tensor* seq_lens, const pkv_tensor* new_seq_lens, const pkv_tensor* shared_blocks,
+                           int32_t block_size, pkv_tensor* block_tables, pkv_tensor* free_blocks,
+                           const pkv_tensor* free_count, pkv_tensor* new_free_count, pkv_tensor* cu_seqlens_q,
+                           pkv_tensor* slot_mapping, pkv_tensor* positions, void* stream) {
+  int64_t B;
+  PKV_TRY(check_step(cu_seqlens_q, seq_lens, B));
+  PKV_TRY(check_vector_i32("new_seq_lens", new_seq_lens, B));
+  if (shared_blocks != nullptr) PKV_TRY(check_vector_i32("shared_blocks", shared_blocks, B));
+  PKV_TRY(check_block_tables(block_tables, B));
+  PKV_NEED(block_size >= 1, "block_size must be >= 1");
+  PKV_NEED(block_tables->shape[1] <= INT32_MAX / block_size, "max_blocks * block_size beyond int32");
+  PKV_TRY(check_tensor("free_blocks", free_blocks, 1));
+  PKV_TRY(check_vector_i32("free_blocks", free_blocks, free_blocks->shape[0]));
+  PKV_NEED(free_blocks->shape[0] < INT32_MAX, "free_blocks beyond int32");
+  PKV_TRY(check_vector_i32("free_count", free_count, 1));
+  PKV_TRY(check_vector_i32("new_free_count", new_free_count, 1));
+  PKV_TRY(check_tensor("slot_mapping", slot_mapping, 1));
+  const int64_t T = slot_mapping->shape[0];
+  PKV_NEED(T < INT32_MAX, "T beyond int32");
+  PKV_TRY(check_index_vector("slot_mapping", slot_mapping, T));
+  if (positions != nullptr) PKV_TRY(check_vector_i32("positions", positions, T));
+  // CTAs are still reading while others write; only the count is read by all before it is written
+  const pkv_tensor none{};
+  const std::pair<const char*, pkv_tensor*> outs[] = {{"block_tables", block_tables}, {"free_blocks", free_blocks}, {"cu_seqlens_q", cu_seqlens_q},
+                                                     {"slot_mapping", slot_mapping},  {"positions", positions},     {"new_free_count", new_free_count}};
+  for (size_t i = 0; i < sizeof(outs) / sizeof(outs[0]); ++i) {
+    if (outs[i].second == nullptr) continue;
+    PKV_TRY(check_apart(outs[i].first, outs[i].second,
+                        {{"seq_lens", seq_lens}, {"new_seq_lens", new_seq_lens}, {"shared_blocks", shared_blocks != nullptr ? shared_blocks : &none}}));
+    if (outs[i].second != new_free_count) PKV_TRY(check_apart(outs[i].first, outs[i].second, {{"free_count", free_count}}));
+    for (size_t j = 0; j < i; ++j)
+      if (outs[j].second != nullptr) PKV_TRY(check_apart(outs[i].first, outs[i].second, {outs[j]}));
+  }
+  if (B > kMaxRequests) return fail(PKV_ERR_UNSUPPORTED, "more than " + std::to_string(kMaxRequests) + " requests");
+  StepTablesParams p{};
+  int sms = 0;
+  PKV_TRY(device_state(&p.err, &sms));
+  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  p.new_seq_lens = static_cast<const int32_t*>(new_seq_lens->data);
+  p.shared_blocks = shared_blocks != nullptr ? static_cast<const int32_t*>(shared_blocks->data) : nullptr;
+  p.bs = block_size;
+  p.by_bs = fast_div(static_cast<uint32_t>(block_size));
+  p.bt = static_cast<int32_t*>(block_tables->data);
+  p.bt_stride = block_tables->stride[0];
+  p.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  p.B = static_cast<int32_t>(B);
+  p.free_blocks = static_cast<int32_t*>(free_blocks->data);
+  p.F = free_blocks->shape[0];
+  p.free_count = static_cast<const int32_t*>(free_count->data);
+  p.new_free_count = static_cast<int32_t*>(new_free_count->data);
+  p.cu_q = static_cast<int32_t*>(cu_seqlens_q->data);
+  p.slots = slot_mapping->data;
+  p.positions = positions != nullptr ? static_cast<int32_t*>(positions->data) : nullptr;
+  p.T = T;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_step_tables(p, slot_mapping->dtype == PKV_I64, st);
+  if (e != cudaSuccess) return cuda_fail(e, "step tables launch");
+  return finish(st, "pkv_step_tables");
+}
+
+pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens, const pkv_tensor* block_tables,
+                               int32_t block_size, int32_t min_tokens, pkv_tensor* groups, void* stream) {
+  int64_t B;
+  PKV_TRY(check_step(cu_seqlens_q, seq_lens, B));
+  PKV_TRY(check_block_tables(block_tables, B));
+  PKV_NEED(block_size >= 1, "block_size must be >= 1");
+  PKV_NEED(block_tables->shape[1] <= INT32_MAX / block_size, "max_blocks * block_size beyond int32");
+  PKV_NEED(min_tokens >= 1, "min_tokens must be >= 1");
+  PKV_TRY(check_groups(groups, B));
+  PKV_TRY(check_apart("groups", groups, {{"cu_seqlens_q", cu_seqlens_q}, {"seq_lens", seq_lens}, {"block_tables", block_tables}}));
+  if (B > kMaxRequests) return fail(PKV_ERR_UNSUPPORTED, "more than " + std::to_string(kMaxRequests) + " requests");
+  PrefixParams p{};
+  int sms = 0;
+  PKV_TRY(device_state(&p.err, &sms));
+  if (B == 0) return PKV_OK;
+  p.cu_q = static_cast<const int32_t*>(cu_seqlens_q->data);
+  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  p.bt = static_cast<const int32_t*>(block_tables->data);
+  p.bt_stride = block_tables->stride[0];
+  p.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  p.B = static_cast<int32_t>(B);
+  p.bs = block_size;
+  p.min_tokens = min_tokens;
+  p.groups = static_cast<int32_t*>(groups->data);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_shared_prefixes(p, st);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefixes launch");
+  return finish(st, "pkv_shared_prefixes");
+}
+
+}  // extern "C"

@@ -16,41 +16,6 @@ using namespace pkv;
 
 namespace {
 
-constexpr int kTreeKeySlack = 256;  // key numbers, in 32 bits, run up to two tiles past a sequence (the next tile's pages)
-
-pkv_status check_index_vector(const char* name, const pkv_tensor* t, int64_t len) {
-  PKV_TRY(check_tensor(name, t, 1));
-  PKV_NEED(t->dtype == PKV_I32 || t->dtype == PKV_I64, describe(name, t) + ": must be i32 or i64");
-  PKV_NEED(t->shape[0] == len, describe(name, t) + ": expected length " + std::to_string(len));
-  PKV_NEED(len <= 1 || t->stride[0] == 1, describe(name, t) + ": must be contiguous");
-  return PKV_OK;
-}
-
-// [T, H, D] rows: unit stride in D, 16-byte aligned
-pkv_status check_rows(const char* name, const pkv_tensor* t) {
-  const int es = esize(t->dtype);
-  PKV_NEED(t->stride[2] == 1 || t->shape[2] == 1, std::string(name) + " must have unit stride in D");
-  PKV_NEED(aligned(t->data, 16) && (t->stride[0] * es) % 16 == 0 && (t->stride[1] * es) % 16 == 0,
-           std::string(name) + " rows must be 16-byte aligned (data and strides)");
-  return PKV_OK;
-}
-
-pkv_status check_scales(float k_scale, float v_scale) {
-  PKV_NEED(k_scale > 0.f && v_scale > 0.f && isfinite(k_scale) && isfinite(v_scale),
-           "fp8 scales must be positive and finite");
-  return PKV_OK;
-}
-
-// Lengths, counts and tables of a step: B sequences.
-pkv_status check_step(const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens, int64_t& B) {
-  PKV_TRY(check_tensor("seq_lens", seq_lens, 1));
-  B = seq_lens->shape[0];
-  PKV_NEED(B <= (1 << 24), "B beyond 2^24 sequences");
-  PKV_TRY(check_vector_i32("seq_lens", seq_lens, B));
-  PKV_TRY(check_vector_i32("cu_seqlens_q", cu_seqlens_q, B + 1));
-  return PKV_OK;
-}
-
 pkv_status check_mask(const char* name, const pkv_tensor* m, int64_t T) {
   PKV_TRY(check_tensor(name, m, 2));
   PKV_NEED(m->dtype == PKV_I32, describe(name, m) + ": must be i32");
@@ -59,28 +24,6 @@ pkv_status check_mask(const char* name, const pkv_tensor* m, int64_t T) {
   PKV_NEED(m->shape[1] <= 1 || m->stride[1] == 1, std::string(name) + ": column stride must be 1");
   PKV_NEED(m->shape[0] <= 1 || m->stride[0] >= m->shape[1], std::string(name) + ": rows overlap");
   return PKV_OK;
-}
-
-// nodes a sequence may have: the caller's bound, else every row
-int64_t max_nodes_of(int32_t max_q_len, int64_t T) {
-  return max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T;
-}
-
-// Whether the address ranges that two tensors span have a byte in common.
-bool spans_overlap(const pkv_tensor* a, const pkv_tensor* b) {
-  auto span = [](const pkv_tensor* t, uintptr_t& lo, uintptr_t& hi) {
-    int64_t first = 0, last = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-      if (t->shape[i] == 0) return false;
-      const int64_t d = (t->shape[i] - 1) * t->stride[i];
-      (d < 0 ? first : last) += d;
-    }
-    lo = reinterpret_cast<uintptr_t>(t->data) + first * esize(t->dtype);
-    hi = reinterpret_cast<uintptr_t>(t->data) + (last + 1) * esize(t->dtype);
-    return true;
-  };
-  uintptr_t al, ah, bl, bh;
-  return span(a, al, ah) && span(b, bl, bh) && al < bh && bl < ah;
 }
 
 // Whether a row of a [T, H, D] and one of b [U, J, D] (unit stride in D) have a
@@ -107,13 +50,6 @@ bool rows_overlap(const pkv_tensor* a, const pkv_tensor* b) {
     }
   }
   return false;
-}
-
-// What a call writes must not overlap what its CTAs still read.
-pkv_status check_apart(const char* name, const pkv_tensor* out, std::initializer_list<std::pair<const char*, const pkv_tensor*>> others) {
-  for (const auto& o : others)
-    PKV_NEED(!spans_overlap(out, o.second), std::string(name) + " must not overlap " + o.first);
-  return PKV_OK;
 }
 
 }  // namespace

@@ -3,7 +3,8 @@ append, tree mask, tree attention and path commit.
 
 Like the rest of the binding it only marshals arguments.  The calls that a
 step makes once per layer, whose kernels take a few microseconds, go through
-the compiled module csrc/pkv_binding.cpp; the others through ctypes.
+the compiled module csrc/pkv_binding.cpp; the others through ctypes.  sharing.py
+takes both from here.
 """
 import ctypes
 import importlib.machinery
@@ -46,7 +47,9 @@ def _lib():
                            ("pkv_tree_mask", [p] * 6),
                            ("pkv_tree_attention_workspace_size", [p, p, p, i, ctypes.POINTER(z)]),
                            ("pkv_tree_attention", [p] * 7 + [f, f, f, i, p, p, z, p]),
-                           ("pkv_tree_commit", [p] * 9)):
+                           ("pkv_tree_commit", [p] * 9),
+                           ("pkv_step_tables", [p] * 3 + [i] + [p] * 8),
+                           ("pkv_shared_prefixes", [p] * 3 + [i, i, p, p])):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, ctypes.c_int
         _ready = lib
@@ -65,7 +68,8 @@ def _binding():
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
         loader.exec_module(m)
         at = lambda fn: ctypes.cast(fn, ctypes.c_void_p).value  # noqa: E731
-        m.bind(PkvError, at(lib.pkv_rope_append), at(lib.pkv_tree_mask), at(lib.pkv_tree_attention), at(lib.pkv_tree_commit))
+        m.bind(PkvError, *(at(getattr(lib, "pkv_" + name)) for name in (
+            "rope_append", "tree_mask", "tree_attention", "tree_commit", "step_tables", "shared_prefixes")))
         _calls = m
     return _calls
 
