@@ -551,6 +551,9 @@ PKV_API pkv_status pkv_tree_commit(const pkv_tensor* accepted, const pkv_tensor*
  *
  *   pkv_step_tables      lengths -> tables, rows, slots and positions
  *   pkv_shared_prefixes  tables  -> which requests share a prefix
+ *   per layer:
+ *     pkv_append or pkv_rope_append, then
+ *     pkv_shared_attention: the step's attention, each shared prefix read once
  */
 
 /*
@@ -631,6 +634,57 @@ PKV_API pkv_status pkv_step_tables(const pkv_tensor* seq_lens, const pkv_tensor*
 PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens,
                                        const pkv_tensor* block_tables, int32_t block_size, int32_t min_tokens,
                                        pkv_tensor* groups, void* stream);
+
+/*
+ * pkv_shared_attention -- pkv_attention for requests that share prefixes: the
+ * blocks of a shared prefix are read once for the rows of all the requests that
+ * share it, and joined with each request's own keys.
+ *
+ * Arguments, layouts and results as pkv_attention (causal, q_s new rows of a
+ * request at its end), and
+ *
+ *   groups         [B, 3] int32, contiguous, as pkv_shared_prefixes writes it or
+ *                  the caller knows it: first request, request behind the last,
+ *                  and tokens of the prefix, the same three numbers for every
+ *                  request of a group.  A request with prefix 0 is alone, and
+ *                  its other two numbers are not read
+ *   max_q_len      a host-side upper bound on q_s (<= 0: unknown)
+ *   max_group_len  a host-side upper bound on the new rows of a group's requests
+ *                  together (<= 0: unknown); like max_q_len it chooses the tiles
+ *   workspace      pkv_shared_attention_workspace_size() bytes, 256-byte aligned;
+ *                  scratch of one call: nothing in it is kept between calls
+ *
+ * Groups must not overlap, and the tables of a group must agree in the entries of
+ * the prefix: it is read through its first request's table, whose own lengths do
+ * not matter.  A prefix is whole blocks, and context of every request of the group
+ * (prefix <= N_s - q_s).  A request that breaks this, or whose first request's
+ * numbers differ from its own, or with more than max_q_len rows in itself or
+ * max_group_len in its group, or with inconsistent lengths, is recorded (bit 4)
+ * and its rows are left as they are; so are rows at or beyond cu_seqlens_q[B].  A
+ * key whose block id is out of range is recorded (bit 2) and adds nothing; a row
+ * that sees no key gets zeros.
+ *
+ * Values of keys that a row does not see never reach it (an infinity in a row of V
+ * that every row of a request sees may reach them as NaN).  Precision as
+ * pkv_tree_attention.  A row's result depends on its own request, its group's
+ * prefix and on the call's shapes (T, B, Hq, Hkv, max_q_len, max_group_len,
+ * max_blocks * block_size: they choose how a long axis is split), not on block
+ * size, placement or the other requests.
+ *
+ * Supported: as pkv_tree_attention (bf16 q with bf16 or e4m3 caches at D = 64 and
+ * 128; f32 q with f32 caches at D a multiple of 32 up to 256, where each request
+ * reads its own table).
+ */
+PKV_API pkv_status pkv_shared_attention_workspace_size(const pkv_tensor* q, const pkv_tensor* block_tables,
+                                                       const pkv_tensor* k_cache, int32_t max_q_len,
+                                                       int32_t max_group_len, size_t* bytes);
+
+PKV_API pkv_status pkv_shared_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_q,
+                                        const pkv_tensor* seq_lens, const pkv_tensor* block_tables,
+                                        const pkv_tensor* groups, const pkv_tensor* k_cache,
+                                        const pkv_tensor* v_cache, float scale, float k_scale, float v_scale,
+                                        int32_t max_q_len, int32_t max_group_len, pkv_tensor* out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /*
  * pkv_device_errors -- synchronise the stream, then return (in *flags) and

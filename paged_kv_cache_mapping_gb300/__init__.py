@@ -29,6 +29,13 @@ and, from .speculative (a speculative decoding step):
                      scale, out, k_scale=1.0, v_scale=1.0, max_q_len=0, workspace=None)
   pkv_tree_commit(accepted, accepted_lens, cu_seqlens_q, seq_lens, block_tables,
                   k_cache, v_cache, new_seq_lens=None)
+and, from .sharing (requests that grow, shrink and share prompts):
+  pkv_step_tables(seq_lens, new_seq_lens, block_tables, block_size, free_blocks, free_count, cu_seqlens_q,
+                  slot_mapping, shared_blocks=None, positions=None, new_free_count=None)
+  pkv_shared_prefixes(cu_seqlens_q, seq_lens, block_tables, block_size, min_tokens=256, groups=None)
+  pkv_shared_attention_workspace_size(q, block_tables, k_cache, max_q_len=0, max_group_len=0)
+  pkv_shared_attention(q, cu_seqlens_q, seq_lens, block_tables, groups, k_cache, v_cache, scale, out,
+                       k_scale=1.0, v_scale=1.0, max_q_len=0, max_group_len=0, workspace=None)
 """
 import ctypes
 import os
@@ -38,7 +45,8 @@ import torch
 __all__ = ["PkvError", "pkv_slot_mapping", "pkv_csr_to_block_tables", "pkv_append", "pkv_attention", "pkv_attention_workspace_size",
            "pkv_attention_plan", "pkv_attention_run", "pkv_attention_static_workspace", "pkv_device_errors",
            "pkv_rope_init", "pkv_rope_append", "pkv_tree_mask", "pkv_tree_attention_workspace_size", "pkv_tree_attention",
-           "pkv_tree_commit", "pkv_step_tables", "pkv_shared_prefixes", "pkv_version", "library_path", "load_library",
+           "pkv_tree_commit", "pkv_step_tables", "pkv_shared_prefixes",
+           "pkv_shared_attention_workspace_size", "pkv_shared_attention", "pkv_version", "library_path", "load_library",
            "EXPORTED", "STATIC_WORKSPACE_BYTES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -49,7 +57,8 @@ EXPORTED = ("pkv_slot_mapping", "pkv_append", "pkv_attention_workspace_size", "p
             "pkv_version", "pkv_csr_to_block_tables", "pkv_bm_create", "pkv_bm_destroy", "pkv_bm_add_sequence", "pkv_bm_append",
             "pkv_bm_free_sequence", "pkv_bm_block_table", "pkv_bm_build_step", "pkv_bm_stats",
             "pkv_rope_init", "pkv_rope_append", "pkv_tree_mask", "pkv_tree_attention_workspace_size",
-            "pkv_tree_attention", "pkv_tree_commit", "pkv_step_tables", "pkv_shared_prefixes")
+            "pkv_tree_attention", "pkv_tree_commit", "pkv_step_tables", "pkv_shared_prefixes",
+            "pkv_shared_attention_workspace_size", "pkv_shared_attention")
 # PKV_STATIC_WORKSPACE_BYTES of include/pkv.h
 STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -289,4 +298,5 @@ def pkv_device_errors(device=None) -> int:
 
 from .speculative import (Rope, pkv_rope_append, pkv_rope_init, pkv_tree_attention,  # noqa: E402,F401
                           pkv_tree_attention_workspace_size, pkv_tree_commit, pkv_tree_mask)
-from .sharing import pkv_shared_prefixes, pkv_step_tables  # noqa: E402,F401
+from .sharing import (pkv_shared_attention, pkv_shared_attention_workspace_size, pkv_shared_prefixes,  # noqa: E402,F401
+                      pkv_step_tables)

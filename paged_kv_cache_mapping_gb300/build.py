@@ -24,7 +24,7 @@ BINDING_SRC = os.path.join(CSRC, "pkv_binding.cpp")
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_FOR = os.path.join(BUILD, "binding_for.txt")  # what the binding was built against
 SOURCES = ["pkv_api.cu", "pkv_append.cu", "pkv_plan.cu", "pkv_decode.cu", "pkv_prefill.cu", "pkv_f32.cu", "pkv_static_ws.cu", "pkv_prefill_tc.cu", "pkv_blocks.cu",
-           "pkv_spec_api.cu", "pkv_share_api.cu", "pkv_tables.cu", "pkv_rope.cu", "pkv_tree.cu", "pkv_tree_tc.cu", "pkv_tree_wide.cu"]
+           "pkv_spec_api.cu", "pkv_share_api.cu", "pkv_tables.cu", "pkv_share_tc.cu", "pkv_share_wide.cu", "pkv_rope.cu", "pkv_tree.cu", "pkv_tree_tc.cu", "pkv_tree_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}"]

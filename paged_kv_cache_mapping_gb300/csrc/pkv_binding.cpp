@@ -28,6 +28,7 @@ decltype(&pkv_tree_attention) f_tree_attention;
 decltype(&pkv_tree_commit) f_tree_commit;
 decltype(&pkv_step_tables) f_step_tables;
 decltype(&pkv_shared_prefixes) f_shared_prefixes;
+decltype(&pkv_shared_attention) f_shared_attention;
 
 bool refuse(int status, const std::string& what) {
   if (g_error == nullptr) {
@@ -142,9 +143,10 @@ bool real(PyObject* o, float& x) {
   return PyErr_Occurred() == nullptr;
 }
 
-// bind(PkvError, rope_append, tree_mask, tree_attention, tree_commit, step_tables, shared_prefixes): addresses as integers
+// bind(PkvError, rope_append, tree_mask, tree_attention, tree_commit, step_tables, shared_prefixes,
+//      shared_attention): addresses as integers
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  constexpr int kCalls = 6;
+  constexpr int kCalls = 7;
   if (!want(n, 1 + kCalls)) return nullptr;
   void* p[kCalls];
   for (int i = 0; i < kCalls; ++i) {
@@ -159,6 +161,7 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   f_tree_commit = reinterpret_cast<decltype(f_tree_commit)>(p[3]);
   f_step_tables = reinterpret_cast<decltype(f_step_tables)>(p[4]);
   f_shared_prefixes = reinterpret_cast<decltype(f_shared_prefixes)>(p[5]);
+  f_shared_attention = reinterpret_cast<decltype(f_shared_attention)>(p[6]);
   Py_RETURN_NONE;
 }
 
@@ -205,6 +208,20 @@ PyObject* tree_mask(PyObject* const* a, Py_ssize_t n) {
   return rc.o != nullptr ? Py_BuildValue("(OOO)", rc.o, mask.o, positions.o) : nullptr;
 }
 
+// a call's scratch; NULL when it is none
+const at::Tensor* workspace(PyObject* o, int dev) {
+  if (!THPVariable_Check(o)) {
+    PyErr_SetString(PyExc_TypeError, "workspace must be a torch.Tensor");
+    return nullptr;
+  }
+  const at::Tensor& ws = THPVariable_Unpack(o);
+  if (!ws.is_cuda() || ws.device().index() != dev || !ws.is_contiguous()) {
+    refuse(PKV_ERR_INVALID_ARGUMENT, "workspace must be contiguous, on cuda:" + std::to_string(dev));
+    return nullptr;
+  }
+  return &ws;
+}
+
 // tree_attention(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, tree_mask, scale, k_scale, v_scale, max_q_len,
 //                out, workspace)
 PyObject* tree_attention(PyObject* const* a, Py_ssize_t n) {
@@ -215,24 +232,13 @@ PyObject* tree_attention(PyObject* const* a, Py_ssize_t n) {
       !t.add(a[4], "k_cache") || !t.add(a[5], "v_cache") || !t.add(a[6], "tree_mask") || !t.add(a[11], "out") ||
       !real(a[7], scale) || !real(a[8], ks) || !real(a[9], vs))
     return nullptr;
-  const long long max_q = PyLong_AsLongLong(a[10]);
-  if (PyErr_Occurred()) return nullptr;
-  if (max_q > INT32_MAX) {
-    refuse(PKV_ERR_INVALID_ARGUMENT, "max_q_len beyond int32");
-    return nullptr;
-  }
-  if (!THPVariable_Check(a[12])) {
-    PyErr_SetString(PyExc_TypeError, "workspace must be a torch.Tensor");
-    return nullptr;
-  }
-  const at::Tensor& ws = THPVariable_Unpack(a[12]);
-  if (!ws.is_cuda() || ws.device().index() != t.dev || !ws.is_contiguous()) {
-    refuse(PKV_ERR_INVALID_ARGUMENT, "workspace must be contiguous, on cuda:" + std::to_string(t.dev));
-    return nullptr;
-  }
+  int32_t max_q;
+  if (!whole(a[10], "max_q_len", max_q)) return nullptr;
+  const at::Tensor* ws = workspace(a[12], t.dev);
+  if (ws == nullptr) return nullptr;
   return run(t.dev, [&](cudaStream_t st) {
     return f_tree_attention(&t.t[0], &t.t[1], &t.t[2], &t.t[3], &t.t[4], &t.t[5], &t.t[6], scale, ks, vs,
-                            static_cast<int32_t>(max_q < 0 ? 0 : max_q), &t.t[7], ws.data_ptr(), ws.nbytes(), st);
+                            max_q, &t.t[7], ws->data_ptr(), ws->nbytes(), st);
   });
 }
 
@@ -284,10 +290,29 @@ PyObject* shared_prefixes(PyObject* const* a, Py_ssize_t n) {
   return run(t.dev, [&](cudaStream_t st) { return f_shared_prefixes(&t.t[0], &t.t[1], &t.t[2], bs, least, &t.t[3], st); });
 }
 
+// shared_attention(q, cu_seqlens_q, seq_lens, block_tables, groups, k_cache, v_cache, scale, k_scale, v_scale, max_q_len,
+//                  max_group_len, out, workspace)
+PyObject* shared_attention(PyObject* const* a, Py_ssize_t n) {
+  if (!want(n, 14)) return nullptr;
+  Tensors t;
+  float scale, ks, vs;
+  int32_t max_q, max_group;
+  if (!t.add(a[0], "q") || !t.add(a[1], "cu_seqlens_q") || !t.add(a[2], "seq_lens") || !t.add(a[3], "block_tables") ||
+      !t.add(a[4], "groups") || !t.add(a[5], "k_cache") || !t.add(a[6], "v_cache") || !t.add(a[12], "out") || !real(a[7], scale) ||
+      !real(a[8], ks) || !real(a[9], vs) || !whole(a[10], "max_q_len", max_q) || !whole(a[11], "max_group_len", max_group))
+    return nullptr;
+  const at::Tensor* ws = workspace(a[13], t.dev);
+  if (ws == nullptr) return nullptr;
+  return run(t.dev, [&](cudaStream_t st) {
+    return f_shared_attention(&t.t[0], &t.t[1], &t.t[2], &t.t[3], &t.t[4], &t.t[5], &t.t[6], scale, ks, vs, max_q, max_group,
+                              &t.t[7], ws->data_ptr(), ws->nbytes(), st);
+  });
+}
+
 #define PKV_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(method<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PKV_METHOD(bind),           PKV_METHOD(rope_append), PKV_METHOD(tree_mask),
                          PKV_METHOD(tree_attention), PKV_METHOD(tree_commit), PKV_METHOD(step_tables),
-                         PKV_METHOD(shared_prefixes), {nullptr, nullptr, 0, nullptr}};
+                         PKV_METHOD(shared_prefixes), PKV_METHOD(shared_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

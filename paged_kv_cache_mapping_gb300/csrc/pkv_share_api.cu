@@ -1,6 +1,6 @@
 // pkv_share_api.cu -- C entry points for requests that grow, shrink and share
 // prompts (declared in include/pkv.h): host-side validation and launches of the
-// step's tables and the shared prefixes.
+// step's tables, the shared prefixes and the attention that uses them.
 #include <algorithm>
 
 #include "pkv.h"
@@ -99,6 +99,46 @@ pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv_tensor*
   const cudaError_t e = launch_shared_prefixes(p, st);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefixes launch");
   return finish(st, "pkv_shared_prefixes");
+}
+
+pkv_status pkv_shared_attention_workspace_size(const pkv_tensor* q, const pkv_tensor* block_tables, const pkv_tensor* k_cache,
+                                               int32_t max_q_len, int32_t max_group_len, size_t* bytes) {
+  PKV_TRY(check_tensor("q", q, 3));
+  PKV_TRY(check_tensor("block_tables", block_tables, 2));
+  PKV_TRY(check_tensor("k_cache", k_cache, 4));
+  PKV_NEED(bytes != nullptr, "bytes is NULL");
+  *bytes = 0;
+  const int64_t T = q->shape[0], B = block_tables->shape[0], Hkv = k_cache->shape[2], G = Hkv > 0 ? q->shape[1] / Hkv : 1;
+  if (k_cache->dtype == PKV_F32 || T == 0 || B == 0) return PKV_OK;
+  const int64_t rows = shared_rows(T, B, Hkv, G, max_nodes_of(max_q_len, T), max_nodes_of(max_group_len, T),
+                                   block_tables->shape[1] * k_cache->shape[1], k_cache->dtype == PKV_FP8_E4M3);
+  *bytes = align_up(sizeof(float) * rows * q->shape[1] * (q->shape[2] + 1), 256);
+  return PKV_OK;
+}
+
+pkv_status pkv_shared_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens,
+                                const pkv_tensor* block_tables, const pkv_tensor* groups, const pkv_tensor* k_cache,
+                                const pkv_tensor* v_cache, float scale, float k_scale, float v_scale, int32_t max_q_len,
+                                int32_t max_group_len, pkv_tensor* out, void* workspace, size_t workspace_bytes, void* stream) {
+  TreeParams p{};
+  int kv;
+  PKV_TRY(check_paged_rows(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, scale, k_scale, v_scale, out, p, kv));
+  PKV_TRY(check_groups(groups, p.B));
+  size_t ws_need = 0;
+  PKV_TRY(pkv_shared_attention_workspace_size(q, block_tables, k_cache, max_q_len, max_group_len, &ws_need));
+  PKV_TRY(check_workspace(workspace, workspace_bytes, ws_need));
+  const int64_t max_q = max_nodes_of(max_q_len, p.T), max_group = max_nodes_of(max_group_len, p.T);
+  p.max_nodes = static_cast<int32_t>(max_q);
+  int sms = 0;
+  PKV_TRY(device_state(&p.err, &sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.T == 0 || p.B == 0) return PKV_OK;
+  const int out_kind = out->dtype == PKV_BF16;
+  const int32_t* g = static_cast<const int32_t*>(groups->data);
+  const cudaError_t e = kv == 0 ? launch_shared_f32(p, g, max_group, out_kind, st)
+                                : launch_shared_tc(p, g, kv == 2, out_kind, max_q, max_group, block_tables->shape[1] * p.bs, workspace, sms, st);
+  if (e != cudaSuccess) return cuda_fail(e, "shared attention launch");
+  return finish(st, "pkv_shared_attention");
 }
 
 }  // extern "C"

@@ -1,0 +1,182 @@
+// pkv_share_tc.cu -- attention of requests that share prefixes over the paged
+// cache, on the fifth-generation tensor cores.
+//
+// What it computes: causal attention of every request over its own table, where
+// the first tokens of neighbouring requests lie in the same blocks.  With p the
+// group's prefix, row r of a request has
+//     o_r = sum_c 2^(lse_c - M) o_c / sum_c 2^(lse_c - M)
+// over chunks c of the keys 0 .. p - 1 and of the keys p .. of its own, each with
+// its normalised output o_c and its log2-sum-exp2 lse_c.  The prefix's chunks take
+// the rows of all the group's requests as one block of rows that see every key, so
+// a prefix tile is read once for 16 to 128 rows (tiles of pkv_tree_narrow.cuh and
+// pkv_tree_wide.cuh) instead of once for each request; the own keys are those
+// kernels' chunks with a causal bound for a mask.
+//
+// Three launches: the prefixes, the own keys beside them (their CTAs take the SMs as
+// the prefixes' leave them, see begin_phase()), and a join.
+#include "pkv_tree_narrow.cuh"
+
+namespace pkv {
+namespace {
+
+// A prefix is cut so that the rows, in tiles for each KV head, give every SM work,
+// and into no more chunks than leave kPrePartRows partial rows per head in all.
+constexpr int kPrePartRows = 4096;
+struct Cut {
+  int n_pre, n_own;  // rows per MMA tile
+  Chunking pre, own;
+  int64_t pre_chunks, rows_per_seq;
+};
+Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
+  Cut c;
+  c.n_pre = tree_tile_rows(max_group * G, f8);
+  c.n_own = tree_tile_rows(max_q * G, f8);
+  c.own = call_chunking(B, Hkv, max_q * G, f8);
+  c.pre = tree_chunking(Hkv * ((T * G + c.n_pre - 1) / c.n_pre));
+  c.pre.most = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(c.pre.most, kPrePartRows / std::max<int64_t>(T, 1))));
+  auto chunks = [&](const Chunking& k) { return std::max<int64_t>(1, std::min<int64_t>(k.most, (max_ctx + k.least - 1) / k.least)); };
+  c.pre_chunks = chunks(c.pre);
+  c.rows_per_seq = chunks(c.own) > 1 ? std::min<int64_t>(max_q * chunks(c.own), kTreePartRows) : 0;
+  return c;
+}
+
+// One warp per (row, query head), as in tree_join_kernel: lane l holds elements l
+// D / 32 .., four chunks' loads in flight; lane c of the weights holds those of
+// chunks c, c + 32, .. (the prefix's, then the request's own).
+template <int D, typename OutT>
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ TcArgs a) {
+  constexpr int E = D / 32, kAt = 4, kW = 2 * kTreeMaxChunks / 32;
+  const TreeParams& p = a.p;
+  const SharedArgs& h = a.shared;
+  const int s = blockIdx.x, lane = threadIdx.x & 31;
+  // what does not come from the kernels before is read while they still run
+  int c0, q, n, prefix;
+  const bool bad = shared_request(p, h, s, c0, q, n, prefix) || q == 0;
+  int np = 0, own = 1;
+  if (!bad) {
+    if (prefix > 0) np = (prefix - 1) / tree_chunk(prefix, 1, h.pre) + 1;
+    own = (n - prefix - 1) / tree_chunk(n - prefix, q, a.chunking) + 1;
+  }
+  grid_dep_wait();
+  launch_dependents();
+  const int nc = np + own;
+  if (bad || nc == 1) return;
+  const int64_t rows = (int64_t)q * p.Hq;
+  for (int64_t r = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.y * 8) {
+    const int i = static_cast<int>(r / p.Hq), hq = static_cast<int>(r - (int64_t)i * p.Hq);
+    const int64_t pre_at = (int64_t)(c0 + i) * h.pre_chunks;
+    const int64_t own_at = own == 1 ? shared_single(p.T, h.pre_chunks, c0 + i)
+                                    : shared_own(p.T, h.pre_chunks, a.rows_per_seq, s) + (int64_t)i * own;
+    auto row_of = [&](int c) { return ((c < np ? pre_at + c : own_at + (c - np)) * p.Hq + hq); };
+    float v[kAt][E];
+    auto load = [&](int b) {
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) {
+        if (b + k < nc) {
+          const float* q = a.part_o + row_of(b + k) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(q));
+            v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(q));
+            v[k][0] = f.x, v[k][1] = f.y;
+          }
+        }
+      }
+    };
+    float w[kW], M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kW; ++k) w[k] = lane + 32 * k < nc ? __ldcg(a.part_lse + row_of(lane + 32 * k)) : -INFINITY;
+    load(0);  // together with the weights
+#pragma unroll
+    for (int k = 0; k < kW; ++k) M = fmaxf(M, w[k]);  // a NaN stays out of M and comes back through the weights
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+      w[k] = lane + 32 * k < nc ? exp2f(w[k] - ms) : 0.f;
+      L += w[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int b = 0;;) {
+      float ws = w[0];
+#pragma unroll
+      for (int k = 1; k < kW; ++k) ws = b >= 32 * k ? w[k] : ws;
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, ws, (b + k) & 31);
+        if (b + k < nc && wk != 0.f) {  // a chunk without weight adds nothing
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[k][e], acc[e]);
+        }
+      }
+      b += kAt;
+      if (b >= nc) break;
+      load(b);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    OutT* dst = static_cast<OutT*>(p.out) + (int64_t)(c0 + i) * p.o_st + (int64_t)hq * p.o_sh + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) store2(dst + e, acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+template <int D, bool F8>
+cudaError_t launch_phase(const TcArgs& a, int N, int64_t most, int num_sms, cudaStream_t st) {
+  if constexpr (!F8) {
+    if (N == 128) return launch_shared_wide(a, most, num_sms, st);
+  }
+  return N == 16   ? launch_items<Geo<D, 16, F8, true>>(tree_tc_kernel<D, 16, F8, true>, a, most, num_sms, st)
+         : N == 32 ? launch_items<Geo<D, 32, F8, true>>(tree_tc_kernel<D, 32, F8, true>, a, most, num_sms, st)
+                   : launch_items<Geo<D, 64, F8, true>>(tree_tc_kernel<D, 64, F8, true>, a, most, num_sms, st);
+}
+
+}  // namespace
+
+int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
+  const Cut c = shared_cut(T, B, Hkv, G, max_q, max_group, max_ctx, f8);
+  return shared_own(T, c.pre_chunks, c.rows_per_seq, B);
+}
+
+cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8, int out_kind, int64_t max_q, int64_t max_group,
+                             int64_t max_ctx, void* workspace, int num_sms, cudaStream_t st) {
+  TcArgs a{};
+  a.p = p;
+  a.out_bf16 = out_kind;
+  a.by_g = fast_div(static_cast<uint32_t>(p.G));
+  a.by_bs = fast_div(static_cast<uint32_t>(p.bs));
+  const Cut c = shared_cut(p.T, p.B, p.Hkv, p.G, max_q, max_group, max_ctx, f8);
+  a.rows_per_seq = static_cast<int32_t>(c.rows_per_seq);
+  a.chunking = c.own;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = a.part_o + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq * p.D;
+  a.shared = SharedArgs{groups, kPrefixes, static_cast<int32_t>(max_group), static_cast<int32_t>(c.pre_chunks), c.pre};
+  cudaError_t e;
+  for (const int phase : {kPrefixes, kOwnKeys}) {
+    a.shared.phase = phase;
+    // the wide kernel masks the products before they are scaled
+    const int most_n = phase == kPrefixes ? c.n_pre : c.n_own, N = p.qk_scale_log2 > 0.f ? most_n : std::min(most_n, 64);
+    const int64_t most = phase == kPrefixes ? c.pre_chunks * p.Hkv * ((p.T * p.G + N - 1) / N + p.B)
+                                            : (int64_t)p.B * kTreeMaxChunks * p.Hkv * ((max_q * p.G + N - 1) / N);
+    if (p.D == 128)
+      e = f8 ? launch_phase<128, true>(a, N, most, num_sms, st) : launch_phase<128, false>(a, N, most, num_sms, st);
+    else
+      e = f8 ? launch_phase<64, true>(a, N, most, num_sms, st) : launch_phase<64, false>(a, N, most, num_sms, st);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t want = (max_q * p.Hq + 7) / 8;
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(want, (8 * num_sms + p.B - 1) / p.B));
+  const dim3 grid((unsigned)p.B, (unsigned)y);
+#define PKV_JOIN(D, O) launch_ex(shared_join_kernel<D, O>, grid, dim3(256), 0, st, true, a)
+  if (p.D == 128) return out_kind ? PKV_JOIN(128, __nv_bfloat16) : PKV_JOIN(128, float);
+  return out_kind ? PKV_JOIN(64, __nv_bfloat16) : PKV_JOIN(64, float);
+#undef PKV_JOIN
+}
+
+}  // namespace pkv

@@ -294,92 +294,25 @@ pkv_status pkv_tree_attention(const pkv_tensor* q, const pkv_tensor* cu_seqlens_
                               const pkv_tensor* tree_mask, float scale, float k_scale, float v_scale,
                               int32_t max_q_len, pkv_tensor* out, void* workspace, size_t workspace_bytes,
                               void* stream) {
-  int64_t B;
-  PKV_TRY(check_tensor("q", q, 3));
-  PKV_TRY(check_tensor("out", out, 3));
-  PKV_TRY(check_step(cu_seqlens_q, seq_lens, B));
-  PKV_TRY(check_block_tables(block_tables, B));
-  PKV_TRY(check_caches(k_cache, v_cache));
-  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2];
-  const int64_t NB = k_cache->shape[0], bs = k_cache->shape[1], Hkv = k_cache->shape[2];
-  PKV_NEED(T <= INT32_MAX, "T beyond int32");
-  PKV_NEED(k_cache->shape[3] == D, "q and cache head dims differ");
-  PKV_NEED(Hq >= 1 && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
-  PKV_NEED(Hq <= (1 << 16), "Hq beyond 65536");
-  PKV_NEED(out->shape[0] == T && out->shape[1] == Hq && out->shape[2] == D, describe("out", out) + " must have q's shape");
-  PKV_NEED(out->dtype == PKV_F32 || out->dtype == PKV_BF16, "out must be f32 or bf16");
-  PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX - kTreeKeySlack, "max_blocks * block_size beyond int32");
-  PKV_NEED(NB >= 1, "the cache has no blocks");
-  if (q->dtype != PKV_F32 && T > (int64_t(1) << 30) / Hq)
-    return fail(PKV_ERR_UNSUPPORTED, "T * Hq beyond 2^30 (a sequence's rows and work items are numbered in 32 bits)");
-  if (NB * bs > INT32_MAX / Hkv)
-    return fail(PKV_ERR_UNSUPPORTED, "num_blocks * block_size * Hkv beyond int32 (rows are numbered in 32 bits)");
-  PKV_TRY(check_mask("tree_mask", tree_mask, T));
-  PKV_NEED(max_q_len <= 0 || 32 * tree_mask->shape[1] >= max_q_len, "tree_mask: fewer than max_q_len bits a row");
+  TreeParams p{};
   int kv;
-  if (q->dtype == PKV_F32 && k_cache->dtype == PKV_F32)
-    kv = 0;
-  else if (q->dtype == PKV_BF16 && k_cache->dtype == PKV_BF16)
-    kv = 1;
-  else if (q->dtype == PKV_BF16 && k_cache->dtype == PKV_FP8_E4M3)
-    kv = 2;
-  else
-    return fail(PKV_ERR_UNSUPPORTED, std::string("q ") + dtype_name(q->dtype) + " with a " +
-                                         dtype_name(k_cache->dtype) + " cache");
-  if (kv == 0)
-    PKV_NEED(D % 32 == 0 && D <= 256, "f32 attention needs D a multiple of 32, at most 256");
-  else if (D != 64 && D != 128)
-    return fail(PKV_ERR_UNSUPPORTED, "bf16/fp8 attention is built for D = 64 and D = 128");
-  PKV_TRY(check_rows("q", q));
-  PKV_NEED(out->stride[2] == 1 || D == 1, "out must have unit stride in D");
-  const int oes = esize(out->dtype);
-  PKV_NEED(aligned(out->data, 16) && (out->stride[0] * oes) % 8 == 0 && (out->stride[1] * oes) % 8 == 0,
-           "out rows must be 8-byte aligned (data and strides)");
-  if (kv == 2) PKV_TRY(check_scales(k_scale, v_scale));
-  PKV_NEED(scale == scale, "scale is NaN");
+  PKV_TRY(check_paged_rows(q, cu_seqlens_q, seq_lens, block_tables, k_cache, v_cache, scale, k_scale, v_scale, out, p, kv));
+  PKV_TRY(check_mask("tree_mask", tree_mask, p.T));
+  PKV_NEED(max_q_len <= 0 || 32 * tree_mask->shape[1] >= max_q_len, "tree_mask: fewer than max_q_len bits a row");
   size_t ws_need = 0;
   PKV_TRY(pkv_tree_attention_workspace_size(q, block_tables, k_cache, max_q_len, &ws_need));
-  if (workspace_bytes < ws_need)
-    return fail(PKV_ERR_WORKSPACE_TOO_SMALL,
-                "workspace needs " + std::to_string(ws_need) + " bytes, got " + std::to_string(workspace_bytes));
-  PKV_NEED(ws_need == 0 || (workspace != nullptr && aligned(workspace, 256)), "workspace must be 256-byte aligned");
-  TreeParams p{};
-  p.q = q->data;
-  p.q_st = q->stride[0];
-  p.q_sh = q->stride[1];
-  p.out = out->data;
-  p.T = T;
-  p.o_st = out->stride[0];
-  p.o_sh = out->stride[1];
-  p.cu_q = static_cast<const int32_t*>(cu_seqlens_q->data);
-  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
-  p.bt = static_cast<const int32_t*>(block_tables->data);
-  p.bt_stride = block_tables->stride[0];
-  p.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
-  p.B = static_cast<int32_t>(B);
+  PKV_TRY(check_workspace(workspace, workspace_bytes, ws_need));
   p.mask = static_cast<const int32_t*>(tree_mask->data);
   p.mask_stride = tree_mask->stride[0];
-  const int64_t max_q = max_nodes_of(max_q_len, T);
+  const int64_t max_q = max_nodes_of(max_q_len, p.T);
   p.max_nodes = static_cast<int32_t>(std::min<int64_t>(32 * tree_mask->shape[1], max_q));
-  p.k_cache = k_cache->data;
-  p.v_cache = v_cache->data;
-  p.num_blocks = NB;
-  p.bs = static_cast<int32_t>(bs);
-  p.bs_shift = log2_exact(bs);
-  p.Hq = static_cast<int32_t>(Hq);
-  p.Hkv = static_cast<int32_t>(Hkv);
-  p.G = static_cast<int32_t>(Hq / Hkv);
-  p.D = static_cast<int32_t>(D);
-  const float kLog2e = 1.4426950408889634f;
-  p.qk_scale_log2 = scale * (kv == 2 ? k_scale : 1.0f) * kLog2e;
-  p.v_scale = kv == 2 ? v_scale : 1.0f;
   int sms = 0;
   PKV_TRY(device_state(&p.err, &sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T == 0 || B == 0) return PKV_OK;
+  if (p.T == 0 || p.B == 0) return PKV_OK;
   const int out_kind = out->dtype == PKV_BF16;
   const cudaError_t e = kv == 0 ? launch_tree_f32(p, out_kind, st)
-                                : launch_tree_tc(p, kv == 2, out_kind, max_q, block_tables->shape[1] * bs, workspace, sms, st);
+                                : launch_tree_tc(p, kv == 2, out_kind, max_q, block_tables->shape[1] * p.bs, workspace, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return finish(st, "pkv_tree_attention");
 }

@@ -2,6 +2,7 @@
 // plain attention kernel of the fp32 path, and the move of an accepted
 // path's cache rows.
 #include "pkv_kernels.h"
+#include "pkv_share.cuh"
 
 namespace pkv {
 
@@ -174,8 +175,9 @@ cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st) {
 // fp32 queries and caches, on the CUDA cores like pkv_attention's fp32 path:
 // one CTA per (row, KV head), a warp per query head of the group, lanes over
 // D, one key at a time.
-template <typename OutT>
-__global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
+// kShared: requests that share prefixes, each over its own table, causal.
+template <typename OutT, bool kShared>
+__global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p, SharedArgs h) {
   launch_dependents();
   grid_dep_wait();
   const int64_t t = blockIdx.x;
@@ -184,6 +186,11 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
   if (g == 0) {
     // inconsistent lengths are recorded, those of sequences without a row of their own too
     for (int64_t i = t * blockDim.x + threadIdx.x; i < p.B; i += (int64_t)gridDim.x * blockDim.x) {
+      if constexpr (kShared) {
+        int a, e, m, f;
+        if (shared_request(p, h, static_cast<int>(i), a, e, m, f)) atomicOr(p.err, kErrLengths);
+        continue;
+      }
       const int a = __ldg(p.cu_q + i), e = __ldg(p.cu_q + i + 1), m = __ldg(p.seq_lens + i);
       if (a < 0 || e < a || (int64_t)e > p.T || e - a > m || (int64_t)m > (int64_t)p.max_blocks * p.bs || e - a > p.max_nodes)
         atomicOr(p.err, kErrLengths);
@@ -199,12 +206,16 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrLengths);
     return;
   }
+  if constexpr (kShared) {
+    int a, e, m, f;
+    if (shared_request(p, h, s, a, e, m, f)) return;
+  }
   const int ctx = n - q_s;
   const int per = p.D / 32;  // elements per lane, <= 8
   const float* kc = static_cast<const float*>(p.k_cache);
   const float* vc = static_cast<const float*>(p.v_cache);
   const int32_t* bt_row = p.bt + (int64_t)s * p.bt_stride;
-  const int32_t* mask = p.mask + t * p.mask_stride;
+  const int32_t* mask = kShared ? nullptr : p.mask + t * p.mask_stride;
   for (int hh = warp; hh < p.G; hh += blockDim.x >> 5) {
     const int h = g * p.G + hh;
     const float* qrow = static_cast<const float*>(p.q) + t * p.q_st + (int64_t)h * p.q_sh;
@@ -216,7 +227,8 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
     }
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
-      if (j >= ctx && !((static_cast<uint32_t>(__ldg(mask + ((j - ctx) >> 5))) >> ((j - ctx) & 31)) & 1u)) continue;
+      if (kShared && j > ctx + static_cast<int>(t - c0)) break;
+      if (!kShared && j >= ctx && !((static_cast<uint32_t>(__ldg(mask + ((j - ctx) >> 5))) >> ((j - ctx) & 31)) & 1u)) continue;
       const int lb = p.bs_shift >= 0 ? (j >> p.bs_shift) : (j / p.bs);
       const int32_t blk = __ldg(bt_row + lb);
       if (blk < 0 || blk >= p.num_blocks) {
@@ -248,10 +260,22 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p) {
   }
 }
 
-cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st) {
+template <bool kShared>
+static cudaError_t launch_f32_rows(const TreeParams& p, const SharedArgs& h, int out_kind, cudaStream_t st) {
   const dim3 grid((unsigned)p.T, (unsigned)p.Hkv), block(128);
-  return out_kind ? launch_ex(tree_f32_kernel<__nv_bfloat16>, grid, block, 0, st, true, p)
-                  : launch_ex(tree_f32_kernel<float>, grid, block, 0, st, true, p);
+  return out_kind ? launch_ex(tree_f32_kernel<__nv_bfloat16, kShared>, grid, block, 0, st, true, p, h)
+                  : launch_ex(tree_f32_kernel<float, kShared>, grid, block, 0, st, true, p, h);
+}
+
+cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st) {
+  return launch_f32_rows<false>(p, SharedArgs{}, out_kind, st);
+}
+
+cudaError_t launch_shared_f32(const TreeParams& p, const int32_t* groups, int64_t max_group, int out_kind, cudaStream_t st) {
+  SharedArgs h{};
+  h.groups = groups;
+  h.max_group = static_cast<int32_t>(max_group);
+  return launch_f32_rows<true>(p, h, out_kind, st);
 }
 
 }  // namespace pkv

@@ -1,5 +1,5 @@
-// pkv_tree_tc.cuh -- what the tensor-core kernels of tree attention share: the
-// cut of a call into items, the barriers of a CTA, the warps that find items and
+// pkv_tree_tc.cuh -- what the tensor-core kernels of tree attention, and of
+// attention with shared prefixes, have in common: the cut of a call into items, the barriers of a CTA, the warps that find items and
 // bring their query rows, the warps that copy K and V tiles, and the PTX they
 // are made of.
 #pragma once
@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "pkv_kernels.h"
+#include "pkv_share.cuh"
 
 namespace pkv {
 
@@ -40,9 +41,6 @@ constexpr int kInfoSlots = 8;
 constexpr int kTreeMaxChunks = 64;
 constexpr int kTreePartRows = 1024;
 constexpr int kTreeItems = 8 * 152;
-struct Chunking {
-  int32_t least, most;
-};
 inline Chunking tree_chunking(int64_t units) {
   Chunking c;
   c.least = units >= 256 ? 2048 : units >= 16 ? 1024 : 256;
@@ -64,7 +62,7 @@ struct alignas(16) Item {
   int t0, q_s, n;       // first packed row, nodes, keys
   int k0, k1;           // keys of the chunk
   int c, nchunks;       // its index, chunks of the sequence
-  int nt, pad;          // key tiles (0: no more items)
+  int nt, ctx;          // key tiles (0: no more items); keys before ctx are seen by every row
 };
 
 constexpr int kMiscBytes = 6656;  // a CTA's control area
@@ -297,7 +295,48 @@ struct TcArgs {
   int32_t out_bf16;
   float* part_o;         // [B * rows_per_seq, Hq, D] normalised chunk outputs
   float* part_lse;       // [B * rows_per_seq, Hq]
+  SharedArgs shared;     // requests that share prefixes
 };
+
+// Where an item's rows go: to partial row at + i * step for node (or row) i, or,
+// when nothing has to be joined, straight to the output.
+struct Part {
+  int64_t at, step;
+  bool split;
+};
+// Trees: the chunks of a node side by side, rows_per_seq rows a sequence.
+// Requests that share prefixes: the prefix chunks of packed row t at t *
+// pre_chunks; then one row for each packed row (requests of one chunk of their
+// own); then those of requests of several, as for trees.
+template <bool S>
+__device__ __forceinline__ Part part_of(const TcArgs& a, const Item& it) {
+  if constexpr (!S) {
+    return Part{(int64_t)it.s * a.rows_per_seq + it.c, it.nchunks, it.nchunks > 1};
+  } else {
+    const SharedArgs& h = a.shared;
+    if (h.phase == kPrefixes) return Part{(int64_t)it.t0 * h.pre_chunks + it.c, h.pre_chunks, true};
+    if (it.nchunks == 1) return Part{shared_single(a.p.T, h.pre_chunks, it.t0), 1, it.k0 > 0};
+    return Part{shared_own(a.p.T, h.pre_chunks, a.rows_per_seq, it.s) + it.c, it.nchunks, true};
+  }
+}
+// whether node i sees drafted key jj (key ctx + jj)
+template <bool S>
+__device__ __forceinline__ bool sees(const TreeParams& p, const Item& it, int i, int jj) {
+  if constexpr (S) return jj < i;
+  return (static_cast<uint32_t>(__ldg(p.mask + (int64_t)(it.t0 + i) * p.mask_stride + (jj >> 5))) >> (jj & 31)) & 1u;
+}
+// The prefixes' kernel lets that of the requests' own keys start beside it, once
+// what came before both is complete; so that one need not wait for it, but only
+// end after it (its first CTA waits), since the join waits for the last kernel alone.
+template <bool S>
+__device__ __forceinline__ void begin_phase(const TcArgs& a) {
+  if (!S || a.shared.phase == kPrefixes) grid_dep_wait();
+  if (S && a.shared.phase == kPrefixes) launch_dependents();
+}
+template <bool S>
+__device__ __forceinline__ void end_phase(const TcArgs& a) {
+  if (S && a.shared.phase == kOwnKeys && blockIdx.x == 0) grid_dep_wait();
+}
 
 // What every warp of a CTA needs: its barriers and its items.
 struct Cta {
@@ -472,7 +511,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   const int lane = cta.lane, G = p.G, Hkv = p.Hkv;
   auto bar = [&](int i) -> uint32_t { return cta.bar(i); };
   int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
-  int c0 = 0, q_s = 0, n = 0, chunk = 1, nchunks = 0, rts = 0;
+  int c0 = 0, q_s = 0, n = 0, k_at = 0, chunk = 1, nchunks = 0, rts = 0;  // (k_at: a request's first own key)
   // items: this sequence's, prefix in the group, in it; before it.  A sequence has
   // at most Hq max(1024, q_s) / 16 + 64 Hkv of them, 2^27 since T Hq <= 2^30, and so
   // a group's fit 32 bits, whatever the lengths are
@@ -495,18 +534,39 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       const int s = gb + lane;
       cnt = 0;
       if (s < p.B) {
-        c0 = __ldg(p.cu_q + s);
-        const int c1 = __ldg(p.cu_q + s + 1);
-        n = __ldg(p.seq_lens + s);
-        q_s = c1 - c0;
-        const bool bad = c0 < 0 || c1 < c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs ||
-                         q_s > p.max_nodes;
-        if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-        if (!bad && q_s > 0) {
-          chunk = tree_chunk(n, q_s, a.chunking);
-          nchunks = (n - 1) / chunk + 1;
-          rts = (q_s * G - 1) / N + 1;
-          cnt = nchunks * Hkv * rts;
+        if constexpr (G_::kShared) {
+          if (a.shared.phase == kPrefixes) {
+            // the rows of all the group's requests, the prefix's keys; every row sees all of them
+            if (shared_prefix(p, a.shared, s, c0, q_s, n)) {
+              chunk = tree_chunk(n, 1, a.shared.pre);
+              nchunks = (n - 1) / chunk + 1;
+              rts = (q_s * G - 1) / N + 1;
+              cnt = nchunks * Hkv * rts;
+            }
+          } else {
+            const bool bad = shared_request(p, a.shared, s, c0, q_s, n, k_at);
+            if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
+            if (!bad && q_s > 0) {
+              chunk = tree_chunk(n - k_at, q_s, a.chunking);
+              nchunks = (n - k_at - 1) / chunk + 1;
+              rts = (q_s * G - 1) / N + 1;
+              cnt = nchunks * Hkv * rts;
+            }
+          }
+        } else {
+          c0 = __ldg(p.cu_q + s);
+          const int c1 = __ldg(p.cu_q + s + 1);
+          n = __ldg(p.seq_lens + s);
+          q_s = c1 - c0;
+          const bool bad = c0 < 0 || c1 < c0 || (int64_t)c1 > p.T || q_s > n || (int64_t)n > (int64_t)p.max_blocks * p.bs ||
+                           q_s > p.max_nodes;
+          if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
+          if (!bad && q_s > 0) {
+            chunk = tree_chunk(n, q_s, a.chunking);
+            nchunks = (n - 1) / chunk + 1;
+            rts = (q_s * G - 1) / N + 1;
+            cnt = nchunks * Hkv * rts;
+          }
         }
       }
       incl = cnt;
@@ -533,7 +593,9 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       it.c = z / Hkv;
       it.h = z - it.c * Hkv;
       it.k0 = it.c * len;
+      if constexpr (G_::kShared) it.k0 += __shfl_sync(0xffffffffu, k_at, o);
       it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
+      it.ctx = !G_::kShared ? it.n - it.q_s : a.shared.phase == kPrefixes ? it.n : it.n - it.q_s + 1;
       it.nt = (it.k1 - it.k0 + kKeys - 1) / kKeys;
     }
     ok = wait_bar(bar(kBItemEmpty) + 8 * ir.at, ir.pass ^ 1) && !cta.aborted();
@@ -714,7 +776,15 @@ cudaError_t launch_items(Kern kern, TcArgs a, int64_t max_items, int num_sms, cu
   return launch_ex(kern, dim3((unsigned)std::min<int64_t>(num_sms, max_items)), dim3(G_::kThreads), G_::kSmem, st, true, a, mk, mv);
 }
 
-// 128 rows a tile, bf16 caches (pkv_tree_wide.cu)
+// Rows per MMA tile: the narrowest that holds the largest tree.
+inline int tree_tile_rows(int64_t rows, bool f8) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || f8 ? 64 : 128; }
+inline Chunking call_chunking(int64_t B, int64_t Hkv, int64_t rows, bool f8) {
+  const int64_t N = tree_tile_rows(rows, f8);
+  return tree_chunking(B * Hkv * ((rows + N - 1) / N));
+}
+
+// 128 rows a tile, bf16 caches: trees (pkv_tree_wide.cu), requests that share prefixes (pkv_share_wide.cu)
 cudaError_t launch_tree_wide(const TcArgs& a, int64_t max_items, int num_sms, cudaStream_t st);
+cudaError_t launch_shared_wide(const TcArgs& a, int64_t max_items, int num_sms, cudaStream_t st);
 
 }  // namespace pkv

@@ -208,4 +208,86 @@ inline pkv_status check_apart(const char* name, const pkv_tensor* out, std::init
   return PKV_OK;
 }
 
+// Rows of a packed batch over the paged caches, as the attention of trees and of
+// shared prefixes takes them: checks, then everything of p that follows from these.
+// kv: 0 = f32, 1 = bf16, 2 = e4m3.
+inline pkv_status check_paged_rows(const pkv_tensor* q, const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens,
+                                   const pkv_tensor* block_tables, const pkv_tensor* k_cache, const pkv_tensor* v_cache,
+                                   float scale, float k_scale, float v_scale, const pkv_tensor* out, TreeParams& p, int& kv) {
+  int64_t B;
+  PKV_TRY(check_tensor("q", q, 3));
+  PKV_TRY(check_tensor("out", out, 3));
+  PKV_TRY(check_step(cu_seqlens_q, seq_lens, B));
+  PKV_TRY(check_block_tables(block_tables, B));
+  PKV_TRY(check_caches(k_cache, v_cache));
+  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2];
+  const int64_t NB = k_cache->shape[0], bs = k_cache->shape[1], Hkv = k_cache->shape[2];
+  PKV_NEED(T <= INT32_MAX, "T beyond int32");
+  PKV_NEED(k_cache->shape[3] == D, "q and cache head dims differ");
+  PKV_NEED(Hq >= 1 && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
+  PKV_NEED(Hq <= (1 << 16), "Hq beyond 65536");
+  PKV_NEED(out->shape[0] == T && out->shape[1] == Hq && out->shape[2] == D, describe("out", out) + " must have q's shape");
+  PKV_NEED(out->dtype == PKV_F32 || out->dtype == PKV_BF16, "out must be f32 or bf16");
+  PKV_NEED(block_tables->shape[1] * bs <= INT32_MAX - kTreeKeySlack, "max_blocks * block_size beyond int32");
+  PKV_NEED(NB >= 1, "the cache has no blocks");
+  if (q->dtype != PKV_F32 && T > (int64_t(1) << 30) / Hq)
+    return fail(PKV_ERR_UNSUPPORTED, "T * Hq beyond 2^30 (a sequence's rows and work items are numbered in 32 bits)");
+  if (NB * bs > INT32_MAX / Hkv)
+    return fail(PKV_ERR_UNSUPPORTED, "num_blocks * block_size * Hkv beyond int32 (rows are numbered in 32 bits)");
+  if (q->dtype == PKV_F32 && k_cache->dtype == PKV_F32)
+    kv = 0;
+  else if (q->dtype == PKV_BF16 && k_cache->dtype == PKV_BF16)
+    kv = 1;
+  else if (q->dtype == PKV_BF16 && k_cache->dtype == PKV_FP8_E4M3)
+    kv = 2;
+  else
+    return fail(PKV_ERR_UNSUPPORTED, std::string("q ") + dtype_name(q->dtype) + " with a " +
+                                         dtype_name(k_cache->dtype) + " cache");
+  if (kv == 0)
+    PKV_NEED(D % 32 == 0 && D <= 256, "f32 attention needs D a multiple of 32, at most 256");
+  else if (D != 64 && D != 128)
+    return fail(PKV_ERR_UNSUPPORTED, "bf16/fp8 attention is built for D = 64 and D = 128");
+  PKV_TRY(check_rows("q", q));
+  PKV_NEED(out->stride[2] == 1 || D == 1, "out must have unit stride in D");
+  const int oes = esize(out->dtype);
+  PKV_NEED(aligned(out->data, 16) && (out->stride[0] * oes) % 8 == 0 && (out->stride[1] * oes) % 8 == 0,
+           "out rows must be 8-byte aligned (data and strides)");
+  if (kv == 2) PKV_TRY(check_scales(k_scale, v_scale));
+  PKV_NEED(scale == scale, "scale is NaN");
+  p.q = q->data;
+  p.q_st = q->stride[0];
+  p.q_sh = q->stride[1];
+  p.out = out->data;
+  p.T = T;
+  p.o_st = out->stride[0];
+  p.o_sh = out->stride[1];
+  p.cu_q = static_cast<const int32_t*>(cu_seqlens_q->data);
+  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  p.bt = static_cast<const int32_t*>(block_tables->data);
+  p.bt_stride = block_tables->stride[0];
+  p.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  p.B = static_cast<int32_t>(B);
+  p.k_cache = k_cache->data;
+  p.v_cache = v_cache->data;
+  p.num_blocks = NB;
+  p.bs = static_cast<int32_t>(bs);
+  p.bs_shift = log2_exact(bs);
+  p.Hq = static_cast<int32_t>(Hq);
+  p.Hkv = static_cast<int32_t>(Hkv);
+  p.G = static_cast<int32_t>(Hq / Hkv);
+  p.D = static_cast<int32_t>(D);
+  const float kLog2e = 1.4426950408889634f;
+  p.qk_scale_log2 = scale * (kv == 2 ? k_scale : 1.0f) * kLog2e;
+  p.v_scale = kv == 2 ? v_scale : 1.0f;
+  return PKV_OK;
+}
+
+inline pkv_status check_workspace(const void* workspace, size_t bytes, size_t need_bytes) {
+  if (bytes < need_bytes)
+    return fail(PKV_ERR_WORKSPACE_TOO_SMALL,
+                "workspace needs " + std::to_string(need_bytes) + " bytes, got " + std::to_string(bytes));
+  PKV_NEED(need_bytes == 0 || (workspace != nullptr && aligned(workspace, 256)), "workspace must be 256-byte aligned");
+  return PKV_OK;
+}
+
 }  // namespace pkv

@@ -49,7 +49,9 @@ def _lib():
                            ("pkv_tree_attention", [p] * 7 + [f, f, f, i, p, p, z, p]),
                            ("pkv_tree_commit", [p] * 9),
                            ("pkv_step_tables", [p] * 3 + [i] + [p] * 8),
-                           ("pkv_shared_prefixes", [p] * 3 + [i, i, p, p])):
+                           ("pkv_shared_prefixes", [p] * 3 + [i, i, p, p]),
+                           ("pkv_shared_attention_workspace_size", [p, p, p, i, i, ctypes.POINTER(z)]),
+                           ("pkv_shared_attention", [p] * 7 + [f, f, f, i, i, p, p, z, p])):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, ctypes.c_int
         _ready = lib
@@ -69,7 +71,8 @@ def _binding():
         loader.exec_module(m)
         at = lambda fn: ctypes.cast(fn, ctypes.c_void_p).value  # noqa: E731
         m.bind(PkvError, *(at(getattr(lib, "pkv_" + name)) for name in (
-            "rope_append", "tree_mask", "tree_attention", "tree_commit", "step_tables", "shared_prefixes")))
+            "rope_append", "tree_mask", "tree_attention", "tree_commit", "step_tables", "shared_prefixes",
+            "shared_attention")))
         _calls = m
     return _calls
 

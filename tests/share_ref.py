@@ -1,5 +1,7 @@
 """Plain references of the calls for requests that grow, shrink and share
-prompts, written from their definitions, a request at a time."""
+prompts, written from their definitions, a request at a time, and a batch of
+requests in groups."""
+from tests.spec_ref import Batch
 
 
 def step_tables(old, new, shared, bs, tables, free, count, T, width=None):
@@ -68,3 +70,22 @@ def shared_prefixes(cu, n, tables, bs, least):
         out += [[s, e, min(common[s + 1:e], default=0) * bs]] * (e - s)
         s = e
     return out, flags
+
+
+class SharedBatch(Batch):
+    """Requests in groups [(size, prefix tokens)] over a shuffled paged cache: own context tokens and new tokens of each.
+    The requests of a group list the first one's blocks for their prefix."""
+
+    def __init__(self, groups, own, q_lens, Hq, Hkv, D, bs, kv, seed, **kw):
+        prefix = [p for size, p in groups for _ in range(size)]
+        chain = [i - 1 for q in q_lens for i in range(q)]  # a chain of tokens sees what comes before: causal
+        super().__init__([p + o for p, o in zip(prefix, own)], q_lens, Hq, Hkv, D, bs, kv, seed, parents=chain, **kw)
+        at, self.groups = 0, []
+        for size, p in groups:
+            assert p % bs == 0
+            self.groups += [[at, at + size, p]] * size
+            for s in range(at, at + size):
+                self.tables[s][:p // bs] = self.tables[at][:p // bs]
+            at += size
+        assert at == self.B
+        self.max_group = max([int(self.cu[e] - self.cu[f]) for f, e, _ in self.groups] + [1])
