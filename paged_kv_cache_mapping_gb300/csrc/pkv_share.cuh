@@ -17,9 +17,11 @@ struct Chunking {
 struct SharedArgs {
   const int32_t* groups;  // [B, 3]: first request, request behind the last, tokens of the prefix
   int32_t phase;          // kPrefixes: the groups' rows over their prefixes; kOwnKeys: requests over the rest
+  int32_t alone;          // requests with rows enough for tiles of their own: none reads a prefix with others
   int32_t max_group;      // rows of a group at most
   int32_t pre_chunks;     // chunks of a prefix at most
   Chunking pre;           // how prefixes are cut
+  unsigned int* claims;   // items of the own keys that are taken (see next_item())
 };
 
 // Partial rows of the workspace: pre_chunks for each packed row, one more for each,
@@ -29,8 +31,8 @@ __host__ __device__ inline int64_t shared_own(int64_t T, int64_t pre_chunks, int
   return T * (pre_chunks + 1) + s * rows_per_seq;
 }
 
-// Request s: packed rows c0 .. c0 + q - 1, n keys, the first `prefix` of them its
-// group's.  Returns whether it takes no part: inconsistent lengths, a prefix that
+// Request s: packed rows c0 .. c0 + q - 1, n keys, the first `prefix` of them read
+// with its group.  Returns whether it takes no part: inconsistent lengths, a prefix that
 // is not whole blocks of its context, or a group that its first request does not
 // name in the same words or whose rows do not hold the request's.
 __device__ __forceinline__ bool shared_request(const TreeParams& p, const SharedArgs& h, int s, int& c0, int& q, int& n, int& prefix) {
@@ -44,8 +46,9 @@ __device__ __forceinline__ bool shared_request(const TreeParams& p, const Shared
   if (prefix == 0) return false;
   if (prefix < 0 || prefix > n - q || prefix % p.bs != 0 || g0 < 0 || g0 > s || g1 <= s || g1 > p.B) return true;
   const int32_t* f = h.groups + 3 * (int64_t)g0;
-  const int t0 = __ldg(p.cu_q + g0), t1 = __ldg(p.cu_q + g1);
-  return __ldg(f) != g0 || __ldg(f + 1) != g1 || __ldg(f + 2) != prefix || t0 < 0 || t0 > c0 || t1 < c1 || (int64_t)t1 > p.T ||
+  const int t0 = __ldg(p.cu_q + g0), t1 = __ldg(p.cu_q + g1), same = prefix;
+  if (h.alone) prefix = 0;
+  return __ldg(f) != g0 || __ldg(f + 1) != g1 || __ldg(f + 2) != same || t0 < 0 || t0 > c0 || t1 < c1 || (int64_t)t1 > p.T ||
          t1 - t0 > h.max_group;
 }
 
@@ -53,6 +56,7 @@ __device__ __forceinline__ bool shared_request(const TreeParams& p, const Shared
 // its table, for rows c0 .. c0 + q - 1 (those of all its requests).  What
 // shared_request() takes for a request of the group has passed all of this.
 __device__ __forceinline__ bool shared_prefix(const TreeParams& p, const SharedArgs& h, int s, int& c0, int& q, int& n) {
+  if (h.alone) return false;
   const int32_t* g = h.groups + 3 * (int64_t)s;
   const int g0 = __ldg(g), g1 = __ldg(g + 1);
   c0 = __ldg(p.cu_q + s);

@@ -19,23 +19,50 @@
 namespace pkv {
 namespace {
 
-// A prefix is cut so that the rows, in tiles for each KV head, give every SM work,
-// and into no more chunks than leave kPrePartRows partial rows per head in all.
+// How a call's keys are cut.  A chunk costs its rows' partials, an item's start and
+// end, and the join's reading; too few leave SMs without work.  `units` are the row
+// tiles of all rows, times the KV heads, as if every tile were full.
+//
+// Prefixes: chunks of `least` keys, but no more of them than give each SM one item of
+// one full group, or 8, and no more than leave kPrePartRows partial rows per head in
+// all.  Measured, us, `least` 256 / 512 / 1024 / 2048 / 4096 (whole calls):
+//     8 units, 4 rows over 1,024 keys    13.9 / 12.8 / 15.6 / 15.6 / 15.6
+//    12       , 92 rows, D 64, 12 to 3,001   27.8 / 21.9 / 22.2 / 29.4 / 37.4
+//    16       , 64 rows over 2,048       82.3 / 74.8 / 76.2 / 79.8 / 79.8
+//    32       , 64 rows in 10 groups, 1,024 to 8,192   74.6 / 64.5 / 62.2 / 67.6 / 69.3
+//   128, e4m3 , 256 rows in 16 groups, 512 to 2,048    143 / 127 / 121 / 117 / 117
+//   and 8 units, 65,536 keys, e4m3, at most 64 / 19 / 8 / 4 chunks   84 / 70 / 100 / 164
+//
+// Own keys: the trees' rule, but at most 1,024 keys a chunk, since what is left over
+// when CTAs claim their last items is an item (64 requests of 512 to 2,048 keys, 512 /
+// 1,024 / 2,048 keys: 71.9 / 71.8 / 74.7; 256 of 64 to 1,024, e4m3: 123 / 117 / 117).
+//
+// Where a request's own rows fill a tile, on average, a prefix tile would serve no
+// more of them, and its partials only cost: every request then takes all of its keys
+// alone (16 requests of 64 rows times 4 heads behind 4,096 keys: 119 us instead of
+// 125), with chunks of 8,192 keys when there are units for all SMs (1,024 / 2,048 /
+// 4,096 / 8,192 keys: 119 / 118 / 119 / 103).
 constexpr int kPrePartRows = 4096;
+constexpr int kSms = 152;  // counted here, not asked for: a workspace's size is known without a device
 struct Cut {
   int n_pre, n_own;  // rows per MMA tile
   Chunking pre, own;
+  bool alone;
   int64_t pre_chunks, rows_per_seq;
 };
 Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
   Cut c;
   c.n_pre = tree_tile_rows(max_group * G, f8);
   c.n_own = tree_tile_rows(max_q * G, f8);
+  c.alone = T * G >= B * c.n_pre;
+  const int64_t units = std::max<int64_t>(1, Hkv * ((T * G + c.n_pre - 1) / c.n_pre));
   c.own = call_chunking(B, Hkv, max_q * G, f8);
-  c.pre = tree_chunking(Hkv * ((T * G + c.n_pre - 1) / c.n_pre));
+  c.own.least = c.alone && units >= kSms ? 8192 : std::min(c.own.least, 1024);
+  c.pre.least = units < 32 ? 512 : units < 128 ? 1024 : 2048;
+  c.pre.most = static_cast<int32_t>(std::min<int64_t>(kTreeMaxChunks, std::max<int64_t>(8, kSms / units)));
   c.pre.most = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(c.pre.most, kPrePartRows / std::max<int64_t>(T, 1))));
   auto chunks = [&](const Chunking& k) { return std::max<int64_t>(1, std::min<int64_t>(k.most, (max_ctx + k.least - 1) / k.least)); };
-  c.pre_chunks = chunks(c.pre);
+  c.pre_chunks = c.alone ? 0 : chunks(c.pre);
   c.rows_per_seq = chunks(c.own) > 1 ? std::min<int64_t>(max_q * chunks(c.own), kTreePartRows) : 0;
   return c;
 }
@@ -156,13 +183,14 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   a.chunking = c.own;
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq * p.D;
-  a.shared = SharedArgs{groups, kPrefixes, static_cast<int32_t>(max_group), static_cast<int32_t>(c.pre_chunks), c.pre};
+  a.shared = SharedArgs{groups, kPrefixes, c.alone, static_cast<int32_t>(max_group), static_cast<int32_t>(c.pre_chunks), c.pre, nullptr};
+  a.shared.claims = reinterpret_cast<unsigned int*>(a.part_lse + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq);
   cudaError_t e;
   for (const int phase : {kPrefixes, kOwnKeys}) {
     a.shared.phase = phase;
     // the wide kernel masks the products before they are scaled
     const int most_n = phase == kPrefixes ? c.n_pre : c.n_own, N = p.qk_scale_log2 > 0.f ? most_n : std::min(most_n, 64);
-    const int64_t most = phase == kPrefixes ? c.pre_chunks * p.Hkv * ((p.T * p.G + N - 1) / N + p.B)
+    const int64_t most = phase == kPrefixes ? std::max<int64_t>(1, c.pre_chunks * p.Hkv * ((p.T * p.G + N - 1) / N + p.B))
                                             : (int64_t)p.B * kTreeMaxChunks * p.Hkv * ((max_q * p.G + N - 1) / N);
     if (p.D == 128)
       e = f8 ? launch_phase<128, true>(a, N, most, num_sms, st) : launch_phase<128, false>(a, N, most, num_sms, st);

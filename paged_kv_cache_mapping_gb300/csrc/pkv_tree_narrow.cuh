@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(Geo<D, N, F8, S>::kThreads, 1)
         // first try: all of the tile's work against the references there are;
         // careful: new references; last: the work against those
         enum : int { kTry, kCareful, kLast };
-        for (int mode = masked || vmask ? kCareful : kTry;;) {
+        for (int mode = (masked && t == 0) || vmask ? kCareful : kTry;;) {
           uint32_t u[NC];
           tm_ld(ts, u);
           wait_ld();

@@ -331,7 +331,10 @@ __device__ __forceinline__ bool sees(const TreeParams& p, const Item& it, int i,
 template <bool S>
 __device__ __forceinline__ void begin_phase(const TcArgs& a) {
   if (!S || a.shared.phase == kPrefixes) grid_dep_wait();
-  if (S && a.shared.phase == kPrefixes) launch_dependents();
+  if (S && a.shared.phase == kPrefixes) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.shared.claims = 0;
+    launch_dependents();
+  }
 }
 template <bool S>
 __device__ __forceinline__ void end_phase(const TcArgs& a) {
@@ -500,6 +503,19 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
     }
 }
 
+// Own keys: a CTA's first items are dealt out in strides, and then the CTAs claim the
+// rest, one at a time: their items differ in length, and they start at different
+// times, as the prefixes' kernel leaves the SMs.  That kernel zeroes the counter, so
+// no CTA claims before it is complete.
+constexpr int kDealt = 2;
+__device__ __forceinline__ int64_t next_item(const TcArgs& a, int j, int64_t x, int lane) {
+  if (a.shared.phase == kPrefixes || j < kDealt) return x + gridDim.x;
+  if (j == kDealt) grid_dep_wait();
+  unsigned int n = 0;
+  if (lane == 0) n = atomicAdd(a.shared.claims, 1u);
+  return (int64_t)kDealt * gridDim.x + __shfl_sync(0xffffffffu, n, 0);
+}
+
 // ---------------------------------------------------------------- items, query rows
 // One warp finds the CTA's items, publishes them and brings their query rows.
 // qscale: e4m3: [4][64], the rows' scales.
@@ -526,8 +542,9 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   bool ok = true;
   gb = -32;
   int64_t x = blockIdx.x;
-  for (int j = 0;; ++j, x += gridDim.x) {
+  for (int j = 0;; ++j) {
     // item number x of the call
+    if (j > 0) x = G_::kShared ? next_item(a, j, x, lane) : x + gridDim.x;
     while (x - base >= total && gb < p.B) {
       base += total;
       gb += 32;
@@ -596,6 +613,8 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       if constexpr (G_::kShared) it.k0 += __shfl_sync(0xffffffffu, k_at, o);
       it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
       it.ctx = !G_::kShared ? it.n - it.q_s : a.shared.phase == kPrefixes ? it.n : it.n - it.q_s + 1;
+      if (G_::kShared && a.shared.phase == kOwnKeys)  // no key behind the one that the tile's last row sees
+        it.k1 = min(it.k1, max(it.k0 + 1, it.ctx + quot(it.r0 + N - 1, a.by_g)));
       it.nt = (it.k1 - it.k0 + kKeys - 1) / kKeys;
     }
     ok = wait_bar(bar(kBItemEmpty) + 8 * ir.at, ir.pass ^ 1) && !cta.aborted();
