@@ -157,6 +157,7 @@ struct StepTablesParams {
   int32_t* cu_q;
   void* slots;         // int32 or int64 [T]
   int32_t* positions;  // may be NULL
+  int32_t vectors;     // slots and positions lie on 16 bytes
   int64_t T;
   unsigned int* err;
 };

@@ -33,16 +33,21 @@ pkv_status pkv_step_tables(const pkv_tensor* seq_lens, const pkv_tensor* new_seq
   PKV_TRY(check_index_vector("slot_mapping", slot_mapping, T));
   if (positions != nullptr) PKV_TRY(check_vector_i32("positions", positions, T));
   // CTAs are still reading while others write; only the count is read by all before it is written
-  const pkv_tensor none{};
-  const std::pair<const char*, pkv_tensor*> outs[] = {{"block_tables", block_tables}, {"free_blocks", free_blocks}, {"cu_seqlens_q", cu_seqlens_q},
-                                                     {"slot_mapping", slot_mapping},  {"positions", positions},     {"new_free_count", new_free_count}};
-  for (size_t i = 0; i < sizeof(outs) / sizeof(outs[0]); ++i) {
-    if (outs[i].second == nullptr) continue;
-    PKV_TRY(check_apart(outs[i].first, outs[i].second,
-                        {{"seq_lens", seq_lens}, {"new_seq_lens", new_seq_lens}, {"shared_blocks", shared_blocks != nullptr ? shared_blocks : &none}}));
-    if (outs[i].second != new_free_count) PKV_TRY(check_apart(outs[i].first, outs[i].second, {{"free_count", free_count}}));
-    for (size_t j = 0; j < i; ++j)
-      if (outs[j].second != nullptr) PKV_TRY(check_apart(outs[i].first, outs[i].second, {outs[j]}));
+  const struct {
+    const char* name;
+    const pkv_tensor* t;
+    bool out;
+  } args[] = {{"seq_lens", seq_lens, false},        {"new_seq_lens", new_seq_lens, false}, {"shared_blocks", shared_blocks, false},
+              {"free_count", free_count, false},    {"block_tables", block_tables, true},  {"free_blocks", free_blocks, true},
+              {"cu_seqlens_q", cu_seqlens_q, true}, {"slot_mapping", slot_mapping, true},  {"positions", positions, true},
+              {"new_free_count", new_free_count, true}};
+  constexpr int kArgs = sizeof(args) / sizeof(args[0]);
+  Span spans[kArgs];
+  for (int i = 0; i < kArgs; ++i) {
+    if (args[i].t != nullptr) spans[i] = span_of(args[i].t);
+    for (int j = 0; args[i].out && j < i; ++j)
+      PKV_NEED(!spans[i].meets(spans[j]) || (args[i].t == new_free_count && args[j].t == free_count),
+               std::string(args[i].name) + " must not overlap " + args[j].name);
   }
   if (B > kMaxRequests) return fail(PKV_ERR_UNSUPPORTED, "more than " + std::to_string(kMaxRequests) + " requests");
   StepTablesParams p{};

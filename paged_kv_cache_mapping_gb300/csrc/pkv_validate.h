@@ -184,22 +184,24 @@ inline int64_t max_nodes_of(int32_t max_q_len, int64_t T) {
   return max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T;
 }
 
-// Whether the address ranges that two tensors span have a byte in common.
-inline bool spans_overlap(const pkv_tensor* a, const pkv_tensor* b) {
-  auto span = [](const pkv_tensor* t, uintptr_t& lo, uintptr_t& hi) {
-    int64_t first = 0, last = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-      if (t->shape[i] == 0) return false;
-      const int64_t d = (t->shape[i] - 1) * t->stride[i];
-      (d < 0 ? first : last) += d;
-    }
-    lo = reinterpret_cast<uintptr_t>(t->data) + first * esize(t->dtype);
-    hi = reinterpret_cast<uintptr_t>(t->data) + (last + 1) * esize(t->dtype);
-    return true;
-  };
-  uintptr_t al, ah, bl, bh;
-  return span(a, al, ah) && span(b, bl, bh) && al < bh && bl < ah;
+// The address range that a tensor spans (lo == hi: it has no elements).
+struct Span {
+  uintptr_t lo = 0, hi = 0;
+  bool meets(const Span& o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
+};
+inline Span span_of(const pkv_tensor* t) {
+  int64_t first = 0, last = 0;
+  for (int i = 0; i < t->ndim; ++i) {
+    if (t->shape[i] == 0) return {};
+    const int64_t d = (t->shape[i] - 1) * t->stride[i];
+    (d < 0 ? first : last) += d;
+  }
+  const uintptr_t at = reinterpret_cast<uintptr_t>(t->data);
+  return {at + first * esize(t->dtype), at + (last + 1) * esize(t->dtype)};
 }
+
+// Whether the address ranges that two tensors span have a byte in common.
+inline bool spans_overlap(const pkv_tensor* a, const pkv_tensor* b) { return span_of(a).meets(span_of(b)); }
 
 // What a call writes must not overlap what its CTAs still read.
 inline pkv_status check_apart(const char* name, const pkv_tensor* out, std::initializer_list<std::pair<const char*, const pkv_tensor*>> others) {
