@@ -506,8 +506,10 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
 // Own keys: a CTA's first items are dealt out in strides, and then the CTAs claim the
 // rest, one at a time: their items differ in length, and they start at different
 // times, as the prefixes' kernel leaves the SMs.  That kernel zeroes the counter, so
-// no CTA claims before it is complete.
-constexpr int kDealt = 2;
+// no CTA claims before it is complete.  Calls of 64 and 256 requests, us, dealing 1 / 2
+// / 3 / 4: 74.6 / 71.9 / 71.5 / 71.4 and 120.1 / 117.4 / 115.5 / 114.8; all of them: 73.6
+// and 126.0.  Each claim made an item ahead: no better.
+constexpr int kDealt = 4;
 __device__ __forceinline__ int64_t next_item(const TcArgs& a, int j, int64_t x, int lane) {
   if (a.shared.phase == kPrefixes || j < kDealt) return x + gridDim.x;
   if (j == kDealt) grid_dep_wait();

@@ -9,7 +9,7 @@ import paged_kv_cache_mapping_gb300 as pkv
 from paged_kv_cache_mapping_gb300 import build as pkv_build
 from paged_kv_cache_mapping_gb300 import speculative as spec
 from tests import share_ref
-from tests.test_abi import BF16, FAKE, I32, I64, _t
+from tests.test_abi import BF16, E4M3, F32, FAKE, I32, I64, _t
 
 PASSED = 4  # no GPU here: the first CUDA call after the checks fails
 
@@ -119,3 +119,63 @@ def test_reference_of_groups_by_hand():
     assert out == [[0, 3, 12]] * 3 + [[3, 4, 0], [4, 5, 0], [5, 6, 0], [6, 7, 0]]
     assert share_ref.shared_prefixes(cu, n, tables, 4, 13)[0] == [[s, s + 1, 0] for s in range(7)]
     assert share_ref.shared_prefixes([0, 20], [5], [[1, 2]], 4, 1) == ([[0, 1, 0]], 4)
+
+
+# ---------------------------------------------------------------- attention
+SHORT = 3
+
+
+def attention_args(T=6, Hq=8, Hkv=2, D=64, dt=BF16, cdt=BF16, B=2):
+    return dict(q=at(1, dt, [T, Hq, D]), cu=at(2, I32, [B + 1]), sl=at(3, I32, [B]), bt=at(4, I32, [B, 5]), g=at(5, I32, [B, 3]),
+                kc=at(6, cdt, [10, 16, Hkv, D]), vc=at(7, cdt, [10, 16, Hkv, D]), scale=0.1, ks=1.0, vs=1.0, max_q=3, max_g=6,
+                o=at(8, F32, [T, Hq, D]), ws=FAKE, bytes=1 << 34)
+
+
+def attention(lib, a):
+    return lib.pkv_shared_attention(ptr(a["q"]), ptr(a["cu"]), ptr(a["sl"]), ptr(a["bt"]), ptr(a["g"]), ptr(a["kc"]), ptr(a["vc"]), a["scale"],
+                                    a["ks"], a["vs"], a["max_q"], a["max_g"], ptr(a["o"]), a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=at(1, BF16, [6, 7, 64]), o=at(8, F32, [6, 7, 64])), 1), (dict(o=at(8, F32, [6, 8, 32])), 1), (dict(o=at(8, I32, [6, 8, 64])), 1),
+    (dict(g=at(5, I32, [3, 3])), 1), (dict(g=at(5, I32, [2, 2])), 1), (dict(g=at(5, I64, [2, 3])), 1), (dict(g=at(5, I32, [2, 3], [4, 1])), 1),
+    (dict(g=at(5, I32, [6])), 1), (dict(g=None), 1), (dict(bt=at(4, I32, [3, 5])), 1), (dict(cu=at(2, I32, [2])), 1), (dict(sl=None), 1),
+    (dict(scale=float("nan")), 1), (dict(q=at(1, BF16, [6, 8, 64], [1024, 64, 1]), o=at(8, F32, [6, 8, 64], [513, 64, 1])), 1),
+    (dict(q=_t(FAKE + 2, BF16, [6, 8, 64])), 1), (dict(q=at(1, BF16, [6, 8, 64], [514, 64, 1])), 1), (dict(q=at(1, F32, [6, 8, 64])), 2),
+    (dict(q=at(1, BF16, [6, 8, 96]), o=at(8, F32, [6, 8, 96]), kc=at(6, BF16, [10, 16, 2, 96]), vc=at(7, BF16, [10, 16, 2, 96])), 2),
+    (dict(kc=at(6, BF16, [1 << 26, 16, 2, 64]), vc=at(7, BF16, [1 << 26, 16, 2, 64])), 2), (dict(kc=at(6, BF16, [0, 16, 2, 64]), vc=at(7, BF16, [0, 16, 2, 64])), 1),
+    (dict(kc=at(6, E4M3, [10, 16, 2, 64]), vc=at(7, E4M3, [10, 16, 2, 64]), ks=-1.0), 1), (dict(vc=at(7, BF16, [10, 16, 2, 128])), 1),
+    (dict(bt=at(4, I32, [2, 2 ** 27])), 1), (dict(bytes=0), SHORT), (dict(bytes=255), SHORT), (dict(ws=FAKE + 16), 1), (dict(ws=None), 1),
+    ({}, PASSED), (dict(max_q=0, max_g=0), PASSED), (dict(max_q=-5, max_g=1 << 30), PASSED),
+])
+def test_shared_attention_refusals(lib, change, status):
+    if status == PASSED and torch.cuda.is_available():
+        pytest.skip("what passes the checks would be launched")
+    assert attention(lib, {**attention_args(), **change}) == status, lib.pkv_last_error()
+    assert lib.pkv_last_error() != b""
+
+
+def workspace(lib, a):
+    n = ctypes.c_size_t(0)
+    assert lib.pkv_shared_attention_workspace_size(ptr(a["q"]), ptr(a["bt"]), ptr(a["kc"]), a["max_q"], a["max_g"], ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_workspace_sizes(lib):
+    """A row for each token and chunk of a prefix, one more for each, and the chunks of a request's own keys."""
+    a = attention_args(T=64, Hq=32, Hkv=8, D=128, B=64)
+    row = 4 * 32 * 129
+    for blocks in (1, 8, 100, 100000):
+        for q, g in ((1, 1), (1, 64), (0, 0)):
+            n = workspace(lib, {**a, "bt": at(4, I32, [64, blocks]), "max_q": q, "max_g": g})
+            assert 64 * row <= n <= (64 * 65 + 64 * 1024) * row + 256
+    assert workspace(lib, {**a, "kc": at(6, F32, [10, 16, 8, 128])}) == 0  # f32 needs none
+    assert workspace(lib, {**attention_args(T=0), "q": at(1, BF16, [0, 8, 64])}) == 0
+    huge = {**attention_args(T=1 << 25, Hq=32, Hkv=8, D=64), "max_q": 0, "max_g": 0}
+    assert workspace(lib, huge) > 0
+    assert attention(lib, {**huge, "o": at(8, F32, [1 << 25, 32, 64]), "kc": at(6, BF16, [10, 16, 8, 64]), "vc": at(7, BF16, [10, 16, 8, 64]),
+                           "bytes": 0}) == SHORT
+    for name in ("max_q_len", "max_group_len"):
+        with pytest.raises(pkv.PkvError, match=f"{name} beyond int32"):
+            i = torch.zeros(1, dtype=torch.int32)
+            pkv.pkv_shared_attention_workspace_size(i, i, i, **{name: 2 ** 31})
