@@ -102,6 +102,33 @@ def test_bf16_output_is_the_rounded_f32_output(kv):
     assert torch.equal(h, f.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("name,shape", [
+    ("many requests", ([(25, 16)] * 60, [s % 20 for s in range(1500)], [1] * 1500, 2, 1, 64, 16)),
+    ("many rows behind a prefix", ([(2, 64), (40, 96)], [0, 90] + [5] * 40, [2100, 2300] + [1] * 40, 2, 1, 64, 32)),
+    ("rows enough for tiles of their own", ([(5, 512)], [0, 7, 100, 300, 64], [130, 64, 200, 90, 128], 8, 4, 64, 16)),
+    ("more KV heads than SMs", ([(3, 32)], [4, 40, 0], [1, 2, 1], 320, 160, 64, 16)),
+    ("one long request among short ones", ([(30, 128)], [1] * 29 + [30000], [1] * 30, 2, 2, 64, 16)),
+])
+def test_large_and_uneven_batches(name, shape, kv):
+    compare(SharedBatch(*shape, kv=kv, seed=len(name)))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_blocks_beyond_two_billion_elements(kv):
+    b = SharedBatch([(3, 64), (1, 0)], [40, 3, 170, 90], [1, 2, 1, 1], 8, 2, 128, 16, kv, seed=47)
+    blocks = (1 << 31) // (16 * 2 * 128) + 5000  # an element's number passes 31 bits
+    d = Dev(b)
+    old = [d.kc, d.vc]
+    d.kc, d.vc = (torch.empty((blocks, 16, 2, 128), dtype=x.dtype, device="cuda") for x in old)
+    for x, y in zip(old, (d.kc, d.vc)):
+        y[-b.nb:].view(torch.uint8).copy_(x.view(torch.uint8))
+    d.bt = torch.where(d.bt >= 0, d.bt + (blocks - b.nb), d.bt)
+    d.run()
+    assert pkv.pkv_device_errors() == 0
+    close(b, d.out)
+
+
 def test_requests_without_a_prefix_are_pkv_attention():
     b = SharedBatch([(1, 0)] * 5, [300, 0, 17, 1000, 64], [1, 1, 1, 1, 1], 8, 2, 128, 16, "bf16", seed=2)
     d = compare(b)
