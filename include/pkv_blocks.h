@@ -26,7 +26,8 @@
  * pkv_bm_build_step: rejected ones would keep counting in the sequence's length,
  * and blocks that drafted rows filled would be found by later prompts under
  * tokens whose rows pkv_tree_commit has moved.  A server that speculates keeps the
- * tables and lengths of its drafted rows itself.
+ * tables and lengths of its drafted rows itself (pkv_step_tables in pkv.h does
+ * that on the device, rejected rows and their blocks included).
  *
  * The manager is plain host memory and host code: it never touches the GPU.
  * Its outputs (slot mapping, block tables, lengths) are the inputs of
