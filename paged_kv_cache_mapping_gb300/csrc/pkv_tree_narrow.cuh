@@ -547,7 +547,9 @@ __global__ void __launch_bounds__(Geo<D, N, F8, S>::kThreads, 1)
           if (some) vmask = unset4[grp * 4] | unset4[grp * 4 + 1] | unset4[grp * 4 + 2] | unset4[grp * 4 + 3];
         }
         // first try: all of the tile's work against the references there are;
-        // careful: new references; last: the work against those
+        // careful: new references; last: the work against those.  (A tile that a mask
+        // cuts is tried like any other once the rows have references: what they do not
+        // see is -infinity.)
         enum : int { kTry, kCareful, kLast };
         for (int mode = (masked && t == 0) || vmask ? kCareful : kTry;;) {
           uint32_t u[NC];
