@@ -243,6 +243,37 @@ def test_long_common_prefixes(blocks):
     assert pkv.pkv_device_errors() == 0
 
 
+@pytest.mark.parametrize("wide", [0, 1000, 1100, 5000, 40000])
+@pytest.mark.parametrize("B", [7, 8, 9, 17, 65, 200, 256, 257])
+def test_groups_of_wide_tables(B, wide):
+    """Tables much wider than what is used."""
+    cu, n, tables = batch(B, B, 4, 6)
+    want, flags = share_ref.shared_prefixes(cu, n, tables, 4, 4)
+    t = torch.full((B, len(tables[0]) + wide), -9, dtype=torch.int32, device=DEV)
+    t[:, :len(tables[0])] = i32(tables)
+    assert pkv.pkv_shared_prefixes(i32(cu), i32(n), t, 4, 4).tolist() == want
+    assert pkv.pkv_device_errors() == flags
+
+
+@pytest.mark.parametrize("B", [2, 60, 256])
+def test_first_differences_anywhere(B):
+    """Tables that part at every place of a few trips."""
+    r = random.Random(B)
+    width = 1024 if B == 256 else 4000
+    row = [r.randrange(1 << 20) for _ in range(width)]
+    tables = []
+    for s in range(B):
+        row = list(row)
+        at = r.choice([0, 1, 31, 32, 255, 256, 1023, 1024, 3000, width - 1, r.randrange(width)]) % width
+        row[at] = (1 << 20) + s
+        tables.append(row)
+    n = [r.choice([width, width - 1, width // 2]) * 2 for _ in range(B)]
+    cu = [0] * (B + 1)
+    want, _ = share_ref.shared_prefixes(cu, n, tables, 2, 1)
+    assert pkv.pkv_shared_prefixes(i32(cu), i32(n), i32(tables), 2, 1).tolist() == want
+    assert pkv.pkv_device_errors() == 0
+
+
 def test_bad_lengths_share_nothing():
     tables = [[1, 2, 3]] * 6
     for n, cu in (([8, 8, 13, 8, 8, 8], [0, 1, 2, 3, 4, 5, 6]), ([8, 8, -1, 8, 8, 8], [0, 1, 2, 3, 4, 5, 6]),
