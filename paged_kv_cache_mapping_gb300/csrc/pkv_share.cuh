@@ -7,7 +7,9 @@
 
 namespace pkv {
 
-enum : int { kPrefixes = 0, kOwnKeys = 1 };
+// What a launch computes: the groups' rows over their prefixes, the requests' rows
+// over the rest, or first the one and then the other.
+enum : int { kPrefixes = 0, kOwnKeys = 1, kBoth = 2 };
 
 // Keys per chunk of a long axis (see tree_chunking()).
 struct Chunking {
@@ -16,11 +18,11 @@ struct Chunking {
 
 struct SharedArgs {
   const int32_t* groups;  // [B, 3]: first request, request behind the last, tokens of the prefix
-  int32_t phase;          // kPrefixes: the groups' rows over their prefixes; kOwnKeys: requests over the rest
+  int32_t phase;          // kPrefixes, kOwnKeys or kBoth
   int32_t alone;          // requests with rows enough for tiles of their own: none reads a prefix with others
   int32_t max_group;      // rows of a group at most
   int32_t pre_chunks;     // chunks of a prefix at most
-  Chunking pre;           // how prefixes are cut
+  Chunking pre, own;      // how prefixes and own keys are cut
   unsigned int* claims;   // items of the own keys that are taken (see next_item())
 };
 

@@ -13,17 +13,18 @@
 // kernels' chunks with a causal bound for a mask.
 //
 // Three launches: the prefixes, the own keys beside them (their CTAs take the SMs as
-// the prefixes' leave them, see begin_phase()), and a join.
+// the prefixes' leave them, see begin_phase()), and a join.  Where both take tiles of
+// one size, the first two are one launch of which the prefixes are the first items.
 //
 // Bound: the memory on bf16 caches, once a kernel runs (its start takes about 5 us, of
-// which there are two); on e4m3 caches the softmax of the prefixes' 64-row tiles, and
+// which there are mostly two); on e4m3 caches the softmax of the prefixes' 64-row tiles, and
 // for short requests what an item costs besides its tiles (3 us, e4m3 4, of which a
 // tile or two are hidden).  Measured, whole calls, 8 KV heads of 4 query heads, D 128,
 // and pkv_attention on the same batch: 64 requests of 512 to 2,048 keys behind 2,048,
 // bf16, 71 us (4.9 TB/s of the 347 MB that have to be read; 105); 64 in groups of 2 to
 // 12 behind 1,024 to 8,192, bf16, 62 us (4.3 TB/s of 268 MB; 128); 16 behind 65,536,
 // e4m3, 70 us (2.9 TB/s of 205 MB; 418); 256 of 64 to 1,024 in groups of 16 behind 512
-// to 2,048, e4m3, 115 us (2.9 TB/s of 329 MB; 202); 4 behind 1,024, bf16, 13 us (28);
+// to 2,048, e4m3, 115 us (2.9 TB/s of 329 MB; 202); 4 behind 1,024, bf16, 12 us (28);
 // nothing shared, 64 of 512 to 4,096, bf16, 96 us (105).
 #include "pkv_tree_narrow.cuh"
 
@@ -52,7 +53,7 @@ namespace {
 // more of them, and its partials only cost: every request then takes all of its keys
 // alone (16 requests of 64 rows times 4 heads behind 4,096 keys: 119 us instead of
 // 125), with chunks of 8,192 keys when there are units for all SMs (1,024 / 2,048 /
-// 4,096 / 8,192 keys: 119 / 118 / 119 / 103).
+// 4,096 / 8,192 keys: 119 / 118 / 119 / 103, as two launches).
 constexpr int kPrePartRows = 4096;
 constexpr int kSms = 152;  // counted here, not asked for: a workspace's size is known without a device
 struct Cut {
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   int np = 0, own = 1;
   if (!bad) {
     if (prefix > 0) np = (prefix - 1) / tree_chunk(prefix, 1, h.pre) + 1;
-    own = (n - prefix - 1) / tree_chunk(n - prefix, q, a.chunking) + 1;
+    own = (n - prefix - 1) / tree_chunk(n - prefix, q, h.own) + 1;
   }
   grid_dep_wait();
   launch_dependents();
@@ -191,24 +192,41 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   a.by_bs = fast_div(static_cast<uint32_t>(p.bs));
   const Cut c = shared_cut(p.T, p.B, p.Hkv, p.G, max_q, max_group, max_ctx, f8);
   a.rows_per_seq = static_cast<int32_t>(c.rows_per_seq);
-  a.chunking = c.own;
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq * p.D;
-  a.shared = SharedArgs{groups, kPrefixes, c.alone, static_cast<int32_t>(max_group), static_cast<int32_t>(c.pre_chunks), c.pre, nullptr};
-  a.shared.claims = reinterpret_cast<unsigned int*>(a.part_lse + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq);
+  SharedArgs& h = a.shared;
+  h.groups = groups;
+  h.alone = c.alone;
+  h.max_group = static_cast<int32_t>(max_group);
+  h.pre_chunks = static_cast<int32_t>(c.pre_chunks);
+  h.pre = c.pre;
+  h.own = c.own;
+  h.claims = reinterpret_cast<unsigned int*>(a.part_lse + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq);
+  // the wide kernel masks the products before they are scaled
+  const int wide = p.qk_scale_log2 > 0.f ? 128 : 64, n_pre = std::min(c.n_pre, wide), n_own = std::min(c.n_own, wide);
+  // One launch of one tile saves a kernel's start; us, two launches and one:
+  //   4 requests behind 1,024 keys, 32 heads, bf16                  12.9   11.9
+  //   38, groups up to 16 behind 20,611, 4 heads, D 64, e4m3        28.1   21.7
+  //   62, groups of 2 behind 2,785, 24 heads, e4m3                  46.8   40.9
+  //   16 of 64 rows, each alone (above)                            103.3  102.3
+  // and none of 28 calls became slower.  At the larger of two tiles it would depend on
+  // where the keys are (16 and 32 rows: 18.3 to 14.3, but also 83 to 94).
+  const bool both = n_pre == n_own;
+  const int64_t most_pre = std::max<int64_t>(1, c.pre_chunks * p.Hkv * ((p.T * p.G + n_pre - 1) / n_pre + p.B));
+  const int64_t most_own = (int64_t)p.B * kTreeMaxChunks * p.Hkv * ((max_q * p.G + n_own - 1) / n_own);
+  auto launch = [&](int phase, int N, int64_t most) {
+    h.phase = phase;
+    if (p.D == 128) return f8 ? launch_phase<128, true>(a, N, most, num_sms, st) : launch_phase<128, false>(a, N, most, num_sms, st);
+    return f8 ? launch_phase<64, true>(a, N, most, num_sms, st) : launch_phase<64, false>(a, N, most, num_sms, st);
+  };
   cudaError_t e;
-  for (const int phase : {kPrefixes, kOwnKeys}) {
-    a.shared.phase = phase;
-    // the wide kernel masks the products before they are scaled
-    const int most_n = phase == kPrefixes ? c.n_pre : c.n_own, N = p.qk_scale_log2 > 0.f ? most_n : std::min(most_n, 64);
-    const int64_t most = phase == kPrefixes ? std::max<int64_t>(1, c.pre_chunks * p.Hkv * ((p.T * p.G + N - 1) / N + p.B))
-                                            : (int64_t)p.B * kTreeMaxChunks * p.Hkv * ((max_q * p.G + N - 1) / N);
-    if (p.D == 128)
-      e = f8 ? launch_phase<128, true>(a, N, most, num_sms, st) : launch_phase<128, false>(a, N, most, num_sms, st);
-    else
-      e = f8 ? launch_phase<64, true>(a, N, most, num_sms, st) : launch_phase<64, false>(a, N, most, num_sms, st);
-    if (e != cudaSuccess) return e;
+  if (both) {
+    e = launch(kBoth, n_own, most_pre + most_own);
+  } else {
+    e = launch(kPrefixes, n_pre, most_pre);
+    if (e == cudaSuccess) e = launch(kOwnKeys, n_own, most_own);
   }
+  if (e != cudaSuccess) return e;
   const int64_t want = (max_q * p.Hq + 7) / 8;
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(want, (8 * num_sms + p.B - 1) / p.B));
   const dim3 grid((unsigned)p.B, (unsigned)y);

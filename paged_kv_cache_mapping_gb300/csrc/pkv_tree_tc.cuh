@@ -1,7 +1,7 @@
 // pkv_tree_tc.cuh -- what the tensor-core kernels of tree attention, and of
-// attention with shared prefixes, have in common: the cut of a call into items, the barriers of a CTA, the warps that find items and
-// bring their query rows, the warps that copy K and V tiles, and the PTX they
-// are made of.
+// attention with shared prefixes, have in common: the cut of a call into items,
+// the barriers of a CTA, the warps that find items and bring their query rows,
+// the warps that copy K and V tiles, and the PTX they are made of.
 #pragma once
 #include <cuda.h>
 
@@ -61,7 +61,7 @@ struct alignas(16) Item {
   int s, h, r0;         // sequence, KV head, first row of the tile
   int t0, q_s, n;       // first packed row, nodes, keys
   int k0, k1;           // keys of the chunk
-  int c, nchunks;       // its index, chunks of the sequence
+  int c, nchunks;       // its index, chunks of the sequence (of a shared prefix: as a negative number)
   int nt, ctx;          // key tiles (0: no more items); keys before ctx are seen by every row
 };
 
@@ -314,7 +314,7 @@ __device__ __forceinline__ Part part_of(const TcArgs& a, const Item& it) {
     return Part{(int64_t)it.s * a.rows_per_seq + it.c, it.nchunks, it.nchunks > 1};
   } else {
     const SharedArgs& h = a.shared;
-    if (h.phase == kPrefixes) return Part{(int64_t)it.t0 * h.pre_chunks + it.c, h.pre_chunks, true};
+    if (it.nchunks < 0) return Part{(int64_t)it.t0 * h.pre_chunks + it.c, h.pre_chunks, true};  // of a prefix
     if (it.nchunks == 1) return Part{shared_single(a.p.T, h.pre_chunks, it.t0), 1, it.k0 > 0};
     return Part{shared_own(a.p.T, h.pre_chunks, a.rows_per_seq, it.s) + it.c, it.nchunks, true};
   }
@@ -330,7 +330,7 @@ __device__ __forceinline__ bool sees(const TreeParams& p, const Item& it, int i,
 // end after it (its first CTA waits), since the join waits for the last kernel alone.
 template <bool S>
 __device__ __forceinline__ void begin_phase(const TcArgs& a) {
-  if (!S || a.shared.phase == kPrefixes) grid_dep_wait();
+  if (!S || a.shared.phase != kOwnKeys) grid_dep_wait();
   if (S && a.shared.phase == kPrefixes) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.shared.claims = 0;
     launch_dependents();
@@ -511,7 +511,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& a, const Cta& c, bool i
 // and 126.0.  Each claim made an item ahead: no better.
 constexpr int kDealt = 4;
 __device__ __forceinline__ int64_t next_item(const TcArgs& a, int j, int64_t x, int lane) {
-  if (a.shared.phase == kPrefixes || j < kDealt) return x + gridDim.x;
+  if (a.shared.phase != kOwnKeys || j < kDealt) return x + gridDim.x;
   if (j == kDealt) grid_dep_wait();
   unsigned int n = 0;
   if (lane == 0) n = atomicAdd(a.shared.claims, 1u);
@@ -542,35 +542,41 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   const int ch = lane % kLanes, rr = lane / kLanes;
   Ring ir;
   bool ok = true;
+  // groups of sequences gb .. up to `last`; with shared prefixes those from `own` on are
+  // the requests' own keys, those before it the prefixes
+  int own = 0, last = p.B;
   gb = -32;
+  if constexpr (G_::kShared) {
+    own = (p.B + 31) / 32 * 32;
+    last = a.shared.phase == kPrefixes ? own : 2 * own;
+    if (a.shared.phase == kOwnKeys) gb = own - 32;
+  }
   int64_t x = blockIdx.x;
   for (int j = 0;; ++j) {
     // item number x of the call
     if (j > 0) x = G_::kShared ? next_item(a, j, x, lane) : x + gridDim.x;
-    while (x - base >= total && gb < p.B) {
+    while (x - base >= total && gb < last) {
       base += total;
       gb += 32;
-      const int s = gb + lane;
+      const int s = (G_::kShared && gb >= own ? gb - own : gb) + lane;
       cnt = 0;
-      if (s < p.B) {
+      if (s < p.B && gb < last) {
         if constexpr (G_::kShared) {
-          if (a.shared.phase == kPrefixes) {
+          bool some;
+          k_at = 0;
+          if (gb < own) {
             // the rows of all the group's requests, the prefix's keys; every row sees all of them
-            if (shared_prefix(p, a.shared, s, c0, q_s, n)) {
-              chunk = tree_chunk(n, 1, a.shared.pre);
-              nchunks = (n - 1) / chunk + 1;
-              rts = (q_s * G - 1) / N + 1;
-              cnt = nchunks * Hkv * rts;
-            }
+            some = shared_prefix(p, a.shared, s, c0, q_s, n);
           } else {
             const bool bad = shared_request(p, a.shared, s, c0, q_s, n, k_at);
             if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-            if (!bad && q_s > 0) {
-              chunk = tree_chunk(n - k_at, q_s, a.chunking);
-              nchunks = (n - k_at - 1) / chunk + 1;
-              rts = (q_s * G - 1) / N + 1;
-              cnt = nchunks * Hkv * rts;
-            }
+            some = !bad && q_s > 0;
+          }
+          if (some) {
+            chunk = gb < own ? tree_chunk(n, 1, a.shared.pre) : tree_chunk(n - k_at, q_s, a.shared.own);
+            nchunks = (n - k_at - 1) / chunk + 1;
+            rts = (q_s * G - 1) / N + 1;
+            cnt = nchunks * Hkv * rts;
           }
         } else {
           c0 = __ldg(p.cu_q + s);
@@ -601,7 +607,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       const uint32_t at = static_cast<uint32_t>(x - base);
       const int o = __ffs(__ballot_sync(0xffffffffu, incl > at)) - 1;
       const int y = static_cast<int>(at - __shfl_sync(0xffffffffu, incl - cnt, o));
-      it.s = gb + o;
+      it.s = (G_::kShared && gb >= own ? gb - own : gb) + o;
       it.t0 = __shfl_sync(0xffffffffu, c0, o);
       it.q_s = __shfl_sync(0xffffffffu, q_s, o);
       it.n = __shfl_sync(0xffffffffu, n, o);
@@ -614,9 +620,17 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       it.k0 = it.c * len;
       if constexpr (G_::kShared) it.k0 += __shfl_sync(0xffffffffu, k_at, o);
       it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
-      it.ctx = !G_::kShared ? it.n - it.q_s : a.shared.phase == kPrefixes ? it.n : it.n - it.q_s + 1;
-      if (G_::kShared && a.shared.phase == kOwnKeys)  // no key behind the one that the tile's last row sees
-        it.k1 = min(it.k1, max(it.k0 + 1, it.ctx + quot(it.r0 + N - 1, a.by_g)));
+      it.ctx = it.n - it.q_s;
+      if constexpr (G_::kShared) {
+        if (gb < own) {
+          it.nchunks = -it.nchunks;
+          it.ctx = it.n;
+        } else {
+          ++it.ctx;  // the first new key, too, is seen by every row
+          // no key behind the one that the tile's last row sees
+          it.k1 = min(it.k1, max(it.k0 + 1, it.ctx + quot(it.r0 + N - 1, a.by_g)));
+        }
+      }
       it.nt = (it.k1 - it.k0 + kKeys - 1) / kKeys;
     }
     ok = wait_bar(bar(kBItemEmpty) + 8 * ir.at, ir.pass ^ 1) && !cta.aborted();
