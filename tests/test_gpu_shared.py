@@ -115,6 +115,25 @@ def test_large_and_uneven_batches(name, shape, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G,q", [(1, 1), (4, 2), (5, 3), (8, 4), (8, 8), (8, 9)])
+def test_groups_whose_rows_need_no_larger_tile_than_their_requests(G, q, kv):
+    # pairs of requests of 9 to 16, 17 to 32, .. rows and some alone, in more than one set
+    # of 32 requests; every ninth has no rows, every seventh no keys of its own but the new
+    r = np.random.default_rng(900 + 10 * G + q)
+    groups = [(2 if i % 4 else 1, int(r.integers(0, 9)) * 48) for i in range(42)]
+    B = sum(g for g, _ in groups)
+    own = [0 if i % 7 == 3 else int(r.integers(0, 700)) for i in range(B)]
+    new = [0 if i % 9 == 5 else 1 + (i * 5) % q for i in range(B)]
+    b = SharedBatch(groups, own, new, 2 * G, 2, 64 if q & 1 else 128, 48, kv=kv, seed=900 + 10 * G + q)
+    d = compare(b)
+    first = d.out.clone()
+    compare(b, max_group=max(new) * B)  # other tiles for the groups
+    d.out.fill_(7.0)
+    d.run()
+    assert torch.equal(first, d.out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_blocks_beyond_two_billion_elements(kv):
     b = SharedBatch([(3, 64), (1, 0)], [40, 3, 170, 90], [1, 2, 1, 1], 8, 2, 128, 16, kv, seed=47)
     blocks = (1 << 31) // (16 * 2 * 128) + 5000  # an element's number passes 31 bits
