@@ -542,29 +542,31 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   const int ch = lane % kLanes, rr = lane / kLanes;
   Ring ir;
   bool ok = true;
-  // groups of sequences gb .. up to `last`; with shared prefixes those from `own` on are
-  // the requests' own keys, those before it the prefixes
-  int own = 0, last = p.B;
   gb = -32;
-  if constexpr (G_::kShared) {
-    own = (p.B + 31) / 32 * 32;
-    last = a.shared.phase == kPrefixes ? own : 2 * own;
-    if (a.shared.phase == kOwnKeys) gb = own - 32;
-  }
+  // with shared prefixes: whether it is at these; the requests' own keys follow them
+  bool pre = G_::kShared && a.shared.phase != kOwnKeys;
   int64_t x = blockIdx.x;
   for (int j = 0;; ++j) {
     // item number x of the call
     if (j > 0) x = G_::kShared ? next_item(a, j, x, lane) : x + gridDim.x;
-    while (x - base >= total && gb < last) {
+    while (x - base >= total) {
       base += total;
-      gb += 32;
-      const int s = (G_::kShared && gb >= own ? gb - own : gb) + lane;
+      if (gb + 32 < p.B) {
+        gb += 32;
+      } else if (G_::kShared && pre && a.shared.phase == kBoth) {
+        pre = false;
+        gb = 0;
+      } else {
+        total = 0;
+        break;
+      }
+      const int s = gb + lane;
       cnt = 0;
-      if (s < p.B && gb < last) {
+      if (s < p.B) {
         if constexpr (G_::kShared) {
           bool some;
           k_at = 0;
-          if (gb < own) {
+          if (pre) {
             // the rows of all the group's requests, the prefix's keys; every row sees all of them
             some = shared_prefix(p, a.shared, s, c0, q_s, n);
           } else {
@@ -573,7 +575,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
             some = !bad && q_s > 0;
           }
           if (some) {
-            chunk = gb < own ? tree_chunk(n, 1, a.shared.pre) : tree_chunk(n - k_at, q_s, a.shared.own);
+            chunk = pre ? tree_chunk(n, 1, a.shared.pre) : tree_chunk(n - k_at, q_s, a.shared.own);
             nchunks = (n - k_at - 1) / chunk + 1;
             rts = (q_s * G - 1) / N + 1;
             cnt = nchunks * Hkv * rts;
@@ -607,7 +609,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       const uint32_t at = static_cast<uint32_t>(x - base);
       const int o = __ffs(__ballot_sync(0xffffffffu, incl > at)) - 1;
       const int y = static_cast<int>(at - __shfl_sync(0xffffffffu, incl - cnt, o));
-      it.s = (G_::kShared && gb >= own ? gb - own : gb) + o;
+      it.s = gb + o;
       it.t0 = __shfl_sync(0xffffffffu, c0, o);
       it.q_s = __shfl_sync(0xffffffffu, q_s, o);
       it.n = __shfl_sync(0xffffffffu, n, o);
@@ -622,7 +624,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
       it.ctx = it.n - it.q_s;
       if constexpr (G_::kShared) {
-        if (gb < own) {
+        if (pre) {
           it.nchunks = -it.nchunks;
           it.ctx = it.n;
         } else {
