@@ -22,15 +22,22 @@ struct SharedArgs {
   int32_t alone;          // requests with rows enough for tiles of their own: none reads a prefix with others
   int32_t max_group;      // rows of a group at most
   int32_t pre_chunks;     // chunks of a prefix at most
+  int32_t own_chunks;     // partial rows for each packed row, of own keys; 0: they are counted by request
   Chunking pre, own;      // how prefixes and own keys are cut
   unsigned int* claims;   // items of the own keys that are taken (see next_item())
 };
 
 // Partial rows of the workspace: pre_chunks for each packed row, one more for each,
-// rows_per_seq for each request.
+// then those of own keys in several chunks: own_chunks for each packed row, or
+// rows_per_seq for each request, whichever is less in all.  (A bound on a request's
+// rows says little of a batch with one prompt among decodes, and the number of packed
+// rows little where most of them are padding.)
 __host__ __device__ inline int64_t shared_single(int64_t T, int64_t pre_chunks, int64_t t) { return T * pre_chunks + t; }
-__host__ __device__ inline int64_t shared_own(int64_t T, int64_t pre_chunks, int64_t rows_per_seq, int64_t s) {
-  return T * (pre_chunks + 1) + s * rows_per_seq;
+__host__ __device__ inline int64_t shared_own(int64_t T, int64_t pre_chunks) { return T * (pre_chunks + 1); }
+// of request s, packed rows from c0 on, nc chunks: its first partial row, and how far a row's are from the last one's
+__device__ __forceinline__ int64_t own_part(const TreeParams& p, const SharedArgs& h, int rows_per_seq, int s, int c0, int nc, int& step) {
+  step = h.own_chunks ? h.own_chunks : nc;
+  return shared_own(p.T, h.pre_chunks) + (h.own_chunks ? (int64_t)c0 * step : (int64_t)s * rows_per_seq);
 }
 
 // Request s: packed rows c0 .. c0 + q - 1, n keys, the first `prefix` of them read

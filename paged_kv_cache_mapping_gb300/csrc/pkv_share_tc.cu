@@ -60,7 +60,8 @@ struct Cut {
   int n_pre, n_own;  // rows per MMA tile
   Chunking pre, own;
   bool alone;
-  int64_t pre_chunks, rows_per_seq;
+  int64_t pre_chunks, own_chunks, rows_per_seq;
+  int64_t rows;  // partial rows in all
 };
 Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
   Cut c;
@@ -75,7 +76,10 @@ Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int6
   c.pre.most = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(c.pre.most, kPrePartRows / std::max<int64_t>(T, 1))));
   auto chunks = [&](const Chunking& k) { return std::max<int64_t>(1, std::min<int64_t>(k.most, (max_ctx + k.least - 1) / k.least)); };
   c.pre_chunks = c.alone ? 0 : chunks(c.pre);
-  c.rows_per_seq = chunks(c.own) > 1 ? std::min<int64_t>(max_q * chunks(c.own), kTreePartRows) : 0;
+  const int64_t most = chunks(c.own);
+  c.rows_per_seq = most > 1 ? std::min<int64_t>(max_q * most, kTreePartRows) : 0;
+  c.own_chunks = most > 1 && T * most <= B * c.rows_per_seq ? most : 0;
+  c.rows = shared_own(T, c.pre_chunks) + (c.own_chunks ? T * c.own_chunks : B * c.rows_per_seq);
   return c;
 }
 
@@ -101,11 +105,12 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const int nc = np + own;
   if (bad || nc == 1) return;
   const int64_t rows = (int64_t)q * p.Hq;
+  int own_step;
+  const int64_t own_first = own_part(p, h, a.rows_per_seq, s, c0, own, own_step);
   for (int64_t r = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.y * 8) {
     const int i = static_cast<int>(r / p.Hq), hq = static_cast<int>(r - (int64_t)i * p.Hq);
     const int64_t pre_at = (int64_t)(c0 + i) * h.pre_chunks;
-    const int64_t own_at = own == 1 ? shared_single(p.T, h.pre_chunks, c0 + i)
-                                    : shared_own(p.T, h.pre_chunks, a.rows_per_seq, s) + (int64_t)i * own;
+    const int64_t own_at = own == 1 ? shared_single(p.T, h.pre_chunks, c0 + i) : own_first + (int64_t)i * own_step;
     auto row_of = [&](int c) { return ((c < np ? pre_at + c : own_at + (c - np)) * p.Hq + hq); };
     float v[kAt][E];
     auto load = [&](int b) {
@@ -179,8 +184,7 @@ cudaError_t launch_phase(const TcArgs& a, int N, int64_t most, int num_sms, cuda
 }  // namespace
 
 int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
-  const Cut c = shared_cut(T, B, Hkv, G, max_q, max_group, max_ctx, f8);
-  return shared_own(T, c.pre_chunks, c.rows_per_seq, B);
+  return shared_cut(T, B, Hkv, G, max_q, max_group, max_ctx, f8).rows;
 }
 
 cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8, int out_kind, int64_t max_q, int64_t max_group,
@@ -193,15 +197,16 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   const Cut c = shared_cut(p.T, p.B, p.Hkv, p.G, max_q, max_group, max_ctx, f8);
   a.rows_per_seq = static_cast<int32_t>(c.rows_per_seq);
   a.part_o = static_cast<float*>(workspace);
-  a.part_lse = a.part_o + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq * p.D;
+  a.part_lse = a.part_o + c.rows * p.Hq * p.D;
   SharedArgs& h = a.shared;
   h.groups = groups;
   h.alone = c.alone;
   h.max_group = static_cast<int32_t>(max_group);
   h.pre_chunks = static_cast<int32_t>(c.pre_chunks);
+  h.own_chunks = static_cast<int32_t>(c.own_chunks);
   h.pre = c.pre;
   h.own = c.own;
-  h.claims = reinterpret_cast<unsigned int*>(a.part_lse + shared_own(p.T, c.pre_chunks, c.rows_per_seq, p.B) * p.Hq);
+  h.claims = reinterpret_cast<unsigned int*>(a.part_lse + c.rows * p.Hq);
   // the wide kernel masks the products before they are scaled
   const int wide = p.qk_scale_log2 > 0.f ? 128 : 64, n_pre = std::min(c.n_pre, wide), n_own = std::min(c.n_own, wide);
   // One launch of one tile saves a kernel's start; us, two launches and one:

@@ -307,7 +307,7 @@ struct Part {
 // Trees: the chunks of a node side by side, rows_per_seq rows a sequence.
 // Requests that share prefixes: the prefix chunks of packed row t at t *
 // pre_chunks; then one row for each packed row (requests of one chunk of their
-// own); then those of requests of several, as for trees.
+// own); then those of requests of several (see own_part()).
 template <bool S>
 __device__ __forceinline__ Part part_of(const TcArgs& a, const Item& it) {
   if constexpr (!S) {
@@ -316,7 +316,9 @@ __device__ __forceinline__ Part part_of(const TcArgs& a, const Item& it) {
     const SharedArgs& h = a.shared;
     if (it.nchunks < 0) return Part{(int64_t)it.t0 * h.pre_chunks + it.c, h.pre_chunks, true};  // of a prefix
     if (it.nchunks == 1) return Part{shared_single(a.p.T, h.pre_chunks, it.t0), 1, it.k0 > 0};
-    return Part{shared_own(a.p.T, h.pre_chunks, a.rows_per_seq, it.s) + it.c, it.nchunks, true};
+    int step;
+    const int64_t at = own_part(a.p, h, a.rows_per_seq, it.s, it.t0, it.nchunks, step);
+    return Part{at + it.c, step, true};
   }
 }
 // whether node i sees drafted key jj (key ctx + jj)
