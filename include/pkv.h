@@ -658,7 +658,10 @@ PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv
  *   workspace      pkv_shared_attention_workspace_size() bytes, 256-byte aligned;
  *                  scratch of one call: nothing in it is kept between calls
  *
- * Groups must not overlap, and the tables of a group must agree in the entries of
+ * Each request follows the numbers that it names itself, and neighbours that name
+ * the same group read its prefix together: where another request stands between
+ * them (one alone, or of another group), those before it and those behind it read the
+ * prefix each for themselves.  The tables of a group must agree in the entries of
  * the prefix: it is read through its first request's table, whose own lengths do
  * not matter.  A prefix is whole blocks, and context of every request of the group
  * (prefix <= N_s - q_s).  A request that breaks this, or whose first request's

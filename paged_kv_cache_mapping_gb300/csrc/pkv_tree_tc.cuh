@@ -532,6 +532,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   auto bar = [&](int i) -> uint32_t { return cta.bar(i); };
   int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
   int c0 = 0, q_s = 0, n = 0, k_at = 0, chunk = 1, nchunks = 0, rts = 0;  // (k_at: a request's first own key)
+  int table = 0;  // of a run of requests: the one whose table has the prefix
   // items: this sequence's, prefix in the group, in it; before it.  A sequence has
   // at most Hq max(1024, q_s) / 16 + 64 Hkv of them, 2^27 since T Hq <= 2^30, and so
   // a group's fit 32 bits, whatever the lengths are
@@ -564,25 +565,25 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       }
       const int s = gb + lane;
       cnt = 0;
-      if (s < p.B) {
-        if constexpr (G_::kShared) {
-          bool some;
-          k_at = 0;
-          if (pre) {
-            // the rows of all the group's requests, the prefix's keys; every row sees all of them
-            some = shared_prefix(p, a.shared, s, c0, q_s, n);
-          } else {
-            const bool bad = shared_request(p, a.shared, s, c0, q_s, n, k_at);
-            if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-            some = !bad && q_s > 0;
-          }
-          if (some) {
-            chunk = pre ? tree_chunk(n, 1, a.shared.pre) : tree_chunk(n - k_at, q_s, a.shared.own);
-            nchunks = (n - k_at - 1) / chunk + 1;
-            rts = (q_s * G - 1) / N + 1;
-            cnt = nchunks * Hkv * rts;
-          }
-        } else {
+      if constexpr (G_::kShared) {
+        bool some = false;
+        k_at = 0;
+        if (pre) {
+          // the rows of all the run's requests, the prefix's keys; every row sees all of them
+          some = shared_run(p, a.shared, gb, lane, c0, q_s, n, table);
+        } else if (s < p.B) {
+          const bool bad = shared_request(p, a.shared, s, c0, q_s, n, k_at);
+          if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
+          some = !bad && q_s > 0;
+        }
+        if (some) {
+          chunk = pre ? tree_chunk(n, 1, a.shared.pre) : tree_chunk(n - k_at, q_s, a.shared.own);
+          nchunks = (n - k_at - 1) / chunk + 1;
+          rts = (q_s * G - 1) / N + 1;
+          cnt = nchunks * Hkv * rts;
+        }
+      } else {
+        if (s < p.B) {
           c0 = __ldg(p.cu_q + s);
           const int c1 = __ldg(p.cu_q + s + 1);
           n = __ldg(p.seq_lens + s);
@@ -626,7 +627,9 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
       it.ctx = it.n - it.q_s;
       if constexpr (G_::kShared) {
+        const int t = __shfl_sync(0xffffffffu, table, o);
         if (pre) {
+          it.s = t;
           it.nchunks = -it.nchunks;
           it.ctx = it.n;
         } else {
