@@ -642,7 +642,9 @@ PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv
 /*
  * pkv_shared_attention -- pkv_attention for requests that share prefixes: the
  * blocks of a shared prefix are read once for the rows of all the requests that
- * share it, and joined with each request's own keys.
+ * share it, and joined with each request's own keys.  A request with rows enough for
+ * tiles of their own (a prompt) gains nothing by that and reads all of its keys alone,
+ * which keeps nobody else from sharing; nor do rows of q behind the last.
  *
  * Arguments, layouts and results as pkv_attention (causal, q_s new rows of a
  * request at its end), and
@@ -674,9 +676,10 @@ PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv
  * Values of keys that a row does not see never reach it (an infinity in a row of V
  * that every row of a request sees may reach them as NaN).  Precision as
  * pkv_tree_attention.  A row's result depends on its own request, its group's
- * prefix and on the call's shapes (T, B, Hq, Hkv, max_q_len, max_group_len,
- * max_blocks * block_size: they choose how a long axis is split), not on block
- * size, placement or the other requests.
+ * prefix, on the call's shapes (T, B, Hq, Hkv, max_q_len, max_group_len,
+ * max_blocks * block_size) and on how many rows the requests have (these choose
+ * which requests share and how a long axis is split), not on block size, placement
+ * or what the other requests hold.
  *
  * Supported: as pkv_tree_attention (bf16 q with bf16 or e4m3 caches at D = 64 and
  * 128; f32 q with f32 caches at D a multiple of 32 up to 256, where each request

@@ -175,8 +175,9 @@ struct PrefixParams {
 cudaError_t launch_shared_prefixes(const PrefixParams& p, cudaStream_t st);
 
 // Attention of requests that share prefixes (TreeParams without masks).  The
-// workspace holds shared_rows() partial rows (D + 1 floats per head).
-int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8);
+// workspace holds shared_rows() partial rows (D + 1 floats per head), then `words`
+// of 32 bits.
+int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8, int64_t* words);
 cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8, int out_kind, int64_t max_q, int64_t max_group,
                              int64_t max_ctx, void* workspace, int num_sms, cudaStream_t st);
 cudaError_t launch_shared_f32(const TreeParams& p, const int32_t* groups, int64_t max_group, int out_kind, cudaStream_t st);

@@ -115,9 +115,10 @@ pkv_status pkv_shared_attention_workspace_size(const pkv_tensor* q, const pkv_te
   *bytes = 0;
   const int64_t T = q->shape[0], B = block_tables->shape[0], Hkv = k_cache->shape[2], G = Hkv > 0 ? q->shape[1] / Hkv : 1;
   if (k_cache->dtype == PKV_F32 || T == 0 || B == 0) return PKV_OK;
+  int64_t words;
   const int64_t rows = shared_rows(T, B, Hkv, G, max_nodes_of(max_q_len, T), max_nodes_of(max_group_len, T),
-                                   block_tables->shape[1] * k_cache->shape[1], k_cache->dtype == PKV_FP8_E4M3);
-  *bytes = align_up(sizeof(float) * rows * q->shape[1] * (q->shape[2] + 1) + sizeof(unsigned int), 256);
+                                   block_tables->shape[1] * k_cache->shape[1], k_cache->dtype == PKV_FP8_E4M3, &words);
+  *bytes = align_up(sizeof(float) * rows * q->shape[1] * (q->shape[2] + 1) + sizeof(int32_t) * words, 256);
   return PKV_OK;
 }
 

@@ -49,38 +49,177 @@ namespace {
 // when CTAs claim their last items is an item (64 requests of 512 to 2,048 keys, 512 /
 // 1,024 / 2,048 keys: 71.9 / 71.8 / 74.7; 256 of 64 to 1,024, e4m3: 123 / 117 / 117).
 //
-// Where a request's own rows fill a tile, on average, a prefix tile would serve no
-// more of them, and its partials only cost: every request then takes all of its keys
-// alone (16 requests of 64 rows times 4 heads behind 4,096 keys: 119 us instead of
-// 125), with chunks of 8,192 keys when there are units for all SMs (1,024 / 2,048 /
-// 4,096 / 8,192 keys: 119 / 118 / 119 / 103, as two launches).
+// A request whose rows fill a tile and that takes all of its keys alone has chunks of
+// 8,192 keys when there are units for all SMs (16 requests of 64 rows times 4 heads behind
+// 4,096 keys, 1,024 / 2,048 / 4,096 / 8,192 keys: 119 / 118 / 119 / 103, as two launches).
 constexpr int kPrePartRows = 4096;
 constexpr int kSms = 152;  // counted here, not asked for: a workspace's size is known without a device
+constexpr int kPreLeast = 512;
+__host__ __device__ inline int64_t row_units(int64_t rows, int64_t Hkv, int64_t G, int64_t tile) {
+  const int64_t units = Hkv * ((rows * G + tile - 1) / tile);
+  return units < 1 ? 1 : units;
+}
+// `rows`: of all the requests, or of those that read a prefix together
+__host__ __device__ inline Chunking prefix_cut(int64_t rows, int64_t units) {
+  const int64_t sms = kSms / units < 8 ? 8 : kSms / units, part = rows < 1 ? kPrePartRows : kPrePartRows / rows;
+  const int64_t most = part < sms ? part : sms;
+  return Chunking{units < 32 ? kPreLeast : units < 128 ? 1024 : 2048, most < 1 ? 1 : most > kTreeMaxChunks ? kTreeMaxChunks : (int32_t)most};
+}
+
+// With a plan, a small kernel looks through the groups first: where a request may have
+// rows for a tile of its own (each other having one at least) and a group rows for several tiles, or where the
+// buffers hold many more rows than the requests can have.  It decides from the rows
+// that are there, request by request, so that neither rows behind the last nor a
+// prompt among decodes keeps others from sharing, and it numbers the rows that share,
+// so that only those have partials.  Without one every group of two and more shares.
 struct Cut {
   int n_pre, n_own;  // rows per MMA tile
   Chunking pre, own;
-  bool alone;
-  int64_t pre_chunks, own_chunks, rows_per_seq;
+  int alone_least;
+  bool plan;
+  int64_t pre_chunks, pre_rows, own_chunks, rows_per_seq;
   int64_t rows;  // partial rows in all
 };
 Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
   Cut c;
   c.n_pre = tree_tile_rows(max_group * G, f8);
   c.n_own = tree_tile_rows(max_q * G, f8);
-  c.alone = T * G >= B * c.n_pre;
-  const int64_t units = std::max<int64_t>(1, Hkv * ((T * G + c.n_pre - 1) / c.n_pre));
-  c.own = call_chunking(B, Hkv, max_q * G, f8);
-  c.own.least = c.alone && units >= kSms ? 8192 : std::min(c.own.least, 1024);
-  c.pre.least = units < 32 ? 512 : units < 128 ? 1024 : 2048;
-  c.pre.most = static_cast<int32_t>(std::min<int64_t>(kTreeMaxChunks, std::max<int64_t>(8, kSms / units)));
-  c.pre.most = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(c.pre.most, kPrePartRows / std::max<int64_t>(T, 1))));
+  const int64_t all = std::min(T, B * max_q), units = row_units(all, Hkv, G, c.n_pre);
   auto chunks = [&](const Chunking& k) { return std::max<int64_t>(1, std::min<int64_t>(k.most, (max_ctx + k.least - 1) / k.least)); };
-  c.pre_chunks = c.alone ? 0 : chunks(c.pre);
+  c.pre = prefix_cut(all, units);
+  c.pre_chunks = chunks(c.pre);
+  c.pre_rows = T * c.pre_chunks;
+  c.plan = (std::min(max_q, std::max<int64_t>(1, T - B + 1)) * G >= c.n_pre && max_group * G > c.n_pre) || c.pre_rows > std::max<int64_t>(T, kPrePartRows);
+  if (c.plan) c.pre_rows = std::min<int64_t>(std::max<int64_t>(T, kPrePartRows), T * kTreeMaxChunks);
+  c.own = call_chunking(B, Hkv, max_q * G, f8);
+  c.own.least = std::min(c.own.least, 1024);
+  c.alone_least = units >= kSms ? 8192 : c.own.least;
   const int64_t most = chunks(c.own);
   c.rows_per_seq = most > 1 ? std::min<int64_t>(max_q * most, kTreePartRows) : 0;
   c.own_chunks = most > 1 && T * most <= B * c.rows_per_seq ? most : 0;
-  c.rows = shared_own(T, c.pre_chunks) + (c.own_chunks ? T * c.own_chunks : B * c.rows_per_seq);
+  c.rows = shared_own(T, c.pre_rows) + (c.own_chunks ? T * c.own_chunks : B * c.rows_per_seq);
   return c;
+}
+
+// The plan: which requests read their prefix with their group, where the partials of
+// their rows are, and how prefixes are cut.
+//
+// A request with rows for four tiles reads all of its keys alone.  The others of a
+// group read its prefix together when that takes a fifth fewer tiles than one by one.
+// 16 requests behind 4,096 keys, 4 heads, bf16, tiles of 128 rows, us, together and one
+// by one: 33 rows each 75 / 109, 50 rows 98 / 104, 56 rows 99 / 104, 58 rows 114 / 104, 64
+// rows 121 / 104, 100 rows 175 / 189, 128 rows 206 / 190; e4m3, tiles of 64: 17 rows 71 /
+// 118, 24 to 28 rows 92 / 92, 30 rows 103 / 95.
+// A prompt of 2,048 rows and 32 decodes behind 4,096 keys: all together 537, one by one
+// 356, so 285; e4m3 668, 458 and 391.
+//
+// One CTA, bound by latency: 2 to 3 us of a call (16 requests of 64 rows 102.5 -> 104.7 us,
+// 52 of 1 to 27 rows 44.5 -> 47.4).  A request that takes no part gets -1, which the kernels
+// behind record as they record it without a plan.
+constexpr int kPlanThreads = 1024;
+struct PlanArgs {
+  int32_t* cut;     // [3]
+  int32_t* prefix;  // [B]
+  int32_t* at;      // [B]
+  uint32_t* tiles;  // [B + 1] of the requests before, one by one
+  uint32_t* rows;   // [B + 1] of the requests before
+  int32_t own_least;
+};
+
+// Exclusive sums of two numbers over a block, from `carry` on.  Sums of counts below
+// 2^31 stay there, whatever the lengths are (then v + its number is kSat).
+constexpr uint32_t kSat = 0x7fffffffu;
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSat); }
+__device__ __forceinline__ void warp_sums(uint32_t (&v)[2], int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, v[k], o);
+      if (lane >= o) v[k] = sat_add(v[k], x);
+    }
+  }
+}
+__device__ __forceinline__ void block_sums(uint32_t (&v)[2], uint32_t (&carry)[2], uint32_t (&warps)[32][2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
+  const uint32_t own[2] = {v[0], v[1]};
+  warp_sums(v, lane);
+  __syncthreads();  // the last sums have been read
+  if (lane == 31) {
+    warps[warp][0] = v[0];
+    warps[warp][1] = v[1];
+  }
+  __syncthreads();
+  uint32_t w[2] = {lane < n ? warps[lane][0] : 0u, lane < n ? warps[lane][1] : 0u};
+  warp_sums(w, lane);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t before = __shfl_sync(0xffffffffu, w[k], (warp - 1) & 31), all = __shfl_sync(0xffffffffu, w[k], 31);
+    v[k] = sat_add(sat_add(carry[k], warp > 0 ? before : 0u), v[k]) - own[k];
+    carry[k] = sat_add(carry[k], all);
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TreeParams p, const SharedArgs h, const PlanArgs out) {
+  __shared__ uint32_t warps[32][2];
+  launch_dependents();
+  grid_dep_wait();
+  auto heads_rows = [&](int q) { return (uint32_t)max(min(q, (int)p.T), 0) * (uint32_t)p.G; };  // in range whatever the lengths are
+  auto tiles_of = [&](int q) { return (int)((heads_rows(q) + (1u << h.tile_log2) - 1) >> h.tile_log2); };
+  auto is_long = [&](int q) { return heads_rows(q) >> (h.tile_log2 + 2) != 0; };
+  uint32_t carry[2] = {0, 0};
+  for (int base = 0; base < p.B; base += blockDim.x) {
+    const int s = base + threadIdx.x;
+    uint32_t v[2] = {0, 0};
+    if (s < p.B) {
+      const int q = __ldg(p.cu_q + s + 1) - __ldg(p.cu_q + s);
+      if (!is_long(q)) {
+        v[0] = tiles_of(q);
+        v[1] = max(q, 0);
+      }
+    }
+    block_sums(v, carry, warps);
+    if (s < p.B) {
+      out.tiles[s] = v[0];
+      out.rows[s] = v[1];
+    }
+  }
+  if (threadIdx.x == 0) {
+    out.tiles[p.B] = carry[0];
+    out.rows[p.B] = carry[1];
+  }
+  __syncthreads();
+  uint32_t sums[2] = {0, 0};  // rows that share
+  for (int base = 0; base < p.B; base += blockDim.x) {
+    const int s = base + threadIdx.x;
+    uint32_t v[2] = {0, 0};
+    int prefix = 0, q = 0;
+    if (s < p.B) {
+      int c0, n;
+      Group of;
+      if (shared_request(p, h, s, c0, q, n, of)) {
+        prefix = -1;
+      } else if (of.shares() && !is_long(q)) {
+        const uint32_t alone = __ldcg(out.tiles + of.end) - __ldcg(out.tiles + of.first), rows = __ldcg(out.rows + of.end) - __ldcg(out.rows + of.first);
+        if (5 * (int64_t)tiles_of(static_cast<int>(rows)) <= 4 * (int64_t)alone) prefix = of.prefix;
+      }
+      if (prefix > 0) v[0] = q;
+    }
+    block_sums(v, sums, warps);
+    if (s < p.B) {
+      // (more rows than there are: lengths that are inconsistent elsewhere)
+      out.prefix[s] = prefix > 0 && (int64_t)v[0] + q > p.T ? -1 : prefix;
+      out.at[s] = static_cast<int32_t>(v[0]);
+    }
+  }
+  if (threadIdx.x == 0) {
+    const int all = max(min(__ldg(p.cu_q + p.B), (int)p.T), 0), tile = 1 << h.tile_log2;
+    const int64_t rows = min((int64_t)sums[0], p.T);
+    const Chunking c = prefix_cut(rows, row_units(rows, p.Hkv, p.G, tile));
+    out.cut[0] = c.least;
+    out.cut[1] = c.most;
+    out.cut[2] = row_units(all, p.Hkv, p.G, tile) >= kSms ? 8192 : out.own_least;
+  }
 }
 
 // One warp per (row, query head), as in tree_join_kernel: lane l holds elements l
@@ -93,12 +232,21 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const SharedArgs& h = a.shared;
   const int s = blockIdx.x, lane = threadIdx.x & 31;
   // what does not come from the kernels before is read while they still run
-  int c0, q, n, prefix;
-  const bool bad = shared_request(p, h, s, c0, q, n, prefix) || q == 0;
-  int np = 0, own = 1;
+  int c0, q, n, np = 0, own = 1, at = 0, pre_step = 0;
+  Group of;
+  const bool bad = shared_request(p, h, s, c0, q, n, of) || q == 0;
   if (!bad) {
-    if (prefix > 0) np = (prefix - 1) / tree_chunk(prefix, 1, h.pre) + 1;
-    own = (n - prefix - 1) / tree_chunk(n - prefix, q, h.own) + 1;
+    Chunking cut = h.own;
+    if (of.shares()) {
+      const Chunking pre = prefix_chunking(h);
+      np = (of.prefix - 1) / tree_chunk(of.prefix, 1, pre) + 1;
+      pre_step = prefix_step(h, pre);
+      at = h.at ? __ldg(h.at + s) : c0;
+    } else {
+      of.prefix = 0;
+      if (fills_tile(p, h, q)) cut.least = h.plan ? __ldg(h.plan + 2) : h.alone_least;
+    }
+    own = (n - of.prefix - 1) / tree_chunk(n - of.prefix, q, cut) + 1;
   }
   grid_dep_wait();
   launch_dependents();
@@ -109,8 +257,8 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const int64_t own_first = own_part(p, h, a.rows_per_seq, s, c0, own, own_step);
   for (int64_t r = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.y * 8) {
     const int i = static_cast<int>(r / p.Hq), hq = static_cast<int>(r - (int64_t)i * p.Hq);
-    const int64_t pre_at = (int64_t)(c0 + i) * h.pre_chunks;
-    const int64_t own_at = own == 1 ? shared_single(p.T, h.pre_chunks, c0 + i) : own_first + (int64_t)i * own_step;
+    const int64_t pre_at = (int64_t)(at + i) * pre_step;
+    const int64_t own_at = own == 1 ? shared_single(h.pre_rows, c0 + i) : own_first + (int64_t)i * own_step;
     auto row_of = [&](int c) { return ((c < np ? pre_at + c : own_at + (c - np)) * p.Hq + hq); };
     float v[kAt][E];
     auto load = [&](int b) {
@@ -183,8 +331,10 @@ cudaError_t launch_phase(const TcArgs& a, int N, int64_t most, int num_sms, cuda
 
 }  // namespace
 
-int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8) {
-  return shared_cut(T, B, Hkv, G, max_q, max_group, max_ctx, f8).rows;
+int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8, int64_t* words) {
+  const Cut c = shared_cut(T, B, Hkv, G, max_q, max_group, max_ctx, f8);
+  *words = 1 + (c.plan ? 3 + 4 * B + 2 : 0);
+  return c.rows;
 }
 
 cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8, int out_kind, int64_t max_q, int64_t max_group,
@@ -200,13 +350,33 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   a.part_lse = a.part_o + c.rows * p.Hq * p.D;
   SharedArgs& h = a.shared;
   h.groups = groups;
-  h.alone = c.alone;
+  h.prefix = groups + 2;
+  h.prefix_step = 3;
+  h.tile_log2 = c.n_pre == 16 ? 4 : c.n_pre == 32 ? 5 : c.n_pre == 64 ? 6 : 7;
   h.max_group = static_cast<int32_t>(max_group);
   h.pre_chunks = static_cast<int32_t>(c.pre_chunks);
+  h.pre_rows = c.pre_rows;
   h.own_chunks = static_cast<int32_t>(c.own_chunks);
   h.pre = c.pre;
   h.own = c.own;
+  h.alone_least = c.alone_least;
   h.claims = reinterpret_cast<unsigned int*>(a.part_lse + c.rows * p.Hq);
+  cudaError_t e;
+  if (c.plan) {
+    PlanArgs out;
+    out.cut = reinterpret_cast<int32_t*>(h.claims + 1);
+    out.prefix = out.cut + 3;
+    out.at = out.prefix + p.B;
+    out.tiles = reinterpret_cast<uint32_t*>(out.at + p.B);
+    out.rows = out.tiles + p.B + 1;
+    out.own_least = c.own.least;
+    e = launch_ex(shared_plan_kernel, dim3(1), dim3(std::min(kPlanThreads, (p.B + 31) / 32 * 32)), 0, st, true, p, h, out);
+    if (e != cudaSuccess) return e;
+    h.plan = out.cut;
+    h.prefix = out.prefix;
+    h.prefix_step = 1;
+    h.at = out.at;
+  }
   // the wide kernel masks the products before they are scaled
   const int wide = p.qk_scale_log2 > 0.f ? 128 : 64, n_pre = std::min(c.n_pre, wide), n_own = std::min(c.n_own, wide);
   // One launch of one tile saves a kernel's start; us, two launches and one:
@@ -217,14 +387,13 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   // and none of 28 calls became slower.  At the larger of two tiles it would depend on
   // where the keys are (16 and 32 rows: 18.3 to 14.3, but also 83 to 94).
   const bool both = n_pre == n_own;
-  const int64_t most_pre = std::max<int64_t>(1, c.pre_chunks * p.Hkv * ((p.T * p.G + n_pre - 1) / n_pre + p.B));
+  const int64_t most_pre = std::max<int64_t>(1, (c.plan ? kTreeMaxChunks : c.pre_chunks) * p.Hkv * ((p.T * p.G + n_pre - 1) / n_pre + p.B));
   const int64_t most_own = (int64_t)p.B * kTreeMaxChunks * p.Hkv * ((max_q * p.G + n_own - 1) / n_own);
   auto launch = [&](int phase, int N, int64_t most) {
     h.phase = phase;
     if (p.D == 128) return f8 ? launch_phase<128, true>(a, N, most, num_sms, st) : launch_phase<128, false>(a, N, most, num_sms, st);
     return f8 ? launch_phase<64, true>(a, N, most, num_sms, st) : launch_phase<64, false>(a, N, most, num_sms, st);
   };
-  cudaError_t e;
   if (both) {
     e = launch(kBoth, n_own, most_pre + most_own);
   } else {

@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p, SharedArgs 
     // inconsistent lengths are recorded, those of sequences without a row of their own too
     for (int64_t i = t * blockDim.x + threadIdx.x; i < p.B; i += (int64_t)gridDim.x * blockDim.x) {
       if constexpr (kShared) {
-        int a, e, m, f;
+        int a, e, m;
+        Group f;
         if (shared_request(p, h, static_cast<int>(i), a, e, m, f)) atomicOr(p.err, kErrLengths);
         continue;
       }
@@ -207,7 +208,8 @@ __global__ void __launch_bounds__(128) tree_f32_kernel(TreeParams p, SharedArgs 
     return;
   }
   if constexpr (kShared) {
-    int a, e, m, f;
+    int a, e, m;
+    Group f;
     if (shared_request(p, h, s, a, e, m, f)) return;
   }
   const int ctx = n - q_s;
@@ -274,6 +276,8 @@ cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st) 
 cudaError_t launch_shared_f32(const TreeParams& p, const int32_t* groups, int64_t max_group, int out_kind, cudaStream_t st) {
   SharedArgs h{};
   h.groups = groups;
+  h.prefix = groups + 2;
+  h.prefix_step = 3;
   h.max_group = static_cast<int32_t>(max_group);
   return launch_f32_rows<true>(p, h, out_kind, st);
 }

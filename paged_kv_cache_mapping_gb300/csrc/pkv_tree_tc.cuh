@@ -61,7 +61,8 @@ struct alignas(16) Item {
   int s, h, r0;         // sequence, KV head, first row of the tile
   int t0, q_s, n;       // first packed row, nodes, keys
   int k0, k1;           // keys of the chunk
-  int c, nchunks;       // its index, chunks of the sequence (of a shared prefix: as a negative number)
+  int c, nchunks;       // its index, chunks of the sequence; of a shared prefix: its first partial row, and
+                        // how far a row's partials are from the last one's, as a negative number
   int nt, ctx;          // key tiles (0: no more items); keys before ctx are seen by every row
 };
 
@@ -305,8 +306,8 @@ struct Part {
   bool split;
 };
 // Trees: the chunks of a node side by side, rows_per_seq rows a sequence.
-// Requests that share prefixes: the prefix chunks of packed row t at t *
-// pre_chunks; then one row for each packed row (requests of one chunk of their
+// Requests that share prefixes: the prefix chunks of a row side by side, from where the
+// finder says on; then one row for each packed row (requests of one chunk of their
 // own); then those of requests of several (see own_part()).
 template <bool S>
 __device__ __forceinline__ Part part_of(const TcArgs& a, const Item& it) {
@@ -314,8 +315,8 @@ __device__ __forceinline__ Part part_of(const TcArgs& a, const Item& it) {
     return Part{(int64_t)it.s * a.rows_per_seq + it.c, it.nchunks, it.nchunks > 1};
   } else {
     const SharedArgs& h = a.shared;
-    if (it.nchunks < 0) return Part{(int64_t)it.t0 * h.pre_chunks + it.c, h.pre_chunks, true};  // of a prefix
-    if (it.nchunks == 1) return Part{shared_single(a.p.T, h.pre_chunks, it.t0), 1, it.k0 > 0};
+    if (it.nchunks < 0) return Part{it.c, -it.nchunks, true};  // of a prefix
+    if (it.nchunks == 1) return Part{shared_single(h.pre_rows, it.t0), 1, it.k0 > 0};
     int step;
     const int64_t at = own_part(a.p, h, a.rows_per_seq, it.s, it.t0, it.nchunks, step);
     return Part{at + it.c, step, true};
@@ -532,7 +533,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   auto bar = [&](int i) -> uint32_t { return cta.bar(i); };
   int gb = 0;                        // the group of sequences gb .. gb + 31 held by the lanes
   int c0 = 0, q_s = 0, n = 0, k_at = 0, chunk = 1, nchunks = 0, rts = 0;  // (k_at: a request's first own key)
-  int table = 0;  // of a run of requests: the one whose table has the prefix
+  int table = 0, at_row = 0;  // of a run of requests: the one whose table has the prefix; where its rows' partials are
   // items: this sequence's, prefix in the group, in it; before it.  A sequence has
   // at most Hq max(1024, q_s) / 16 + 64 Hkv of them, 2^27 since T Hq <= 2^30, and so
   // a group's fit 32 bits, whatever the lengths are
@@ -548,6 +549,12 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   gb = -32;
   // with shared prefixes: whether it is at these; the requests' own keys follow them
   bool pre = G_::kShared && a.shared.phase != kOwnKeys;
+  [[maybe_unused]] Chunking cut_pre{};
+  [[maybe_unused]] int alone_least = 0;
+  if constexpr (G_::kShared) {
+    cut_pre = prefix_chunking(a.shared);
+    alone_least = a.shared.plan ? __ldg(a.shared.plan + 2) : a.shared.alone_least;
+  }
   int64_t x = blockIdx.x;
   for (int j = 0;; ++j) {
     // item number x of the call
@@ -568,16 +575,21 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       if constexpr (G_::kShared) {
         bool some = false;
         k_at = 0;
+        Chunking cut = cut_pre;
         if (pre) {
           // the rows of all the run's requests, the prefix's keys; every row sees all of them
           some = shared_run(p, a.shared, gb, lane, c0, q_s, n, table);
+          if (some) at_row = a.shared.at ? __ldg(a.shared.at + s) : c0;
         } else if (s < p.B) {
-          const bool bad = shared_request(p, a.shared, s, c0, q_s, n, k_at);
+          Group of;
+          const bool bad = shared_request(p, a.shared, s, c0, q_s, n, of);
           if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
           some = !bad && q_s > 0;
+          if (of.shares()) k_at = of.prefix;
+          cut = Chunking{k_at == 0 && fills_tile(p, a.shared, q_s) ? alone_least : a.shared.own.least, a.shared.own.most};
         }
         if (some) {
-          chunk = pre ? tree_chunk(n, 1, a.shared.pre) : tree_chunk(n - k_at, q_s, a.shared.own);
+          chunk = tree_chunk(n - k_at, pre ? 1 : q_s, cut);
           nchunks = (n - k_at - 1) / chunk + 1;
           rts = (q_s * G - 1) / N + 1;
           cnt = nchunks * Hkv * rts;
@@ -627,10 +639,11 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
       it.k1 = it.n - it.k0 < len ? it.n : it.k0 + len;
       it.ctx = it.n - it.q_s;
       if constexpr (G_::kShared) {
-        const int t = __shfl_sync(0xffffffffu, table, o);
+        const int t = __shfl_sync(0xffffffffu, table, o), row = __shfl_sync(0xffffffffu, at_row, o);
         if (pre) {
           it.s = t;
-          it.nchunks = -it.nchunks;
+          it.nchunks = -prefix_step(a.shared, cut_pre);
+          it.c -= row * it.nchunks;
           it.ctx = it.n;
         } else {
           ++it.ctx;  // the first new key, too, is seen by every row

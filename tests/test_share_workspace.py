@@ -22,9 +22,9 @@ def test_it_holds_no_more_rows_than_the_batch_can_fill(lib, cdt, B, T, max_q, ma
     prefixes are left in all, and one more."""
     row = 4 * 32 * 129
     n = size(lib, B, T, 8192, max_q, max_group, cdt=cdt)  # 131,072 tokens a table
-    assert n <= (T * chunks + max(4096, T) + T) * row + 8 * B + 512
+    assert n <= (T * chunks + max(4096, T) + T) * row + 32 * B + 512
 
 
 def test_it_counts_requests_where_most_rows_are_padding(lib):  # noqa: F811
     row = 4 * 32 * 129
-    assert size(lib, 64, 1 << 20, 8192, 1, 64) <= (64 * 8 + 2 * (1 << 20)) * row + 1024
+    assert size(lib, 64, 1 << 20, 8192, 1, 64) <= (64 * 8 + 2 * (1 << 20)) * row + 32 * 64 + 512
