@@ -522,7 +522,31 @@ __global__ void __launch_bounds__(Geo<D, N, F8, S>::kThreads, 1)
         // y = score in base 2 less the row's reference, plus kUp
         float y[NC];
         uint32_t hi[NC / 2], lo[NC / 2];  // (lo: bf16)
-        if (F8 && t == 0 && !masked) {
+        if (S && F8 && t == 0 && !masked) {
+          // the first reference: the row's largest score in the tile.  (Not that among some
+          // keys, as below: a row behind a shared prefix has the same bits wherever its group puts it.)
+          uint32_t u[NC];
+          tm_ld(ts, u);
+          wait_ld();
+          float mine = 0.f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float m = redux_max(__uint_as_float(u[c]) * qs[c]);  // NaN is passed over
+            mine = lane == c ? m : mine;
+          }
+          if (lane < NC) xh[quarter * NC + lane] = mine;
+          if (!sync()) { ok = false; break; }
+          bool none = false;
+          if (lane < NC) {  // the same in the group's four warps
+            const float top = fmaxf(fmaxf(xh[lane], xh[NC + lane]), fmaxf(xh[2 * NC + lane], xh[3 * NC + lane]));
+            none = top == -INFINITY;
+            rh[lane] = none ? kUp : kUp - top;
+          }
+          vmask = __ballot_sync(0xffffffffu, none);
+          // every warp has read the scores before the careful path puts others in their place
+          if (vmask != 0 && !sync()) { ok = false; break; }
+          __syncwarp();
+        } else if (F8 && t == 0 && !masked) {
           // the first reference, from the row's largest score among 32 of the
           // tile's keys (each warp takes a quarter of the rows over its own keys)
           uint32_t u[8];
