@@ -661,13 +661,15 @@ PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv
  *                  scratch of one call: nothing in it is kept between calls
  *
  * Each request follows the numbers that it names itself, and neighbours that name
- * the same group read its prefix together: where another request stands between
- * them (one alone, or of another group), those before it and those behind it read the
- * prefix each for themselves.  The tables of a group must agree in the entries of
- * the prefix: it is read through its first request's table, whose own lengths do
- * not matter.  A prefix is whole blocks, and context of every request of the group
- * (prefix <= N_s - q_s).  A request that breaks this, or whose first request's
- * numbers differ from its own, or with more than max_q_len rows in itself or
+ * the same group read its prefix together (where another request stands between
+ * them, one alone or of another group, those before it and those behind it read it
+ * each for themselves), through the table of the group's first request, whose own
+ * lengths do not matter.  That the other tables of a group list the same blocks there
+ * is the caller's to keep and is not looked at: a request that shares has the keys of
+ * the first one's prefix whatever its own table says, one that reads alone (see above)
+ * those of its own.  A prefix is whole blocks, and context of every request of the
+ * group (prefix <= N_s - q_s).  A request whose prefix is not, or whose first
+ * request's numbers differ from its own, or with more than max_q_len rows in itself or
  * max_group_len in its group, or with inconsistent lengths, is recorded (bit 4)
  * and its rows are left as they are; so are rows at or beyond cu_seqlens_q[B].  A
  * key whose block id is out of range is recorded (bit 2) and adds nothing; a row
