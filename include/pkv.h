@@ -630,9 +630,11 @@ PKV_API pkv_status pkv_step_tables(const pkv_tensor* seq_lens, const pkv_tensor*
  * have in common, over the blocks that both have full of context (N_s - q_s
  * tokens); a negative entry is common to nobody.  Request s joins the one before
  * it when c_s * block_size >= min_tokens and 2 c_s >= c_(s-1) and c_(s+1): a
- * group is a run of such requests, its prefix the least c_s of them, so a long
- * prefix is not cut to less than half for one more request.  Requests that
- * share have to be neighbours in the batch.  A request with inconsistent lengths
+ * group is a run of such requests, its prefix the least c_s of them.  So one link
+ * halves the prefix of its neighbours at most, but nothing bounds a chain of them:
+ * requests with 64, 32, 16, 8 and 4 blocks in common, in this order, are one group
+ * with a prefix of 4.  Requests that share have to be neighbours in the batch, those
+ * with most in common next to each other.  A request with inconsistent lengths
  * is recorded (bit 4) and shares nothing.  At most 8,192 requests.
  */
 PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv_tensor* seq_lens,

@@ -273,8 +273,9 @@ cudaError_t launch_step_tables(const StepTablesParams& p, bool slots_i64, cudaSt
 // common[s]: leading entries of the tables of requests s - 1 and s that are the
 // same block, over the blocks that both have full of context.  Request s is linked
 // to the one before it when that is at least min_tokens, and at least half of what
-// either of them shares with its other neighbour: a long prefix is not cut short for
-// one more request.  A group is a run of links, its prefix the least common.
+// either of them shares with its other neighbour.  A group is a run of links, its prefix
+// the least common: a link costs its neighbours half of theirs at most, a chain of
+// links more.
 //
 // A CTA per pair of tables compares 2,048 entries a trip, all loads of a trip in
 // flight, and stops at the first difference; then one CTA finds the runs by a scan.
