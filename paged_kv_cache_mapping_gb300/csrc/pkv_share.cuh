@@ -21,6 +21,7 @@ struct SharedArgs {
   int32_t phase;          // kPrefixes, kOwnKeys or kBoth
   const int32_t* prefix;  // [B], prefix_step apart: tokens of the prefix that a request reads with its group; groups' own, or the plan's
   int32_t prefix_step;
+  FastDiv by_bs;
   int32_t tile_log2;      // rows of a tile over a prefix
   int32_t max_group;      // rows of a group at most
   int32_t pre_chunks;     // chunks of a prefix at most (without a plan)
@@ -59,6 +60,8 @@ struct Group {
   __device__ __forceinline__ bool shares() const { return prefix > 0 && end - first > 1; }
 };
 
+__device__ __forceinline__ bool whole_blocks(const TreeParams& p, const SharedArgs& h, int n) { return quot(n, h.by_bs) * p.bs == n; }
+
 // Request s: packed rows c0 .. c0 + q - 1, n keys, its group.  Returns whether it
 // takes no part: inconsistent lengths, a prefix that is not whole blocks of its
 // context, or a group that its first request does not name in the same words or
@@ -72,7 +75,7 @@ __device__ __forceinline__ bool shared_request(const TreeParams& p, const Shared
   q = c1 - c0;
   if (c0 < 0 || c1 < c0 || (int64_t)c1 > p.T || q > n || (int64_t)n > (int64_t)p.max_blocks * p.bs || q > p.max_nodes) return true;
   if (of.prefix == 0) return false;
-  if (of.prefix < 0 || of.prefix > n - q || of.prefix % p.bs != 0 || g0 < 0 || g0 > s || g1 <= s || g1 > p.B) return true;
+  if (of.prefix < 0 || of.prefix > n - q || !whole_blocks(p, h, of.prefix) || g0 < 0 || g0 > s || g1 <= s || g1 > p.B) return true;
   const int32_t* f = h.groups + 3 * (int64_t)g0;
   const int t0 = __ldg(p.cu_q + g0), t1 = __ldg(p.cu_q + g1);
   of.rows = t1 - t0;
@@ -132,7 +135,7 @@ __device__ __forceinline__ bool shared_run(const TreeParams& p, const SharedArgs
   c0 = __ldg(p.cu_q + min(s, p.B));
   const bool goes_on = head && s > 0 && __ldg(before) == table && __ldg(before + 1) == end && __ldg(m - (s > 0 ? h.prefix_step : 0)) == n;
   head = head && n > 0 && table >= 0 && (table == s || (table < s && !goes_on)) && end > s && end <= p.B && end - table > 1 &&
-         (int64_t)n <= (int64_t)p.max_blocks * p.bs && n % p.bs == 0;
+         (int64_t)n <= (int64_t)p.max_blocks * p.bs && whole_blocks(p, h, n);
   const int t1 = head ? __ldg(p.cu_q + end) : 0;
   // behind the run: the next request that names another group
   const uint32_t other = __ballot_sync(0xffffffffu, !goes_on) & ~((2u << lane) - 1u);

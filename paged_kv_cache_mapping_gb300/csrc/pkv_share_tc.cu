@@ -66,12 +66,14 @@ __host__ __device__ inline Chunking prefix_cut(int64_t rows, int64_t units) {
   return Chunking{units < 32 ? kPreLeast : units < 128 ? 1024 : 2048, most < 1 ? 1 : most > kTreeMaxChunks ? kTreeMaxChunks : (int32_t)most};
 }
 
-// With a plan, a small kernel looks through the groups first: where a request may have
-// rows for a tile of its own (each other having one at least) and a group rows for several tiles, or where the
-// buffers hold many more rows than the requests can have.  It decides from the rows
-// that are there, request by request, so that neither rows behind the last nor a
-// prompt among decodes keeps others from sharing, and it numbers the rows that share,
-// so that only those have partials.  Without one every group of two and more shares.
+// With a plan, a small kernel looks through the groups first: where groups may have
+// rows for several tiles, and a request for kLong, or for one while the buffers hold one
+// for each; or where the buffers hold many more rows than the requests can have.  It
+// decides from the rows that are there, request by request, so that neither rows behind
+// the last nor a prompt among decodes keeps others from sharing, and it numbers the
+// rows that share, so that only those have partials.  Without one every group of two
+// and more shares.
+constexpr int kLong = 4;
 struct Cut {
   int n_pre, n_own;  // rows per MMA tile
   Chunking pre, own;
@@ -89,7 +91,9 @@ Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int6
   c.pre = prefix_cut(all, units);
   c.pre_chunks = chunks(c.pre);
   c.pre_rows = T * c.pre_chunks;
-  c.plan = (std::min(max_q, std::max<int64_t>(1, T - B + 1)) * G >= c.n_pre && max_group * G > c.n_pre) || c.pre_rows > std::max<int64_t>(T, kPrePartRows);
+  const int64_t largest = std::min(max_q, std::max<int64_t>(1, T - B + 1)) * G;  // rows of a request, the others having one at least
+  c.plan = (max_group * G > c.n_pre && (largest >= kLong * c.n_pre || (largest >= c.n_pre && T * G >= B * c.n_pre))) ||
+           c.pre_rows > std::max<int64_t>(T, kPrePartRows);
   if (c.plan) c.pre_rows = std::min<int64_t>(std::max<int64_t>(T, kPrePartRows), T * kTreeMaxChunks);
   c.own = call_chunking(B, Hkv, max_q * G, f8);
   c.own.least = std::min(c.own.least, 1024);
@@ -104,12 +108,14 @@ Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int6
 // The plan: which requests read their prefix with their group, where the partials of
 // their rows are, and how prefixes are cut.
 //
-// A request with rows for four tiles reads all of its keys alone.  The others of a
-// group read its prefix together when that takes a fifth fewer tiles than one by one.
-// 16 requests behind 4,096 keys, 4 heads, bf16, tiles of 128 rows, us, together and one
-// by one: 33 rows each 75 / 109, 50 rows 98 / 104, 56 rows 99 / 104, 58 rows 114 / 104, 64
-// rows 121 / 104, 100 rows 175 / 189, 128 rows 206 / 190; e4m3, tiles of 64: 17 rows 71 /
-// 118, 24 to 28 rows 92 / 92, 30 rows 103 / 95.
+// A request with rows for kLong tiles reads all of its keys alone.  The others of a
+// group read its prefix together when that takes a fifth (e4m3: a third) fewer tiles
+// than one by one.  16 requests behind 4,096 keys, 4 heads, us, together and one by one:
+//   bf16, tiles of 128 rows: 33 rows each 75 / 109, 50 rows 98 / 104, 56 rows 99 / 104, 58
+//   rows 114 / 104, 64 rows 121 / 104, 100 rows 175 / 189, 128 rows 206 / 190, 1 to 61 rows
+//   72 / 93
+//   e4m3, tiles of 64: 17 rows 71 / 118, 20 rows 81 / 92, 24 to 28 rows 92 / 92, 30 rows 103
+//   / 95, 1 to 61 rows 115 / 106
 // A prompt of 2,048 rows and 32 decodes behind 4,096 keys: all together 537, one by one
 // 356, so 285; e4m3 668, 458 and 391.
 //
@@ -123,7 +129,7 @@ struct PlanArgs {
   int32_t* at;      // [B]
   uint32_t* tiles;  // [B + 1] of the requests before, one by one
   uint32_t* rows;   // [B + 1] of the requests before
-  int32_t own_least;
+  int32_t own_least, f8;
 };
 
 // Exclusive sums of two numbers over a block, from `carry` on.  Sums of counts below
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TreePar
   grid_dep_wait();
   auto heads_rows = [&](int q) { return (uint32_t)max(min(q, (int)p.T), 0) * (uint32_t)p.G; };  // in range whatever the lengths are
   auto tiles_of = [&](int q) { return (int)((heads_rows(q) + (1u << h.tile_log2) - 1) >> h.tile_log2); };
-  auto is_long = [&](int q) { return heads_rows(q) >> (h.tile_log2 + 2) != 0; };
+  auto is_long = [&](int q) { return heads_rows(q) >> h.tile_log2 >= kLong; };
   uint32_t carry[2] = {0, 0};
   for (int base = 0; base < p.B; base += blockDim.x) {
     const int s = base + threadIdx.x;
@@ -201,7 +207,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TreePar
         prefix = -1;
       } else if (of.shares() && !is_long(q)) {
         const uint32_t alone = __ldcg(out.tiles + of.end) - __ldcg(out.tiles + of.first), rows = __ldcg(out.rows + of.end) - __ldcg(out.rows + of.first);
-        if (5 * (int64_t)tiles_of(static_cast<int>(rows)) <= 4 * (int64_t)alone) prefix = of.prefix;
+        const int part = out.f8 ? 3 : 5;
+        if (part * (int64_t)tiles_of(static_cast<int>(rows)) <= (part - 1) * (int64_t)alone) prefix = of.prefix;
       }
       if (prefix > 0) v[0] = q;
     }
@@ -350,6 +357,7 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   a.part_lse = a.part_o + c.rows * p.Hq * p.D;
   SharedArgs& h = a.shared;
   h.groups = groups;
+  h.by_bs = a.by_bs;
   h.prefix = groups + 2;
   h.prefix_step = 3;
   h.tile_log2 = c.n_pre == 16 ? 4 : c.n_pre == 32 ? 5 : c.n_pre == 64 ? 6 : 7;
@@ -370,6 +378,7 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
     out.tiles = reinterpret_cast<uint32_t*>(out.at + p.B);
     out.rows = out.tiles + p.B + 1;
     out.own_least = c.own.least;
+    out.f8 = f8;
     e = launch_ex(shared_plan_kernel, dim3(1), dim3(std::min(kPlanThreads, (p.B + 31) / 32 * 32)), 0, st, true, p, h, out);
     if (e != cudaSuccess) return e;
     h.plan = out.cut;

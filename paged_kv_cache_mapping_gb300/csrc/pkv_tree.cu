@@ -276,6 +276,7 @@ cudaError_t launch_tree_f32(const TreeParams& p, int out_kind, cudaStream_t st) 
 cudaError_t launch_shared_f32(const TreeParams& p, const int32_t* groups, int64_t max_group, int out_kind, cudaStream_t st) {
   SharedArgs h{};
   h.groups = groups;
+  h.by_bs = fast_div(static_cast<uint32_t>(p.bs));
   h.prefix = groups + 2;
   h.prefix_step = 3;
   h.max_group = static_cast<int32_t>(max_group);
