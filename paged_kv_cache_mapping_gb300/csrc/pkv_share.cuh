@@ -19,9 +19,9 @@ struct Chunking {
 struct SharedArgs {
   const int32_t* groups;  // [B, 3]: first request, request behind the last, tokens of the prefix
   int32_t phase;          // kPrefixes, kOwnKeys or kBoth
-  const int32_t* prefix;  // [B], prefix_step apart: tokens of the prefix that a request reads with its group; groups' own, or the plan's
+  const int32_t* prefix;  // [B], prefix_step apart: tokens that a request reads with its group, as groups or the plan has them
   int32_t prefix_step;
-  FastDiv by_bs;
+  FastDiv by_bs;          // tokens of a block
   int32_t tile_log2;      // rows of a tile over a prefix
   int32_t max_group;      // rows of a group at most
   int32_t pre_chunks;     // chunks of a prefix at most (without a plan)
@@ -38,9 +38,9 @@ struct SharedArgs {
 
 // Partial rows of the workspace: those of prefixes, so many for each row that reads
 // one with others; one for each packed row; then those of own keys in several chunks:
-// own_chunks for each packed row, or rows_per_seq for each request, whichever is less in all.  (A bound on a request's
-// rows says little of a batch with one prompt among decodes, and the number of packed
-// rows little where most of them are padding.)
+// own_chunks for each packed row, or rows_per_seq for each request, whichever is less
+// in all.  (A bound on a request's rows says little of a batch with one prompt among
+// decodes, and the number of packed rows little where most of them are padding.)
 __host__ __device__ inline int64_t shared_single(int64_t pre_rows, int64_t t) { return pre_rows + t; }
 __host__ __device__ inline int64_t shared_own(int64_t T, int64_t pre_rows) { return pre_rows + T; }
 // of request s, packed rows from c0 on, nc chunks: its first partial row, and how far a row's are from the last one's
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool shared_request(const TreeParams& p, const Shared
   return __ldg(f) != g0 || __ldg(f + 1) != g1 || __ldg(f + 2) != of.prefix || t0 < 0 || t0 > c0 || t1 < c1 || (int64_t)t1 > p.T ||
          of.rows > h.max_group;
 }
-// rows of all heads, as tiles over a prefix count them
+// whether q rows, times the heads, fill a tile over a prefix
 __device__ __forceinline__ bool fills_tile(const TreeParams& p, const SharedArgs& h, int q) { return (q * p.G) >> h.tile_log2 != 0; }
 
 // Prefixes are read for runs of neighbours that name the same group in the same
@@ -93,8 +93,8 @@ __device__ __forceinline__ bool fills_tile(const TreeParams& p, const SharedArgs
 // only one that a request is in.  What shared_request() takes for a request of the run
 // has passed all of this.
 //
-// (Groups taken at their word: 0.1 to 0.4 us less a call.  What is rare stands apart: a
-// call's first item waits until this code is fetched.)
+// (With groups taken at their word small calls took 0.1 to 0.3 us less.  What is rare
+// stands apart, and no division stands here: a call's first item waits for this.)
 static __device__ __noinline__ int run_end(const SharedArgs& h, int s, int lane, int first, int end, int prefix) {
   for (; s < end; s += 128) {
     uint32_t other[4];

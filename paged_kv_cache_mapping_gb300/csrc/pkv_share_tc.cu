@@ -15,17 +15,21 @@
 // Three launches: the prefixes, the own keys beside them (their CTAs take the SMs as
 // the prefixes' leave them, see begin_phase()), and a join.  Where both take tiles of
 // one size, the first two are one launch of which the prefixes are the first items.
+// Calls with prompts, or in buffers of many more rows than they have, have a fourth in
+// front (see Cut).
 //
-// Bound: the memory on bf16 caches, once a kernel runs (its start takes about 5 us, of
-// which there are mostly two); on e4m3 caches the softmax of the prefixes' 64-row
-// tiles, and for short requests what an item costs besides its tiles (3 us, e4m3 4, of
-// which a tile or two are hidden).  Measured, whole calls, 8 KV heads of 4 query heads, D 128,
-// and pkv_attention on the same batch: 64 requests of 512 to 2,048 keys behind 2,048,
-// bf16, 70 us (5.0 TB/s of the 347 MB that have to be read; 105); 64 in groups of 2 to
-// 12 behind 1,024 to 8,192, bf16, 61 us (4.4 TB/s of 268 MB; 128); 16 behind 65,536,
-// e4m3, 70 us (2.9 TB/s of 205 MB; 418); 256 of 64 to 1,024 in groups of 16 behind 512
-// to 2,048, e4m3, 116 us (2.8 TB/s of 329 MB; 202); 4 behind 1,024, bf16, 11 us (28);
-// nothing shared, 64 of 512 to 4,096, bf16, 92 us (104).
+// Bound: the memory on bf16 caches where requests have many keys of their own, once a kernel
+// runs (its start takes about 5 us, of which there are mostly two); on e4m3 caches the
+// chain that the softmax warps of a 64-row tile go through together (load, scores, widening, vote, P: 0.44
+// warps issued per scheduler and 45 % of the memory's rate behind 65,536 keys), and for short
+// requests what an item costs besides its tiles (3 us, e4m3 4, of which a tile or two are
+// hidden).  Measured, whole calls, 8 KV heads of 4 query heads, D 128, and pkv_attention
+// in the same loop on the same batch: 64 requests of 512 to 2,048 keys behind 2,048, bf16, 71 us
+// (4.9 TB/s of the 347 MB that have to be read; 105); 64 in groups of 2 to 12 behind
+// 1,024 to 8,192, bf16, 61 us (4.4 TB/s of 268 MB; 128); 16 behind 65,536, e4m3, 68 us
+// (3.0 TB/s of 205 MB; 418); 256 of 64 to 1,024 in groups of 16 behind 512 to 2,048, e4m3,
+// 112 us (2.9 TB/s of 329 MB; 202); 4 behind 1,024, bf16, 11 us (28); nothing shared, 64
+// of 512 to 4,096, bf16, 101 us (111).
 #include "pkv_tree_narrow.cuh"
 
 namespace pkv {

@@ -53,8 +53,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // One cluster of up to eight CTAs: each scans all the lengths, and they share the
 // rows and blocks.  Bound by latency: lengths, scan, list or table entry, store: 2.4
 // us for 64 decodes, 3.9 for 608 rows and 814 blocks of 37 requests, 10.6 for 33,222
-// rows of 256.  Several independent CTAs would need a launch of their own for the
-// count.
+// rows of 256.  The cluster is for a count in its old place; where that has a place of
+// its own nothing has to be ordered, and independent CTAs on all SMs could share the rows:
+// not built.
 constexpr int kTableThreads = 1024;
 
 template <typename SlotT, int V>
