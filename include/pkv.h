@@ -673,7 +673,9 @@ PKV_API pkv_status pkv_shared_prefixes(const pkv_tensor* cu_seqlens_q, const pkv
  * group (prefix <= N_s - q_s).  A request whose prefix is not, or whose first
  * request's numbers differ from its own, or with more than max_q_len rows in itself or
  * max_group_len in its group, or with inconsistent lengths, is recorded (bit 4)
- * and its rows are left as they are; so are rows at or beyond cu_seqlens_q[B].  A
+ * and its rows are left as they are; so are rows at or beyond cu_seqlens_q[B].  (Where
+ * cu_seqlens_q does not ascend, the rows of other requests of that group are undefined
+ * too.)  A
  * key whose block id is out of range is recorded (bit 2) and adds nothing; a row
  * that sees no key gets zeros.
  *

@@ -6,6 +6,7 @@ import torch
 import paged_kv_cache_mapping_gb300 as pkv
 from tests.share_ref import SharedBatch
 from tests.test_gpu_shared import Dev, close
+from tests.test_gpu_shared_sharing import padded
 
 pytestmark = pytest.mark.gpu
 
@@ -30,6 +31,20 @@ def test_groups_that_overlap(name, new, kv):
         d.run(*bounds)
         assert pkv.pkv_device_errors() == 0
         close(b, d.out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1] * 8, [1, 3, 2, 1, 300, 1, 2, 1]])
+@pytest.mark.parametrize("name", list(GROUPS))
+def test_groups_that_overlap_in_buffers_with_many_more_rows(name, new, kv):
+    b = SharedBatch([(8, 128)], [20 * s for s in range(8)], new, 8, 2, 64, 16, kv, seed=73)
+    d = Dev(b)
+    d.groups.copy_(torch.tensor(GROUPS[name], dtype=torch.int32))
+    out = padded(d, 3000)
+    d.run(0, 0)
+    assert pkv.pkv_device_errors() == 0
+    close(b, out[:b.T])
+    assert (out[b.T:] == 7.0).all()
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
