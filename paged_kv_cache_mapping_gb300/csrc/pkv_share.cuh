@@ -30,8 +30,9 @@ struct SharedArgs {
   Chunking pre, own;      // how prefixes and own keys are cut (pre: without a plan)
   int32_t alone_least;    // own.least of requests that fill tiles and read all of their keys (without a plan)
   unsigned int* claims;   // items of the own keys that are taken (see next_item())
-  // What shared_plan_kernel wrote, or NULL: {pre.least, pre.most, alone_least}, and [B] where the
-  // partial rows of a request's prefix begin, in rows (without a plan: at its packed rows)
+  // What shared_plan_kernel wrote, or NULL: {pre.least, pre.most}, and [B]: where the partial
+  // rows of a request's prefix begin, in rows (without a plan: at its packed rows), or,
+  // of one that reads all of its keys alone, its own.least
   const int32_t* plan;
   const int32_t* at;
 };
@@ -84,6 +85,10 @@ __device__ __forceinline__ bool shared_request(const TreeParams& p, const Shared
 }
 // whether q rows, times the heads, fill a tile over a prefix
 __device__ __forceinline__ bool fills_tile(const TreeParams& p, const SharedArgs& h, int q) { return (q * p.G) >> h.tile_log2 != 0; }
+// own.least of request s, which has q rows and reads all of its keys alone
+__device__ __forceinline__ int own_least(const TreeParams& p, const SharedArgs& h, int s, int q) {
+  return h.plan ? __ldg(h.at + s) : fills_tile(p, h, q) ? h.alone_least : h.own.least;
+}
 
 // Prefixes are read for runs of neighbours that name the same group in the same
 // words, found by a warp for 32 requests (s = from + lane) at a time: whether request s

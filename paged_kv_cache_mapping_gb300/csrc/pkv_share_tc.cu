@@ -128,9 +128,9 @@ Cut shared_cut(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int6
 // behind record as they record it without a plan.
 constexpr int kPlanThreads = 1024;
 struct PlanArgs {
-  int32_t* cut;     // [3]
+  int32_t* cut;     // [2]
   int32_t* prefix;  // [B]
-  int32_t* at;      // [B]
+  int32_t* at;      // [B] (see SharedArgs)
   uint32_t* tiles;  // [B + 1] of the requests before, one by one
   uint32_t* rows;   // [B + 1] of the requests before
   int32_t own_least, f8;
@@ -199,17 +199,20 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TreePar
     out.rows[p.B] = carry[1];
   }
   __syncthreads();
+  const uint32_t all = max(min(__ldg(p.cu_q + p.B), (int)p.T), 0);  // rows there are
+  const int alone_least = (int64_t)tiles_of(static_cast<int>(all)) * p.Hkv >= kSms ? 8192 : out.own_least;
   uint32_t sums[2] = {0, 0};  // rows that share
   for (int base = 0; base < p.B; base += blockDim.x) {
     const int s = base + threadIdx.x;
     uint32_t v[2] = {0, 0};
-    int prefix = 0, q = 0;
+    int prefix = 0, q = 0, least = out.own_least;
     if (s < p.B) {
       int c0, n;
       Group of;
-      if (shared_request(p, h, s, c0, q, n, of)) {
-        prefix = -1;
-      } else if (of.shares() && !is_long(q)) {
+      const bool bad = shared_request(p, h, s, c0, q, n, of);
+      if (bad) prefix = -1;
+      if (!bad && fills_tile(p, h, q)) least = alone_least;
+      if (!bad && of.shares() && !is_long(q)) {
         const uint32_t alone = __ldcg(out.tiles + of.end) - __ldcg(out.tiles + of.first), rows = __ldcg(out.rows + of.end) - __ldcg(out.rows + of.first);
         const int part = out.f8 ? 3 : 5;
         if (part * (int64_t)tiles_of(static_cast<int>(rows)) <= (part - 1) * (int64_t)alone) prefix = of.prefix;
@@ -220,16 +223,14 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TreePar
     if (s < p.B) {
       // (more rows than there are: lengths that are inconsistent elsewhere)
       out.prefix[s] = prefix > 0 && (int64_t)v[0] + q > p.T ? -1 : prefix;
-      out.at[s] = static_cast<int32_t>(v[0]);
+      out.at[s] = prefix > 0 ? static_cast<int32_t>(v[0]) : least;
     }
   }
   if (threadIdx.x == 0) {
-    const int all = max(min(__ldg(p.cu_q + p.B), (int)p.T), 0), tile = 1 << h.tile_log2;
     const int64_t rows = min((int64_t)sums[0], p.T);
-    const Chunking c = prefix_cut(rows, row_units(rows, p.Hkv, p.G, tile));
+    const Chunking c = prefix_cut(rows, max((int64_t)1, (int64_t)tiles_of(static_cast<int>(rows)) * p.Hkv));
     out.cut[0] = c.least;
     out.cut[1] = c.most;
-    out.cut[2] = row_units(all, p.Hkv, p.G, tile) >= kSms ? 8192 : out.own_least;
   }
 }
 
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
       at = h.at ? __ldg(h.at + s) : c0;
     } else {
       of.prefix = 0;
-      if (fills_tile(p, h, q)) cut.least = h.plan ? __ldg(h.plan + 2) : h.alone_least;
+      cut.least = own_least(p, h, s, q);
     }
     own = (n - of.prefix - 1) / tree_chunk(n - of.prefix, q, cut) + 1;
   }
@@ -344,7 +345,7 @@ cudaError_t launch_phase(const TcArgs& a, int N, int64_t most, int num_sms, cuda
 
 int64_t shared_rows(int64_t T, int64_t B, int64_t Hkv, int64_t G, int64_t max_q, int64_t max_group, int64_t max_ctx, bool f8, int64_t* words) {
   const Cut c = shared_cut(T, B, Hkv, G, max_q, max_group, max_ctx, f8);
-  *words = 1 + (c.plan ? 3 + 4 * B + 2 : 0);
+  *words = 1 + (c.plan ? 2 + 4 * B + 2 : 0);
   return c.rows;
 }
 
@@ -377,7 +378,7 @@ cudaError_t launch_shared_tc(const TreeParams& p, const int32_t* groups, bool f8
   if (c.plan) {
     PlanArgs out;
     out.cut = reinterpret_cast<int32_t*>(h.claims + 1);
-    out.prefix = out.cut + 3;
+    out.prefix = out.cut + 2;
     out.at = out.prefix + p.B;
     out.tiles = reinterpret_cast<uint32_t*>(out.at + p.B);
     out.rows = out.tiles + p.B + 1;

@@ -550,11 +550,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
   // with shared prefixes: whether it is at these; the requests' own keys follow them
   bool pre = G_::kShared && a.shared.phase != kOwnKeys;
   [[maybe_unused]] Chunking cut_pre{};
-  [[maybe_unused]] int alone_least = 0;
-  if constexpr (G_::kShared) {
-    cut_pre = prefix_chunking(a.shared);
-    alone_least = a.shared.plan ? __ldg(a.shared.plan + 2) : a.shared.alone_least;
-  }
+  if constexpr (G_::kShared) cut_pre = prefix_chunking(a.shared);
   int64_t x = blockIdx.x;
   for (int j = 0;; ++j) {
     // item number x of the call
@@ -586,7 +582,7 @@ __device__ __forceinline__ void find_items(const TcArgs& a, const Cta& cta, uint
           if (bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
           some = !bad && q_s > 0;
           if (of.shares()) k_at = of.prefix;
-          cut = Chunking{k_at == 0 && fills_tile(p, a.shared, q_s) ? alone_least : a.shared.own.least, a.shared.own.most};
+          cut = Chunking{k_at > 0 ? a.shared.own.least : own_least(p, a.shared, s, q_s), a.shared.own.most};
         }
         if (some) {
           chunk = tree_chunk(n - k_at, pre ? 1 : q_s, cut);
